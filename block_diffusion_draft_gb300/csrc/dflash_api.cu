@@ -1210,6 +1210,388 @@ int dflash_packed_attn_core_backward(dflash_attn* a, int batch, int seq, int n_b
   return DFLASH_OK;
 }
 
+namespace {
+
+// Work on a handle's memory is enqueued on the current device: it has to be
+// the handle's.
+int check_device(int device) {
+  int cur = -1;
+  DF_CUDA(cudaGetDevice(&cur), "current device");
+  if (cur != device)
+    return fail(DFLASH_ERR_ARG, "the current device is %d, the handle's is %d", cur, device);
+  return DFLASH_OK;
+}
+
+// Host counts of an append or read as the kernels take them; `total` gets
+// their sum.
+int q8_rows(const dflash_q8_cache* c, const int32_t* host_first, const int32_t* host_n, Q8Rows& t,
+            long long* total) {
+  long long sum = 0;
+  t.n = c->batch;
+  t.off[0] = 0;
+  for (int b = 0; b < c->batch; ++b) {
+    if (host_n[b] < 0) return fail(DFLASH_ERR_ARG, "rows of sequence %d < 0", b);
+    sum += host_n[b];
+    if (sum > (1LL << 30)) return fail(DFLASH_ERR_SHAPE, "too many rows");
+    t.off[b + 1] = (int)sum;
+    t.first[b] = host_first[b];
+  }
+  *total = sum;
+  return DFLASH_OK;
+}
+
+// Query tiles of an attention call over an 8-bit cache: as few as hold the
+// block's rows, of near-equal size.
+void q8_tiles(int groups, int q_len, int* tokens, int* tiles) {
+  const int most = 128 / groups;
+  *tiles = (q_len + most - 1) / most;
+  *tokens = (q_len + *tiles - 1) / *tiles;
+}
+
+// Attention of a block over the cached rows (lengths `len`); q and its
+// strides, scale, out and lse are set in `a`.
+int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>& len, int q_len,
+                     Q8AttnArgs& a, cudaStream_t s) {
+  a.st = c->st;
+  a.batch = c->batch;
+  a.groups = at->g;
+  a.q_len = q_len;
+  q8_tiles(at->g, q_len, &a.tile_tokens, &a.n_q_tiles);
+  a.window = at->cfg.sliding_window;
+  a.causal = at->cfg.causal != 0;
+  a.part_o = c->part_o;
+  a.part_ml = c->part_ml;
+  a.err = at->err;
+  Q8Plan p;
+  for (int b = 0; b < c->batch; ++b) {
+    p.len[b] = len[b];
+    p.lo[b] = a.window > 0 ? (int)std::max<long long>(
+                                 0, (long long)len[b] - q_len - a.window + 1)
+                           : 0;
+  }
+  plan_q8_attention(p, c->batch, c->nkv, a.n_q_tiles, c->num_sms);
+  TraceScope tr(at, DFLASH_K_ATTN, s);
+  DF_CUDA(launch_q8_attention(c->fmt, a, p, s), "8-bit cache attention launch");
+  return DFLASH_OK;
+}
+
+int check_q8_pair(const dflash_attn* a, const dflash_q8_cache* c, int batch, int q_len) {
+  if (a == nullptr) return fail(DFLASH_ERR_ARG, "null layer handle");
+  if (c == nullptr) return fail(DFLASH_ERR_ARG, "null cache");
+  if (batch <= 0 || q_len <= 0) return fail(DFLASH_ERR_ARG, "batch and q_len must be positive");
+  if (a->dt != DFLASH_BF16) return fail(DFLASH_ERR_UNSUPPORTED, "8-bit caches need a bf16 layer");
+  if (batch != c->batch)
+    return fail(DFLASH_ERR_SHAPE, "batch %d differs from the cache batch %d", batch, c->batch);
+  if (c->nkv != a->nkv || c->d != a->d || c->device != a->device)
+    return fail(DFLASH_ERR_SHAPE, "cache geometry does not match the layer");
+  if (a->g > 128) return fail(DFLASH_ERR_UNSUPPORTED, "more than 128 query heads per KV head");
+  if ((long long)batch * q_len > (1LL << 30) / a->nq)
+    return fail(DFLASH_ERR_SHAPE, "too many query rows");
+  return check_device(a->device);
+}
+
+}  // namespace
+
+int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, int format,
+                           dflash_q8_cache** out) {
+  if (out == nullptr) return fail(DFLASH_ERR_ARG, "out is null");
+  *out = nullptr;
+  if (int r = check_attn(a)) return r;
+  if (a->dt != DFLASH_BF16) return fail(DFLASH_ERR_UNSUPPORTED, "8-bit caches need a bf16 layer");
+  if (batch <= 0 || capacity_rows <= 0)
+    return fail(DFLASH_ERR_ARG, "batch and capacity_rows must be positive");
+  if (batch > kMaxBatch) return fail(DFLASH_ERR_SHAPE, "batch above %d", kMaxBatch);
+  if (capacity_rows > (1 << 30)) return fail(DFLASH_ERR_SHAPE, "capacity_rows above 2^30");
+  if (format != DFLASH_Q8_E4M3 && format != DFLASH_Q8_INT8)
+    return fail(DFLASH_ERR_ARG, "format must be DFLASH_Q8_E4M3 or DFLASH_Q8_INT8");
+  if (int r = check_device(a->device)) return r;
+  dflash_q8_cache* c = nullptr;
+  try {
+    c = new dflash_q8_cache();
+    c->len.assign(batch, 0);
+  } catch (...) {
+    delete c;
+    return fail(DFLASH_ERR_MEMORY, "host allocation failed");
+  }
+  c->batch = batch;
+  c->cap = capacity_rows;
+  c->rows = (capacity_rows + 127) / 128 * 128;
+  c->nkv = a->nkv;
+  c->d = a->d;
+  c->fmt = format;
+  c->device = a->device;
+  c->num_sms = a->num_sms;
+  const size_t rows = (size_t)batch * a->nkv * c->rows;
+  const size_t codes = rows * 128, scales = rows * 4, slots = q8_attention_slots(c->num_sms);
+  cudaError_t e = cudaMalloc(&c->data, 2 * (codes + scales));
+  if (e == cudaSuccess) e = cudaMalloc(&c->part_o, slots * 128 * 128 * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->part_ml, slots * 256 * sizeof(float));
+  // zeroed: rows past a sequence's end are read with its last tile (and
+  // decoded to zero); finished before any other stream can use the cache
+  if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    dflash_q8_cache_destroy(c);
+    return cuda_fail(e, "8-bit cache allocation");
+  }
+  uint8_t* p = static_cast<uint8_t*>(c->data);
+  c->st.k = p;
+  c->st.v = p + codes;
+  c->st.ks = p + 2 * codes;
+  c->st.vs = p + 2 * codes + scales;
+  c->st.n_kv = c->nkv;
+  c->st.cap = c->rows;
+  *out = c;
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_destroy(dflash_q8_cache* c) {
+  if (c == nullptr) return DFLASH_OK;
+  cudaDeviceSynchronize();
+  cudaFree(c->data);
+  cudaFree(c->part_o);
+  cudaFree(c->part_ml);
+  c->stage_k.release();
+  c->stage_v.release();
+  delete c;
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_lengths(const dflash_q8_cache* c, int32_t* host_len) {
+  if (c == nullptr || host_len == nullptr) return fail(DFLASH_ERR_ARG, "null argument");
+  for (int b = 0; b < c->batch; ++b) host_len[b] = c->len[b];
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_crop(dflash_q8_cache* c, const int32_t* host_keep) {
+  if (c == nullptr || host_keep == nullptr) return fail(DFLASH_ERR_ARG, "null argument");
+  for (int b = 0; b < c->batch; ++b)
+    if (host_keep[b] < 0 || host_keep[b] > c->len[b])
+      return fail(DFLASH_ERR_RANGE, "crop(%d) of sequence %d outside [0, %d]", host_keep[b],
+                  b, c->len[b]);
+  for (int b = 0; b < c->batch; ++b) c->len[b] = host_keep[b];
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_data(const dflash_q8_cache* c, void** k_codes, void** v_codes,
+                         void** k_scales, void** v_scales, int32_t* batch, int32_t* n_kv_heads,
+                         int32_t* stored_rows, int32_t* head_dim) {
+  if (c == nullptr) return fail(DFLASH_ERR_ARG, "null cache");
+  if (k_codes) *k_codes = c->st.k;
+  if (v_codes) *v_codes = c->st.v;
+  if (k_scales) *k_scales = c->st.ks;
+  if (v_scales) *v_scales = c->st.vs;
+  if (batch) *batch = c->batch;
+  if (n_kv_heads) *n_kv_heads = c->nkv;
+  if (stored_rows) *stored_rows = c->rows;
+  if (head_dim) *head_dim = c->d;
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_reserve(dflash_q8_cache* c, int max_new_rows) {
+  if (c == nullptr) return fail(DFLASH_ERR_ARG, "null cache");
+  if (max_new_rows <= 0 || max_new_rows > c->cap)
+    return fail(DFLASH_ERR_ARG, "max_new_rows must be in [1, %d]", c->cap);
+  if (int r = check_device(c->device)) return r;
+  const size_t bytes = (size_t)c->batch * c->nkv * max_new_rows * c->d * 2;
+  DF_CUDA(c->stage_k.ensure(bytes), "scratch allocation");
+  DF_CUDA(c->stage_v.ensure(bytes), "scratch allocation");
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_append(dflash_q8_cache* c, const void* k, const void* v,
+                           int64_t k_row_stride, int64_t v_row_stride, const int32_t* host_n,
+                           dflash_stream stream) {
+  if (c == nullptr || host_n == nullptr) return fail(DFLASH_ERR_ARG, "null argument");
+  Q8Rows t;
+  long long total = 0;
+  if (int r = q8_rows(c, c->len.data(), host_n, t, &total)) return r;
+  for (int b = 0; b < c->batch; ++b)
+    if ((long long)c->len[b] + host_n[b] > c->cap)
+      return fail(DFLASH_ERR_CAPACITY, "sequence %d: %d cached + %d rows exceed capacity %d", b,
+                  c->len[b], host_n[b], c->cap);
+  if (total == 0) return DFLASH_OK;
+  if (k == nullptr || v == nullptr) return fail(DFLASH_ERR_ARG, "null tensor");
+  const int64_t width = (int64_t)c->nkv * c->d;
+  if (k_row_stride < width || v_row_stride < width)
+    return fail(DFLASH_ERR_SHAPE, "row strides must be at least %lld elements", (long long)width);
+  if (!aligned16(k) || !aligned16(v) || k_row_stride % 8 != 0 || v_row_stride % 8 != 0)
+    return fail(DFLASH_ERR_ARG, "rows must start on 16-byte boundaries");
+  if (int r = check_device(c->device)) return r;
+  Q8Source src{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), 0, c->d,
+               k_row_stride, v_row_stride, 1};
+  DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, static_cast<cudaStream_t>(stream)),
+          "8-bit cache append launch");
+  for (int b = 0; b < c->batch; ++b) c->len[b] += host_n[b];
+  return DFLASH_OK;
+}
+
+int dflash_q8_cache_read(const dflash_q8_cache* c, const int32_t* host_first,
+                         const int32_t* host_n, void* k_dst, void* v_dst, dflash_stream stream) {
+  if (c == nullptr || host_first == nullptr || host_n == nullptr)
+    return fail(DFLASH_ERR_ARG, "null argument");
+  Q8Rows t;
+  long long total = 0;
+  if (int r = q8_rows(c, host_first, host_n, t, &total)) return r;
+  for (int b = 0; b < c->batch; ++b)
+    if (host_first[b] < 0 || (long long)host_first[b] + host_n[b] > c->len[b])
+      return fail(DFLASH_ERR_RANGE, "rows [%d, %lld) of sequence %d outside [0, %d)",
+                  host_first[b], (long long)host_first[b] + host_n[b], b, c->len[b]);
+  if (total == 0) return DFLASH_OK;
+  if (k_dst == nullptr || v_dst == nullptr) return fail(DFLASH_ERR_ARG, "null tensor");
+  if (!aligned16(k_dst) || !aligned16(v_dst))
+    return fail(DFLASH_ERR_ARG, "bf16 tensors must be 16-byte aligned");
+  if (int r = check_device(c->device)) return r;
+  DF_CUDA(launch_q8_read(c->fmt, c->st, t, k_dst, v_dst, static_cast<cudaStream_t>(stream)),
+          "8-bit cache read launch");
+  return DFLASH_OK;
+}
+
+int dflash_q8_attn_core(dflash_attn* a, dflash_q8_cache* c, int batch, int q_len, const void* q,
+                        void* out, float* lse, dflash_stream stream) {
+  if (int r = check_q8_pair(a, c, batch, q_len)) return r;
+  if (q == nullptr || out == nullptr) return fail(DFLASH_ERR_ARG, "null tensor");
+  if (!aligned16(q) || !aligned16(out))
+    return fail(DFLASH_ERR_ARG, "bf16 tensors must be 16-byte aligned");
+  Q8AttnArgs qa{};
+  qa.q = static_cast<const uint16_t*>(q);
+  qa.q_seq = (long long)q_len * a->nq * a->d;
+  qa.q_tok = (long long)a->nq * a->d;
+  qa.q_head = (long long)a->g * a->d;
+  qa.q_group = a->d;
+  qa.scale = (float)(1.0 / std::sqrt((double)a->d) * 1.4426950408889634);
+  qa.out = static_cast<uint16_t*>(out);
+  qa.lse = lse;
+  try {
+    return run_q8_attention(a, c, c->len, q_len, qa, static_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return fail(DFLASH_ERR_MEMORY, "host allocation failed");
+  }
+}
+
+int dflash_attn_forward_q8(dflash_attn* a, dflash_q8_cache* c, int batch, int q_len,
+                           const void* noise, const void* target_hidden,
+                           const int32_t* host_n_ctx, const int32_t* positions, void* out,
+                           dflash_stream stream) {
+  if (int r = check_q8_pair(a, c, batch, q_len)) return r;
+  if (noise == nullptr || host_n_ctx == nullptr || positions == nullptr || out == nullptr)
+    return fail(DFLASH_ERR_ARG, "null tensor");
+  long long total_ctx = 0;
+  int most = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (host_n_ctx[b] < 0) return fail(DFLASH_ERR_ARG, "n_ctx[%d] < 0", b);
+    total_ctx += host_n_ctx[b];
+    if ((long long)c->len[b] + host_n_ctx[b] + q_len > c->cap)
+      return fail(DFLASH_ERR_CAPACITY, "sequence %d: %d cached + %d + %d rows exceed capacity %d",
+                  b, c->len[b], host_n_ctx[b], q_len, c->cap);
+    most = std::max(most, host_n_ctx[b] + q_len);
+  }
+  if (total_ctx > 0 && target_hidden == nullptr)
+    return fail(DFLASH_ERR_ARG, "target_hidden is null but n_ctx is not all zero");
+  const long long rows_noise = (long long)batch * q_len;
+  if (rows_noise + total_ctx > (1LL << 30)) return fail(DFLASH_ERR_SHAPE, "too many rows");
+  if (!aligned16(noise) || !aligned16(out) || (total_ctx > 0 && !aligned16(target_hidden)))
+    return fail(DFLASH_ERR_ARG, "bf16 tensors must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t qd = (size_t)a->nq * a->d;
+  if (int r = dflash_q8_cache_reserve(c, most)) return r;
+  DF_CUDA(a->qbuf.ensure(rows_noise * qd * 2), "scratch allocation");
+  DF_CUDA(a->attn_out.ensure(rows_noise * qd * 2), "scratch allocation");
+  try {
+    // the new rows' K and V as bf16, [batch][n_kv][most][d] from row 0
+    SeqTable st;
+    Q8Rows t;
+    std::vector<int> len(batch);
+    st.n = batch;
+    st.q_len = q_len;
+    st.ctx_off[0] = 0;
+    t.n = batch;
+    t.off[0] = 0;
+    for (int b = 0; b < batch; ++b) {
+      st.ctx_off[b + 1] = st.ctx_off[b] + host_n_ctx[b];
+      st.cache_len[b] = 0;
+      t.off[b + 1] = t.off[b] + host_n_ctx[b] + q_len;
+      t.first[b] = c->len[b];
+      len[b] = c->len[b] + host_n_ctx[b] + q_len;
+    }
+    QkvOut o = make_qkv_out(a, positions, a->qbuf.p, c->stage_k.p, c->stage_v.p, most, q_len);
+    o.err = a->err;
+    if (int r = run_qkv(a, noise, (int)rows_noise, target_hidden, (int)total_ctx, o, st, s))
+      return r;
+    Q8Source src{static_cast<const uint16_t*>(c->stage_k.p),
+                 static_cast<const uint16_t*>(c->stage_v.p),
+                 (long long)c->nkv * most * c->d, (long long)most * c->d, c->d, c->d, 0};
+    {
+      TraceScope tr(a, DFLASH_K_MISC, s);
+      DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, s), "8-bit cache append launch");
+    }
+    // Q as the projection leaves it: [batch][n_kv][groups][q_len][d], scaled
+    Q8AttnArgs qa{};
+    qa.q = static_cast<const uint16_t*>(a->qbuf.p);
+    qa.q_seq = (long long)q_len * a->nq * a->d;
+    qa.q_head = (long long)q_len * a->g * a->d;
+    qa.q_group = (long long)q_len * a->d;
+    qa.q_tok = a->d;
+    qa.scale = 1.f;
+    qa.out = static_cast<uint16_t*>(a->attn_out.p);
+    if (int r = run_q8_attention(a, c, len, q_len, qa, s)) return r;
+    if (int r = run_o_proj(a, (int)rows_noise, out, s)) return r;
+    c->len.swap(len);
+  } catch (...) {
+    return fail(DFLASH_ERR_MEMORY, "host allocation failed");
+  }
+  return DFLASH_OK;
+}
+
+int dflash_verify(int batch, int n_draft, int vocab, int dtype, const int32_t* draft_tokens,
+                  const void* draft_probs, int64_t draft_batch_stride, int64_t draft_row_stride,
+                  const void* target_probs, int64_t target_batch_stride,
+                  int64_t target_row_stride, const float* u_accept, const float* u_sample,
+                  const int32_t* seq_drafts, int32_t* accepted, int32_t* tokens,
+                  dflash_stream stream) {
+  if (dtype != DFLASH_BF16 && dtype != DFLASH_FP32)
+    return fail(DFLASH_ERR_ARG, "dtype must be DFLASH_BF16 or DFLASH_FP32");
+  if (batch < 0 || n_draft < 0 || vocab <= 0)
+    return fail(DFLASH_ERR_ARG, "batch and n_draft must be >= 0, vocab positive");
+  if (vocab >= (1 << 19)) return fail(DFLASH_ERR_SHAPE, "vocab must be below 2^19");
+  if (batch > (1 << 24) || n_draft > (1 << 20) ||
+      (long long)batch * (n_draft + 1) > (1LL << 30))
+    return fail(DFLASH_ERR_SHAPE, "too many drafted tokens");
+  if (batch == 0) return DFLASH_OK;
+  if (target_probs == nullptr || u_sample == nullptr || accepted == nullptr || tokens == nullptr ||
+      (n_draft > 0 && (draft_tokens == nullptr || u_accept == nullptr)))
+    return fail(DFLASH_ERR_ARG, "null tensor");
+  if (target_row_stride < 0 || target_batch_stride < 0 ||
+      (draft_probs != nullptr && (draft_row_stride < 0 || draft_batch_stride < 0)))
+    return fail(DFLASH_ERR_ARG, "strides must be >= 0");
+  const uintptr_t mask = dtype == DFLASH_BF16 ? 1 : 3;
+  if (((uintptr_t)target_probs & mask) != 0 || ((uintptr_t)draft_probs & mask) != 0)
+    return fail(DFLASH_ERR_ARG, "probabilities must be aligned to their type");
+  int device = 0, num_sms = 0;
+  DF_CUDA(cudaGetDevice(&device), "current device");
+  DF_CUDA(cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device),
+          "device attribute");
+  VerifyArgs a{};
+  a.batch = batch;
+  a.n_draft = n_draft;
+  a.vocab = vocab;
+  a.draft_tokens = draft_tokens;
+  a.draft = n_draft > 0 ? draft_probs : nullptr;
+  a.target = target_probs;
+  a.draft_batch = draft_batch_stride;
+  a.draft_row = draft_row_stride;
+  a.target_batch = target_batch_stride;
+  a.target_row = target_row_stride;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.seq_drafts = seq_drafts;
+  a.accepted = accepted;
+  a.tokens = tokens;
+  DF_CUDA(launch_verify(a, dtype == DFLASH_BF16, num_sms, static_cast<cudaStream_t>(stream)),
+          "verification launch");
+  return DFLASH_OK;
+}
+
 int dflash_wait_probe(dflash_attn* a, int64_t limit_ns, int arrive, dflash_stream stream) {
   if (int r = check_attn(a)) return r;
   if (limit_ns < 1000 || limit_ns > 100000000)

@@ -106,3 +106,18 @@ struct dflash_paged_cache {
   void* k = nullptr;
   void* v = nullptr;
 };
+
+// 8-bit draft KV cache: codes [batch][nkv][rows][d] and scale bytes
+// [batch][nkv][rows][d / 32] of K and of V (q8.cuh).  `rows` is the capacity
+// rounded up to whole 128-key tiles, so that every tile lies in the storage.
+// The attention's partial slots are sized once for every plan, so that a
+// captured call never holds memory a later call has replaced.
+struct dflash_q8_cache {
+  int batch = 0, cap = 0, rows = 0, nkv = 0, d = 0, fmt = 0, device = 0, num_sms = 0;
+  df::Q8Store st{};
+  void* data = nullptr;
+  float* part_o = nullptr;
+  float* part_ml = nullptr;
+  df::Buf stage_k, stage_v;  // bf16 rows of a forward before they are encoded
+  std::vector<int> len;
+};

@@ -286,4 +286,96 @@ cudaError_t launch_packed_prep(const void* q, const void* d_o, const void* o, co
 cudaError_t launch_packed_bwd(const PackedBwdArgs& a, const void* qs, const void* do_tile,
                               const void* k, const void* v, cudaStream_t stream);
 
+// ------------------------------------------------------- 8-bit draft cache
+enum { Q8_E4M3 = 0, Q8_INT8 = 1 };  // as DFLASH_Q8_*
+
+// Storage of an 8-bit cache: codes [B][n_kv][cap][128] and scale bytes
+// [B][n_kv][cap][4] of K and of V (q8.cuh); cap is a multiple of 128.
+struct Q8Store {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  int n_kv;
+  int cap;
+};
+
+// Rows of one append or read: off holds prefix sums of the sequences' row
+// counts, first[b] the cache row of sequence b's first one.
+struct Q8Rows {
+  int n;
+  int off[kMaxBatch + 1];
+  int first[kMaxBatch];
+};
+
+// Where an append reads its bf16 rows, strides in elements: row `local` of
+// sequence b and kv head h starts at b * seq_stride + h * head_stride +
+// row * row_stride, where row is `local` or, for rows packed over the
+// sequences, the call's row number.
+struct Q8Source {
+  const uint16_t* k;
+  const uint16_t* v;
+  long long seq_stride, head_stride, k_row_stride, v_row_stride;
+  int packed;
+};
+
+int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
+                     cudaStream_t s);
+int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
+                   cudaStream_t s);
+
+// Attention over an 8-bit cache (attn_q8.cu).  Query row (b, h, g, t) starts
+// at q + b * q_seq + h * q_head + g * q_group + t * q_tok elements.
+struct Q8AttnArgs {
+  Q8Store st;
+  int batch, groups;
+  int q_len;           // block rows per sequence
+  int tile_tokens;     // block rows per query tile
+  int n_q_tiles;       // query tiles per (sequence, kv head)
+  int window, causal;  // as AttnArgs
+  float scale;         // of a score, in log2 units
+  const uint16_t* q;
+  long long q_seq, q_head, q_group, q_tok;
+  uint16_t* out;       // [B * q_len][n_kv * groups * 128]
+  float* lse;          // [B * q_len][n_kv * groups] natural log, or null
+  float* part_o;       // split units: [slot][128 rows][128] fp32
+  float* part_ml;      // [slot][2][128] running max (log2 units) and sum
+  int* err;
+};
+
+// Work split of one call: every (sequence, query tile, kv head) has n_split
+// units; the units of the sequences follow one another in `order`, as do the
+// partial slots of those with more than one.
+struct Q8Plan {
+  int len[kMaxBatch];           // keys of the sequence
+  int lo[kMaxBatch];            // first key any query of the block can see
+  int n_split[kMaxBatch];
+  int order[kMaxBatch];
+  int unit_off[kMaxBatch + 1];  // first unit of order[i]
+  int slot_off[kMaxBatch];      // first partial slot of order[i] (-1: none)
+};
+
+constexpr int kQ8MaxSplits = 32;
+
+// slots of 128 rows that a plan can need on this GPU
+size_t q8_attention_slots(int num_sms);
+void plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sms);
+int launch_q8_attention(int fmt, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t s);
+
+// ------------------------------------------- verification of drafted tokens
+// One call of dflash_verify (verify.cu); strides in elements.
+struct VerifyArgs {
+  int batch, n_draft, vocab;
+  const int* draft_tokens;
+  const void* draft;   // null: the drafts were not sampled
+  const void* target;
+  long long draft_batch, draft_row, target_batch, target_row;
+  const float* u_accept;
+  const float* u_sample;
+  const int* seq_drafts;  // null: n_draft for every sequence
+  int* accepted;
+  int* tokens;
+};
+int launch_verify(const VerifyArgs& a, int bf16, int num_sms, cudaStream_t s);
+
 }  // namespace df

@@ -425,6 +425,12 @@ DF_DEV float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+DF_DEV unsigned long long ld_cluster_u64(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- misc
 DF_DEV float fast_exp2(float x) {
   float y;

@@ -1,0 +1,135 @@
+// q8_cache.cu -- writing rows into an 8-bit draft KV cache and reading them
+// back (formats: q8.cuh).
+//
+// Both kernels move each byte once and compute a handful of integer
+// operations per channel, so HBM bounds them at large sizes and launch
+// latency at small ones.  Sixteen lanes take one (row, kv head): a lane
+// handles eight channels of K and of V, so that a warp's accesses to the bf16
+// rows are whole 256-byte runs and those to the codes whole 128-byte lines.
+// When writing, a group's four lanes agree on its largest magnitude with two
+// shuffles.
+#include "q8.cuh"
+
+namespace df {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = kThreads / 16;  // (row, kv head) pairs per CTA
+
+// The (row, kv head) that item `it` of a call stands for: row `local` of
+// sequence b, which is row r of the call's packed rows and row `store` of the
+// (sequence, kv head)-major storage.
+struct Item {
+  int b, h, local;
+  long long r;
+  size_t store;
+};
+
+DF_DEV Item item_of(const Q8Rows& t, const Q8Store& st, long long it) {
+  Item w;
+  w.r = it / st.n_kv;
+  w.h = (int)(it - w.r * st.n_kv);
+  int lo = 0, hi = t.n;  // off: prefix sums of the sequences' rows
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.off[mid] <= w.r) lo = mid; else hi = mid;
+  }
+  w.b = lo;
+  w.local = (int)(w.r - t.off[lo]);
+  w.store = ((size_t)lo * st.n_kv + w.h) * st.cap + t.first[lo] + w.local;
+  return w;
+}
+
+struct Coded {
+  uint2 codes;
+  uint32_t byte;
+};
+
+template <int FMT>
+DF_DEV Coded encode8(uint4 x) {
+  constexpr uint32_t m = 0x7fff7fffu;
+  const uint32_t a2 = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
+  uint32_t amax = max(a2 & 0xffffu, a2 >> 16);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  Coded r;
+  r.byte = q8_scale_byte<FMT>(amax);
+  r.codes = make_uint2(0u, 0u);
+  if (r.byte != kQ8NanByte) {
+    const float inv = __uint_as_float((254u - r.byte) << 23);  // 2^-e
+    r.codes.x = q8_encode2<FMT>(x.x, inv) | (q8_encode2<FMT>(x.y, inv) << 16);
+    r.codes.y = q8_encode2<FMT>(x.z, inv) | (q8_encode2<FMT>(x.w, inv) << 16);
+  }
+  return r;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+    q8_append_kernel(const __grid_constant__ Q8Store st, const __grid_constant__ Q8Rows t,
+                     const __grid_constant__ Q8Source src) {
+  const int lane16 = threadIdx.x & 15;
+  const long long it = (long long)blockIdx.x * kItems + (threadIdx.x >> 4);
+  const bool live = it < (long long)t.off[t.n] * st.n_kv;
+  const Item w = item_of(t, st, live ? it : 0);
+  const long long row = src.packed ? w.r : (long long)w.local;
+  const long long base = (long long)w.b * src.seq_stride + (long long)w.h * src.head_stride +
+                         lane16 * 8;
+  grid_dep_sync();
+  const uint4 k =
+      *reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride);
+  const uint4 v =
+      *reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride);
+  const Coded ck = encode8<FMT>(k), cv = encode8<FMT>(v);
+  if (!live) return;
+  *reinterpret_cast<uint2*>(st.k + w.store * 128 + lane16 * 8) = ck.codes;
+  *reinterpret_cast<uint2*>(st.v + w.store * 128 + lane16 * 8) = cv.codes;
+  if ((lane16 & 3) == 0) {
+    st.ks[w.store * 4 + (lane16 >> 2)] = (uint8_t)ck.byte;
+    st.vs[w.store * 4 + (lane16 >> 2)] = (uint8_t)cv.byte;
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+    q8_read_kernel(const __grid_constant__ Q8Store st, const __grid_constant__ Q8Rows t,
+                   uint16_t* k_dst, uint16_t* v_dst) {
+  const int lane16 = threadIdx.x & 15;
+  const long long it = (long long)blockIdx.x * kItems + (threadIdx.x >> 4);
+  const bool live = it < (long long)t.off[t.n] * st.n_kv;
+  const Item w = item_of(t, st, live ? it : 0);
+  grid_dep_sync();
+  if (!live) return;
+  const uint2 ck = *reinterpret_cast<const uint2*>(st.k + w.store * 128 + lane16 * 8);
+  const uint2 cv = *reinterpret_cast<const uint2*>(st.v + w.store * 128 + lane16 * 8);
+  const uint32_t bk = st.ks[w.store * 4 + (lane16 >> 2)];
+  const uint32_t bv = st.vs[w.store * 4 + (lane16 >> 2)];
+  const size_t to = (size_t)it * 128 + lane16 * 8;
+  *reinterpret_cast<uint4*>(k_dst + to) = q8_decode8<FMT>(ck.x, ck.y, q8_scale<FMT>(bk));
+  *reinterpret_cast<uint4*>(v_dst + to) = q8_decode8<FMT>(cv.x, cv.y, q8_scale<FMT>(bv));
+}
+
+unsigned blocks_of(const Q8Rows& t, const Q8Store& st) {
+  return (unsigned)(((long long)t.off[t.n] * st.n_kv + kItems - 1) / kItems);
+}
+
+}  // namespace
+
+int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
+                     cudaStream_t s) {
+  if (t.off[t.n] == 0) return cudaSuccess;
+  const dim3 grid(blocks_of(t, st)), block(kThreads);
+  return fmt == Q8_E4M3 ? launch_pdl(q8_append_kernel<Q8_E4M3>, grid, block, 0, s, st, t, src)
+                        : launch_pdl(q8_append_kernel<Q8_INT8>, grid, block, 0, s, st, t, src);
+}
+
+int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
+                   cudaStream_t s) {
+  if (t.off[t.n] == 0) return cudaSuccess;
+  const dim3 grid(blocks_of(t, st)), block(kThreads);
+  uint16_t* k = static_cast<uint16_t*>(k_dst);
+  uint16_t* v = static_cast<uint16_t*>(v_dst);
+  return fmt == Q8_E4M3 ? launch_pdl(q8_read_kernel<Q8_E4M3>, grid, block, 0, s, st, t, k, v)
+                        : launch_pdl(q8_read_kernel<Q8_INT8>, grid, block, 0, s, st, t, k, v);
+}
+
+}  // namespace df

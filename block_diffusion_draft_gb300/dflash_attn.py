@@ -9,8 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_float, c_int, c_int32, c_void_p
-from typing import Dict, Optional, Sequence
+from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_void_p
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(HERE, "_build", "libdflash_attn.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dflash_attn.h")
 
 DFLASH_BF16, DFLASH_FP32 = 0, 1
+Q8_FORMATS = {"e4m3": 0, "int8": 1}
 STATUS = {0: "OK", -1: "ERR_ARG", -2: "ERR_SHAPE", -3: "ERR_CAPACITY",
           -4: "ERR_RANGE", -5: "ERR_CUDA", -6: "ERR_DEVICE",
           -7: "ERR_UNSUPPORTED", -8: "ERR_MEMORY"}
@@ -77,6 +78,22 @@ _SIGNATURES = {
     "dflash_decoder_layer_forward": ([c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p,
                                       c_void_p, c_void_p, POINTER(c_int32), c_void_p,
                                       c_void_p, c_void_p, c_void_p], c_int),
+    "dflash_q8_cache_create": ([c_void_p, c_int, c_int, c_int, POINTER(c_void_p)], c_int),
+    "dflash_q8_cache_destroy": ([c_void_p], c_int),
+    "dflash_q8_cache_lengths": ([c_void_p, POINTER(c_int32)], c_int),
+    "dflash_q8_cache_crop": ([c_void_p, POINTER(c_int32)], c_int),
+    "dflash_q8_cache_data": ([c_void_p] + [POINTER(c_void_p)] * 4 + [POINTER(c_int32)] * 4,
+                             c_int),
+    "dflash_q8_cache_reserve": ([c_void_p, c_int], c_int),
+    "dflash_q8_cache_append": ([c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                POINTER(c_int32), c_void_p], c_int),
+    "dflash_q8_cache_read": ([c_void_p, POINTER(c_int32), POINTER(c_int32), c_void_p, c_void_p,
+                              c_void_p], c_int),
+    "dflash_q8_attn_core": ([c_void_p, c_void_p, c_int, c_int] + [c_void_p] * 4, c_int),
+    "dflash_attn_forward_q8": ([c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                                POINTER(c_int32), c_void_p, c_void_p, c_void_p], c_int),
+    "dflash_verify": ([c_int] * 4 + [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64,
+                                     c_int64] + [c_void_p] * 6, c_int),
     "dflash_device_error": ([c_void_p, POINTER(c_int32)], c_int),
     "dflash_wait_probe": ([c_void_p, ctypes.c_int64, c_int, c_void_p], c_int),
     "dflash_read_stream_probe": ([c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int64, c_int,
@@ -141,6 +158,28 @@ def _stream(dev: torch.device):
 def _int32_array(xs: Sequence[int]):
     arr = (c_int32 * len(xs))(*[int(x) for x in xs])
     return arr
+
+
+def _require(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device) -> None:
+    """A dense tensor of this type on this device."""
+    if t.dtype != dtype or t.device.type != "cuda" or (
+            device.index is not None and t.device.index != device.index):
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _counts(name: str, n: Sequence[int], batch: int) -> Sequence[int]:
+    if len(n) != batch:
+        raise ValueError(f"{name} must hold one count for each of the {batch} sequences")
+    return n
+
+
+def _block_shape(noise: torch.Tensor, attn: "DFlashAttention") -> Tuple[int, int]:
+    if noise.dim() != 3 or noise.shape[2] != attn.hidden:
+        raise ValueError(f"noise must be [batch, q_len, {attn.hidden}], got {list(noise.shape)}")
+    _require("noise", noise, torch.bfloat16, attn.device)
+    return noise.shape[0], noise.shape[1]
 
 
 class DFlashAttention:
@@ -228,6 +267,52 @@ class DFlashAttention:
                 self.handle, cache.handle, B, q_len, _p(noise), _p(th),
                 _int32_array(n_ctx), _int32_array(len_before), _p(positions),
                 _p(slot_mapping), _p(bt), bt.shape[1], _p(out), _stream(self.device)))
+        return out
+
+    def q8_core(self, cache: "Q8Cache", q: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Attention of a block's queries q [B, q_len, n_heads, d] (bf16, dense,
+        after norm and RoPE) over the rows an 8-bit cache holds.  Returns (out
+        like q, lse [B, q_len, n_heads] fp32, natural log; a row that sees no
+        key has out 0 and lse -inf)."""
+        if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[2:] != (self.n_heads,
+                                                                        self.head_dim):
+            raise ValueError(f"q must be [{cache.batch}, q_len, {self.n_heads}, "
+                             f"{self.head_dim}], got {list(q.shape)}")
+        _require("q", q, torch.bfloat16, self.device)
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
+        with torch.cuda.device(self.device):
+            check(lib().dflash_q8_attn_core(self.handle, cache.handle, q.shape[0], q.shape[1],
+                                            _p(q), _p(out), _p(lse), _stream(self.device)))
+        return out, lse
+
+    def forward_q8(self, cache: "Q8Cache", noise: torch.Tensor,
+                   target_hidden: Optional[torch.Tensor], n_ctx: Sequence[int],
+                   positions: torch.Tensor,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """forward() over an 8-bit cache: the new rows are encoded as they are
+        appended, and the queries see the encoded rows."""
+        B, q_len = _block_shape(noise, self)
+        th = None if target_hidden is None or target_hidden.numel() == 0 else target_hidden
+        rows = sum(_counts("n_ctx", n_ctx, B))
+        if th is not None:
+            if tuple(th.shape) != (rows, self.hidden):
+                raise ValueError(f"target_hidden must be [{rows}, {self.hidden}], "
+                                 f"got {list(th.shape)}")
+            _require("target_hidden", th, torch.bfloat16, self.device)
+        _require("positions", positions, torch.int32, self.device)
+        if positions.numel() != rows + B * q_len:
+            raise ValueError(f"positions must hold {rows + B * q_len} values, "
+                             f"got {positions.numel()}")
+        if out is None:
+            out = torch.empty_like(noise)
+        elif out.shape != noise.shape:
+            raise ValueError("out must have the shape of noise")
+        _require("out", out, torch.bfloat16, self.device)
+        with torch.cuda.device(self.device):
+            check(lib().dflash_attn_forward_q8(
+                self.handle, cache.handle, B, q_len, _p(noise), _p(th),
+                _int32_array(n_ctx), _p(positions), _p(out), _stream(self.device)))
         return out
 
     def forward_packed(self, noise: torch.Tensor, target_hidden: torch.Tensor,
@@ -401,6 +486,137 @@ class PagedCache:
             self.close()
         except Exception:
             pass
+
+
+class Q8Cache:
+    """Draft KV cache in 8 bits held by the library: one code byte per channel
+    and a power-of-two scale per 32 channels (``fmt`` "int8" or "e4m3"; see
+    dflash_q8_cache_* in include/dflash_attn.h)."""
+
+    def __init__(self, attn: DFlashAttention, batch: int, capacity: int, fmt: str = "int8"):
+        if fmt not in Q8_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(Q8_FORMATS)}")
+        self.attn = attn
+        self.batch, self.capacity, self.fmt = batch, capacity, fmt
+        h = c_void_p()
+        with torch.cuda.device(attn.device):
+            check(lib().dflash_q8_cache_create(attn.handle, batch, capacity, Q8_FORMATS[fmt],
+                                               ctypes.byref(h)))
+        self.handle = h
+
+    def lengths(self) -> list:
+        arr = (c_int32 * self.batch)()
+        check(lib().dflash_q8_cache_lengths(self.handle, arr))
+        return list(arr)
+
+    def crop(self, keep: Sequence[int]) -> None:
+        check(lib().dflash_q8_cache_crop(self.handle, _int32_array(
+            _counts("keep", keep, self.batch))))
+
+    def reserve(self, max_new_rows: int) -> None:
+        """Size the scratch of forward_q8 calls that append at most this many
+        rows to a sequence."""
+        with torch.cuda.device(self.attn.device):
+            check(lib().dflash_q8_cache_reserve(self.handle, max_new_rows))
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, n: Sequence[int]) -> None:
+        """Encode n[b] rows behind those of sequence b, from k and v [sum n,
+        n_kv, d] bf16: the sequences' rows one after another.  A row's heads
+        are dense; rows may be slices of a wider tensor."""
+        a = self.attn
+        rows = sum(_counts("n", n, self.batch))
+        shape = (rows, a.n_kv_heads, a.head_dim)
+        strides = []
+        for name, t in (("k", k), ("v", v)):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+            if t.dtype != torch.bfloat16 or t.device.type != "cuda" or (
+                    a.device.index is not None and t.device.index != a.device.index):
+                raise ValueError(f"{name} must be bfloat16 on {a.device}, "
+                                 f"got {t.dtype} on {t.device}")
+            s = t.stride()
+            dense = s[2] == 1 and (s[1] == a.head_dim or a.n_kv_heads == 1)
+            if rows > 0 and not dense:
+                raise ValueError(f"{name}: a row's heads must be dense")
+            strides.append(s[0] if rows > 1 else a.n_kv_heads * a.head_dim)
+        with torch.cuda.device(a.device):
+            check(lib().dflash_q8_cache_append(self.handle, _p(k), _p(v), strides[0], strides[1],
+                                               _int32_array(n), _stream(a.device)))
+
+    def read(self, first: Optional[Sequence[int]] = None, n: Optional[Sequence[int]] = None):
+        """K and V [sum n, n_kv, d] bf16 of rows first[b] .. first[b] + n[b] - 1
+        of every sequence, one sequence after another (default: every row)."""
+        a = self.attn
+        first = [0] * self.batch if first is None else _counts("first", first, self.batch)
+        if n is None:
+            n = [length - f for length, f in zip(self.lengths(), first)]
+        shape = (max(0, sum(_counts("n", n, self.batch))), a.n_kv_heads, a.head_dim)
+        k = torch.empty(shape, device=a.device, dtype=torch.bfloat16)
+        v = torch.empty(shape, device=a.device, dtype=torch.bfloat16)
+        with torch.cuda.device(a.device):
+            check(lib().dflash_q8_cache_read(self.handle, _int32_array(first), _int32_array(n),
+                                             _p(k), _p(v), _stream(a.device)))
+        return k, v
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            lib().dflash_q8_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def verify_draft(draft_tokens: torch.Tensor, draft_probs: Optional[torch.Tensor],
+                 target_probs: torch.Tensor, u_accept: torch.Tensor, u_sample: torch.Tensor,
+                 n_draft: Optional[torch.Tensor] = None):
+    """Verify drafted tokens [B, D] (int32) against the target's probabilities
+    [B, D + 1, V] (fp32 or bf16, a row's values dense, other strides free) from
+    uniform numbers u_accept [B, D] and u_sample [B] (fp32).  draft_probs [B, D,
+    V] are the distributions the drafts were drawn from, None if they were
+    chosen without sampling; n_draft [B] (int32) are the drafts of each
+    sequence where they differ.  Returns (accepted [B], tokens [B, D + 1])
+    int32: the number of accepted drafts, and those followed by one drawn token
+    and -1s.  See dflash_verify in include/dflash_attn.h."""
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise ValueError("draft_tokens must be [B, D] and target_probs [B, D + 1, V]")
+    B, D = draft_tokens.shape
+    V, dev, dt = target_probs.shape[2], target_probs.device, target_probs.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("probabilities must be float32 or bfloat16")
+    if dev.type != "cuda":
+        raise ValueError("the library runs on CUDA devices only")
+    shapes = [("target_probs", target_probs, (B, D + 1, V)),
+              ("draft_probs", draft_probs, (B, D, V)), ("u_accept", u_accept, (B, D)),
+              ("u_sample", u_sample, (B,)), ("n_draft", n_draft, (B,))]
+    for name, t, shape in shapes:
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    for name, t, want in (("draft_tokens", draft_tokens, torch.int32),
+                          ("u_accept", u_accept, torch.float32),
+                          ("u_sample", u_sample, torch.float32),
+                          ("n_draft", n_draft, torch.int32)):
+        if t is not None:
+            _require(name, t, want, dev)
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is not None:
+            if t.dtype != dt or t.device != dev:
+                raise ValueError(f"{name} must be {dt} on {dev}, got {t.dtype} on {t.device}")
+            if t.numel() and t.stride(2) != 1 and V > 1:
+                raise ValueError(f"{name}: a row's values must be dense")
+    q = draft_probs
+    accepted = torch.empty(B, device=dev, dtype=torch.int32)
+    tokens = torch.empty(B, D + 1, device=dev, dtype=torch.int32)
+    with torch.cuda.device(dev):
+        check(lib().dflash_verify(
+            B, D, V, DFLASH_BF16 if dt == torch.bfloat16 else DFLASH_FP32, _p(draft_tokens),
+            _p(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
+            _p(target_probs), target_probs.stride(0), target_probs.stride(1), _p(u_accept),
+            _p(u_sample), _p(n_draft), _p(accepted), _p(tokens), _stream(dev)))
+    return accepted, tokens
 
 
 class KVGroup:

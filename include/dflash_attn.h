@@ -57,6 +57,7 @@ typedef struct dflash_cache dflash_cache; /* one draft KV cache */
 typedef struct dflash_kv_group dflash_kv_group; /* context K/V of several layers */
 typedef struct dflash_mlp dflash_mlp;     /* norms + MLP of a decoder layer */
 typedef struct dflash_paged_cache dflash_paged_cache; /* paged KV storage */
+typedef struct dflash_q8_cache dflash_q8_cache; /* draft KV cache in 8 bits */
 typedef void* dflash_stream;              /* a cudaStream_t */
 
 enum {
@@ -432,6 +433,151 @@ int dflash_packed_attn_core_backward(dflash_attn* attn, int batch, int seq,
                                      const int32_t* anchors, void* dq,
                                      void* dk, void* dv,
                                      dflash_stream stream);
+
+/* Draft KV cache in 8 bits (the pages have no counterpart: a property of this
+ * library, not of the method).  A row of a KV head is 128 code bytes and one
+ * scale byte per group of 32 channels, 132 bytes instead of 256, which is what
+ * a decode step reads per key.
+ *
+ * Value of a channel = code * 2^e, e = scale byte - 127, where for the group's
+ * largest magnitude amax
+ *   DFLASH_Q8_INT8: code a whole number of magnitude at most 127, and
+ *   DFLASH_Q8_E4M3: code an e4m3 number (3 fraction bits) of magnitude at
+ *                   most 448;
+ *   e = the smallest integer with amax <= 127 * 2^e (448 * 2^e), at least
+ *       -117; code = x * 2^-e rounded to nearest, ties to even.
+ * Values read back are exact in bf16.  The error of a channel is at most
+ * 2^(e-1) with int8 (at most amax / 127), and with e4m3 at most 2^-4 of
+ * itself or 2^(e-10): int8 is the finer one for rows whose channels are of one
+ * size, e4m3 keeps the small channels of rows with a few large ones.
+ * Magnitudes above 2^126 are stored as 2^126; a group with an infinity or NaN
+ * reads back as NaN in all of its channels.
+ *
+ * Storage: codes [batch][n_kv_heads][rows][128] (int8: sign in bit 7, then the
+ * magnitude) and scale bytes [batch][n_kv_heads][rows][4], K and V each, rows
+ * = capacity_rows rounded up to a multiple of 128, zeroed at creation.
+ * Lengths start at 0 and are kept on the host, as in dflash_cache; crop moves
+ * no data.  bf16 layers only (else _UNSUPPORTED).
+ *
+ * Every call that enqueues work needs the layer's device to be the current
+ * one (_ARG).  The cache owns the scratch of the attention over it, sized once
+ * at creation: calls on one cache must not run concurrently on different
+ * streams.  In a CUDA graph a call keeps the lengths, and so the rows it
+ * writes and reads, of the moment of its capture. */
+enum { DFLASH_Q8_E4M3 = 0, DFLASH_Q8_INT8 = 1 };
+
+int dflash_q8_cache_create(const dflash_attn* attn, int batch,
+                           int capacity_rows, int format,
+                           dflash_q8_cache** out);
+int dflash_q8_cache_destroy(dflash_q8_cache* cache);
+
+/* As dflash_cache_lengths and dflash_cache_crop. */
+int dflash_q8_cache_lengths(const dflash_q8_cache* cache, int32_t* host_len);
+int dflash_q8_cache_crop(dflash_q8_cache* cache, const int32_t* host_keep);
+
+/* Device pointers to the storage (layout above) and its geometry
+ * (stored_rows: the rounded capacity); any output may be NULL.  For
+ * inspection; writing through them is the caller's risk. */
+int dflash_q8_cache_data(const dflash_q8_cache* cache, void** k_codes,
+                         void** v_codes, void** k_scales, void** v_scales,
+                         int32_t* batch, int32_t* n_kv_heads,
+                         int32_t* stored_rows, int32_t* head_dim);
+
+/* Size the cache's scratch for dflash_attn_forward_q8 calls that append at
+ * most max_new_rows rows (context and block) to any sequence, so that they
+ * allocate nothing for it. */
+int dflash_q8_cache_reserve(dflash_q8_cache* cache, int max_new_rows);
+
+/* Encode host_n[b] rows of K and V behind the rows sequence b holds.
+ *   k, v    device bf16, row r (the sequences' new rows one after another)
+ *           at k + r * k_row_stride elements: [n_kv_heads][128], dense; rows
+ *           may be slices of a wider tensor (strides multiples of 8, at least
+ *           n_kv_heads * 128).  May be NULL when every count is 0.
+ *   host_n  host [batch]
+ * Errors: _ARG, _SHAPE, _CAPACITY (nothing is appended for any sequence),
+ * _CUDA. */
+int dflash_q8_cache_append(dflash_q8_cache* cache, const void* k, const void* v,
+                           int64_t k_row_stride, int64_t v_row_stride,
+                           const int32_t* host_n, dflash_stream stream);
+
+/* Decode rows host_first[b] .. host_first[b] + host_n[b] - 1 of every
+ * sequence, one sequence after another, into the dense device tensors k_dst
+ * and v_dst [sum host_n][n_kv_heads][128] bf16.
+ * Errors: _ARG, _SHAPE, _RANGE (rows the sequence does not hold), _CUDA. */
+int dflash_q8_cache_read(const dflash_q8_cache* cache, const int32_t* host_first,
+                         const int32_t* host_n, void* k_dst, void* v_dst,
+                         dflash_stream stream);
+
+/* Attention of a block's queries over an 8-bit cache, without the layer's
+ * projections (its weights are not used; its head counts, window and causal
+ * flag are).
+ *   q    device bf16 [batch][q_len][n_heads][128], after norm and RoPE
+ *   out  device bf16, as q
+ *   lse  device fp32 [batch][q_len][n_heads] or NULL: natural log of the sum
+ *        over the row's keys of exp(q.k / sqrt(128))
+ * The q_len queries stand at the sequence's last q_len key indices (block row
+ * t at length - q_len + t, which only a window or the causal flag look at); K
+ * and V are the rows the cache holds.  A row that sees no key gets out = 0 and
+ * lse = -infinity.  Any q_len; at most 128 query heads per KV head
+ * (_UNSUPPORTED).  Errors: _ARG, _SHAPE, _UNSUPPORTED, _CUDA. */
+int dflash_q8_attn_core(dflash_attn* attn, dflash_q8_cache* cache, int batch,
+                        int q_len, const void* q, void* out, float* lse,
+                        dflash_stream stream);
+
+/* dflash_attn_forward over an 8-bit cache: arguments, outputs, appended rows,
+ * lengths and errors are those of dflash_attn_forward.  K (after k_norm and
+ * RoPE) and V are rounded to bf16 and encoded as they are appended, and the
+ * queries see the encoded rows, the block's own included.  Any q_len. */
+int dflash_attn_forward_q8(dflash_attn* attn, dflash_q8_cache* cache, int batch,
+                           int q_len, const void* noise_hidden,
+                           const void* target_hidden, const int32_t* host_n_ctx,
+                           const int32_t* positions, void* out,
+                           dflash_stream stream);
+
+/* Verification of drafted tokens against the target's probabilities, from
+ * given uniform numbers ([P3] 关键设计: the target accepts a prefix of the
+ * block, to which the draft cache is then cropped).  Needs no layer.
+ *
+ * Sequence b has drafted tokens x_0 .. x_{n-1}, drawn from the distributions
+ * q_i, and the target's distributions p_0 .. p_n (p_i: after i of them).
+ * Draft i is accepted when every one before it is and
+ *     u_accept[i] * q_i(x_i) < p_i(x_i)        (compared without rounding).
+ * With a the number of accepted drafts, one more token follows them: drawn
+ * from max(p_a - q_a, 0) when draft a was rejected, from p_n when a = n, as
+ * the first token whose cumulative weight exceeds floor(u_sample * sum of the
+ * weights).  Weights are whole multiples of 2^-44: a probability is taken as
+ * floor(min(max(p, 0), 1) * 2^44), NaN as 0.  If the difference leaves no
+ * weight the token is drawn from p_a; if that has none either it is -1.  The
+ * result does not depend on the GPU's order of summation.
+ *
+ * draft_probs NULL: the drafts were chosen without sampling (the largest
+ * logit, say), so q_i is 1 at x_i and 0 elsewhere.
+ *
+ *   dtype         of the probabilities, DFLASH_BF16 or DFLASH_FP32
+ *   draft_tokens  device int32 [batch][n_draft]; a token outside [0, vocab)
+ *                 is rejected
+ *   draft_probs   device: p of token v at batch_stride * b + row_stride * i
+ *                 + v elements, i < n_draft; may be NULL
+ *   target_probs  the same, i <= n_draft.  Rows on 16-byte boundaries are
+ *                 read with wider loads.
+ *   u_accept      device fp32 [batch][n_draft], u_sample fp32 [batch], in
+ *                 [0, 1) (a u_sample outside is moved to the nearest end, NaN
+ *                 to 0)
+ *   seq_drafts    device int32 [batch] or NULL: drafts of each sequence,
+ *                 moved into [0, n_draft]; NULL: n_draft for all
+ *   accepted      device int32 [batch]: a
+ *   tokens        device int32 [batch][n_draft + 1]: the accepted drafts, the
+ *                 token that follows, then -1
+ * n_draft may be 0 (a token is drawn from p_0); draft_tokens and u_accept may
+ * then be NULL.  Work goes to the current device.
+ * Errors: _ARG, _SHAPE (vocab >= 2^19, too many tokens), _CUDA. */
+int dflash_verify(int batch, int n_draft, int vocab, int dtype,
+                  const int32_t* draft_tokens, const void* draft_probs,
+                  int64_t draft_batch_stride, int64_t draft_row_stride,
+                  const void* target_probs, int64_t target_batch_stride,
+                  int64_t target_row_stride, const float* u_accept,
+                  const float* u_sample, const int32_t* seq_drafts,
+                  int32_t* accepted, int32_t* tokens, dflash_stream stream);
 
 /* Kernels this library has launched in this process so far, over every
  * layer, cache and device (a launch that returned an error counts too).  A
