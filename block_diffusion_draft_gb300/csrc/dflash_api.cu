@@ -1269,7 +1269,8 @@ int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>
                                  0, (long long)len[b] - q_len - a.window + 1)
                            : 0;
   }
-  plan_q8_attention(p, c->batch, c->nkv, a.n_q_tiles, c->num_sms);
+  if (!plan_q8_attention(p, c->batch, c->nkv, a.n_q_tiles, c->num_sms))
+    return fail(DFLASH_ERR_SHAPE, "too many key tiles");
   TraceScope tr(at, DFLASH_K_ATTN, s);
   DF_CUDA(launch_q8_attention(c->fmt, a, p, s), "8-bit cache attention launch");
   return DFLASH_OK;
@@ -1323,12 +1324,13 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   c->num_sms = a->num_sms;
   const size_t rows = (size_t)batch * a->nkv * c->rows;
   const size_t codes = rows * 128, scales = rows * 4, slots = q8_attention_slots(c->num_sms);
-  cudaError_t e = cudaMalloc(&c->data, 2 * (codes + scales));
+  const size_t ranges = (size_t)batch * a->nkv * 4 * sizeof(int);
+  cudaError_t e = cudaMalloc(&c->data, 2 * (codes + scales) + ranges);
   if (e == cudaSuccess) e = cudaMalloc(&c->part_o, slots * 128 * 128 * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&c->part_ml, slots * 256 * sizeof(float));
   // zeroed: rows past a sequence's end are read with its last tile (and
   // decoded to zero); finished before any other stream can use the cache
-  if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales));
+  if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales) + ranges);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     dflash_q8_cache_destroy(c);
@@ -1339,6 +1341,7 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   c->st.v = p + codes;
   c->st.ks = p + 2 * codes;
   c->st.vs = p + 2 * codes + scales;
+  c->st.range = reinterpret_cast<int*>(p + 2 * (codes + scales));
   c->st.n_kv = c->nkv;
   c->st.cap = c->rows;
   *out = c;

@@ -290,12 +290,14 @@ cudaError_t launch_packed_bwd(const PackedBwdArgs& a, const void* qs, const void
 enum { Q8_E4M3 = 0, Q8_INT8 = 1 };  // as DFLASH_Q8_*
 
 // Storage of an 8-bit cache: codes [B][n_kv][cap][128] and scale bytes
-// [B][n_kv][cap][4] of K and of V (q8.cuh); cap is a multiple of 128.
+// [B][n_kv][cap][4] of K and of V (q8.cuh); cap is a multiple of 128.  range
+// [B][n_kv][4]: smallest and largest scale byte of K, then of V.
 struct Q8Store {
   uint8_t* k;
   uint8_t* v;
   uint8_t* ks;
   uint8_t* vs;
+  int* range;
   int n_kv;
   int cap;
 };
@@ -338,28 +340,26 @@ struct Q8AttnArgs {
   long long q_seq, q_head, q_group, q_tok;
   uint16_t* out;       // [B * q_len][n_kv * groups * 128]
   float* lse;          // [B * q_len][n_kv * groups] natural log, or null
-  float* part_o;       // split units: [slot][128 rows][128] fp32
+  float* part_o;       // pairs across CTAs: [slot][128 rows][128] fp32
   float* part_ml;      // [slot][2][128] running max (log2 units) and sum
   int* err;
 };
 
-// Work split of one call: every (sequence, query tile, kv head) has n_split
-// units; the units of the sequences follow one another in `order`, as do the
-// partial slots of those with more than one.
+// Work split of one call: the key tiles of all (sequence, query tile, kv head)
+// pairs in one line, `share` consecutive tiles per CTA.
 struct Q8Plan {
-  int len[kMaxBatch];           // keys of the sequence
-  int lo[kMaxBatch];            // first key any query of the block can see
-  int n_split[kMaxBatch];
-  int order[kMaxBatch];
-  int unit_off[kMaxBatch + 1];  // first unit of order[i]
-  int slot_off[kMaxBatch];      // first partial slot of order[i] (-1: none)
+  int len[kMaxBatch];        // keys of the sequence
+  int lo[kMaxBatch];         // first key any query of the block can see
+  int first[kMaxBatch + 1];  // its first tile in the line
+  int share;
 };
 
-constexpr int kQ8MaxSplits = 32;
+constexpr int kQ8MaxSplits = 32;  // CTAs that a pair can lie across
 
 // slots of 128 rows that a plan can need on this GPU
 size_t q8_attention_slots(int num_sms);
-void plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sms);
+// fills first and share from len and lo; false if there are too many tiles
+bool plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sms);
 int launch_q8_attention(int fmt, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t s);
 
 // ------------------------------------------- verification of drafted tokens

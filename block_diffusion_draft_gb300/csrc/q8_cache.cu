@@ -56,11 +56,36 @@ DF_DEV Coded encode8(uint4 x) {
   r.byte = q8_scale_byte<FMT>(amax);
   r.codes = make_uint2(0u, 0u);
   if (r.byte != kQ8NanByte) {
-    const float inv = __uint_as_float((254u - r.byte) << 23);  // 2^-e
+    const float inv = __uint_as_float((254u - max(r.byte, 1u)) << 23);  // 2^-e
     r.codes.x = q8_encode2<FMT>(x.x, inv) | (q8_encode2<FMT>(x.y, inv) << 16);
     r.codes.y = q8_encode2<FMT>(x.z, inv) | (q8_encode2<FMT>(x.w, inv) << 16);
   }
   return r;
+}
+
+// A row's smallest and largest scale byte, over the four groups (zero groups
+// do not count), into the (sequence, kv head)'s range, read beforehand: most
+// rows lie in it already, so an atomic is rare.
+DF_DEV void widen(int* range, int now_lo, int now_hi, uint32_t byte, bool writer) {
+  int lo = byte != 0u ? (int)byte : 255, hi = (int)byte;
+#pragma unroll
+  for (int d = 4; d <= 8; d <<= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+  }
+  if (writer && lo < now_lo) atomicMin(range, lo);
+  if (writer && hi > now_hi) atomicMax(range + 1, hi);
+}
+
+// Ranges of the sequences whose rows begin anew.
+__global__ void q8_reset_kernel(const __grid_constant__ Q8Store st,
+                                const __grid_constant__ Q8Rows t) {
+  grid_dep_sync();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;  // (sequence, head)
+  if (i >= t.n * st.n_kv) return;
+  const int b = i / st.n_kv;
+  if (t.first[b] == 0 && t.off[b + 1] > t.off[b])
+    reinterpret_cast<int4*>(st.range)[i] = make_int4(255, 0, 255, 0);
 }
 
 template <int FMT>
@@ -79,7 +104,11 @@ __global__ void __launch_bounds__(kThreads)
       *reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride);
   const uint4 v =
       *reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride);
+  int* range = st.range + ((size_t)w.b * st.n_kv + w.h) * 4;
+  const int4 now = __ldcg(reinterpret_cast<const int4*>(range));
   const Coded ck = encode8<FMT>(k), cv = encode8<FMT>(v);
+  widen(range, now.x, now.y, ck.byte, live && lane16 == 0);
+  widen(range + 2, now.z, now.w, cv.byte, live && lane16 == 0);
   if (!live) return;
   *reinterpret_cast<uint2*>(st.k + w.store * 128 + lane16 * 8) = ck.codes;
   *reinterpret_cast<uint2*>(st.v + w.store * 128 + lane16 * 8) = cv.codes;
@@ -104,8 +133,8 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t bk = st.ks[w.store * 4 + (lane16 >> 2)];
   const uint32_t bv = st.vs[w.store * 4 + (lane16 >> 2)];
   const size_t to = (size_t)it * 128 + lane16 * 8;
-  *reinterpret_cast<uint4*>(k_dst + to) = q8_decode8<FMT>(ck.x, ck.y, q8_scale<FMT>(bk));
-  *reinterpret_cast<uint4*>(v_dst + to) = q8_decode8<FMT>(cv.x, cv.y, q8_scale<FMT>(bv));
+  *reinterpret_cast<uint4*>(k_dst + to) = bf16_decode8<FMT>(ck.x, ck.y, bf16_scale(bk));
+  *reinterpret_cast<uint4*>(v_dst + to) = bf16_decode8<FMT>(cv.x, cv.y, bf16_scale(bv));
 }
 
 unsigned blocks_of(const Q8Rows& t, const Q8Store& st) {
@@ -117,6 +146,13 @@ unsigned blocks_of(const Q8Rows& t, const Q8Store& st) {
 int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
                      cudaStream_t s) {
   if (t.off[t.n] == 0) return cudaSuccess;
+  bool anew = false;
+  for (int b = 0; b < t.n; ++b) anew = anew || (t.first[b] == 0 && t.off[b + 1] > t.off[b]);
+  if (anew) {
+    const cudaError_t e = launch_pdl(q8_reset_kernel, dim3((t.n * st.n_kv + 255) / 256),
+                                     dim3(256), 0, s, st, t);
+    if (e != cudaSuccess) return e;
+  }
   const dim3 grid(blocks_of(t, st)), block(kThreads);
   return fmt == Q8_E4M3 ? launch_pdl(q8_append_kernel<Q8_E4M3>, grid, block, 0, s, st, t, src)
                         : launch_pdl(q8_append_kernel<Q8_INT8>, grid, block, 0, s, st, t, src);

@@ -445,7 +445,8 @@ int dflash_packed_attn_core_backward(dflash_attn* attn, int batch, int seq,
  *   DFLASH_Q8_E4M3: code an e4m3 number (3 fraction bits) of magnitude at
  *                   most 448;
  *   e = the smallest integer with amax <= 127 * 2^e (448 * 2^e), at least
- *       -117; code = x * 2^-e rounded to nearest, ties to even.
+ *       -117; code = x * 2^-e rounded to nearest, ties to even.  Scale byte 0
+ *   marks a group of zeros.
  * Values read back are exact in bf16.  The error of a channel is at most
  * 2^(e-1) with int8 (at most amax / 127), and with e4m3 at most 2^-4 of
  * itself or 2^(e-10): int8 is the finer one for rows whose channels are of one
@@ -453,8 +454,8 @@ int dflash_packed_attn_core_backward(dflash_attn* attn, int batch, int seq,
  * Magnitudes above 2^126 are stored as 2^126; a group with an infinity or NaN
  * reads back as NaN in all of its channels.
  *
- * Storage: codes [batch][n_kv_heads][rows][128] (int8: sign in bit 7, then the
- * magnitude) and scale bytes [batch][n_kv_heads][rows][4], K and V each, rows
+ * Storage: codes [batch][n_kv_heads][rows][128] (int8: the number plus 128)
+ * and scale bytes [batch][n_kv_heads][rows][4], K and V each, rows
  * = capacity_rows rounded up to a multiple of 128, zeroed at creation.
  * Lengths start at 0 and are kept on the host, as in dflash_cache; crop moves
  * no data.  bf16 layers only (else _UNSUPPORTED).

@@ -201,21 +201,26 @@ def test_refusals():
 
 
 # ---------------------------------------------------------------- attention
+def bounds(q, k, v, window, causal):
+    """One sequence's reference (out, lse) and how far an evaluation may be
+    off, elementwise.  P is rounded once to bf16 (2^-8 relative; fp16 where the
+    scales allow it, which is finer), the output once more; a score's fp32 sum
+    of 128 products is off by at most 128 * 2^-24 of the sum of their
+    magnitudes (Q), which moves a probability by that much relatively, twice
+    with the row's sum; the row's sum of n terms by n * 2^-24; exp2's 2 ulp and
+    the rescalings are covered by 2^-18 in all."""
+    ref, rl, A, Q = R.attend(q, k, v, window, causal)
+    noise = 2 * (2.0 ** -17 * Q + k.shape[0] * 2.0 ** -24 + 2.0 ** -18)
+    return ref, rl, 2.0 ** -8 * (A + np.abs(ref)) * 1.01 + noise[..., None] * A, noise
+
+
 def check_attention(a, cache, q, out, lse, k, v, counts, window, causal):
-    """Bounds, elementwise.  P is rounded once to bf16 (2^-8 relative), the
-    output once more; a score's fp32 sum of 128 products is off by at most
-    128 * 2^-24 of the sum of their magnitudes (Q), which moves a probability
-    by that much relatively, twice with the row's sum; the row's sum of n
-    terms by n * 2^-24; exp2's 2 ulp and the rescalings are covered by 2^-18
-    in all."""
     at = 0
     for b, n in enumerate(counts):
         kb, vb = T.f64(k[at:at + n]), T.f64(v[at:at + n])
         at += n
-        ref, rl, A, Q = R.attend(T.f64(q[b]), kb, vb, window, causal)
-        noise = 2 * (2.0 ** -17 * Q + n * 2.0 ** -24 + 2.0 ** -18)
+        ref, rl, tol, noise = bounds(T.f64(q[b]), kb, vb, window, causal)
         got, gl = T.f64(out[b]), T.f64(lse[b])
-        tol = 2.0 ** -8 * A * 1.01 + 2.0 ** -8 * np.abs(ref) * 1.01 + noise[..., None] * A
         bad = np.abs(got - ref) > tol
         assert not bad.any(), (b, np.argwhere(bad)[:5], np.abs(got - ref).max())
         empty = np.isneginf(rl)
@@ -303,10 +308,10 @@ def test_nan_reaches_only_what_sees_it(fmt):
     a = layer(2, 1, 0, True)
     T_, n = 8, 150
     k, v = rows(n, 1, 1), rows(n, 1, 2)
-    clean = Q8Cache(a, 1, 256, fmt)
-    clean.append(k.cuda(), v.cuda(), [n])
     q = rows(T_, 2, 3, 0.2).view(1, T_, 2, 128).cuda()
-    want, wl = a.q8_core(clean, q)
+    # the rows that see neither NaN are held to the same bounds as without it
+    want, wl, tol, noise = bounds(T.f64(q[0]), R.stored_values(T.f64(k), fmt),
+                                  R.stored_values(T.f64(v), fmt), 0, True)
     v2, k2 = v.clone(), k.clone()
     v2[n - 3, 0, 40] = math.nan   # key 147: seen by rows 5, 6, 7; channels 32..63
     k2[n - 2, 0, 7] = math.inf    # key 148: seen by rows 6, 7
@@ -317,11 +322,36 @@ def test_nan_reaches_only_what_sees_it(fmt):
     cache.append(bad, bad, [60])
     cache.crop([n])
     out, lse = a.q8_core(cache, q)
-    assert torch.equal(out[0, :5], want[0, :5]) and torch.equal(lse[0, :5], wl[0, :5])
-    assert bool(out[0, 5, :, 32:64].isnan().all())
-    assert torch.equal(out[0, 5, :, :32], want[0, 5, :, :32])
-    assert torch.equal(out[0, 5, :, 64:], want[0, 5, :, 64:]) and torch.equal(lse[0, 5], wl[0, 5])
-    assert bool(out[0, 6:].isnan().all()) and bool(lse[0, 6:].isnan().all())
+    got, gl = T.f64(out[0]), T.f64(lse[0])
+    diff = np.abs(got - want) - tol
+    assert np.all(diff[:5] <= 0) and np.all(diff[5, :, :32] <= 0) and np.all(diff[5, :, 64:] <= 0)
+    assert np.all(np.isnan(got[5, :, 32:64]))
+    assert np.all(np.abs(gl[:6] - wl[:6]) <= noise[:6] + 2.0 ** -21 * np.abs(wl[:6]))
+    assert np.all(np.isnan(got[6:])) and np.all(np.isnan(gl[6:]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_scales_far_apart(fmt):
+    """Groups whose scales lie 2^19, 2^20 and up to 2^200 apart, zero rows and
+    groups, and the largest numbers in keys that the mask hides: the others
+    keep their precision."""
+    a = layer(2, 1, 0, True)
+    T_ = 4
+    for n, small, hide in ((140, 2.0 ** -19, 1.0), (140, 2.0 ** -20, 1.0), (300, 2.0 ** -40, 1.0),
+                           (300, 1.0, 2.0 ** 100), (130, 2.0 ** -100, 2.0 ** 90)):
+        k, v = rows(n, 1, 1, 0.0), rows(n, 1, 2, 0.0)
+        v[:, :, 32:64] *= small      # a group of small channels
+        v[n // 2] *= small           # a key of small values
+        v[5], k[9] = 0, 0            # zero rows
+        v[3, :, 64:96] = 0
+        k[7, :, :32] = 0
+        v[n - 2:] *= hide            # seen by the last two block rows only
+        cache = Q8Cache(a, 1, 512, fmt)
+        cache.append(k.cuda(), v.cuda(), [n])
+        q = rows(T_, 2, 3, 0.2).view(1, T_, 2, 128).cuda()
+        out, lse = a.q8_core(cache, q)
+        ck, cv = cache.read()
+        check_attention(a, cache, q, out, lse, ck, cv, [n], 0, True)
 
 
 def test_nan_through_split_units():
