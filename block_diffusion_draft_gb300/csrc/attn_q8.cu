@@ -7,13 +7,11 @@
 // -- stand in one line; CTA c, one per SM, takes tiles [c U, (c + 1) U) of it:
 // segments of one pair after another.  Every SM gets the same number of tiles
 // whatever the lengths, and a pair that lies across CTAs is merged afterwards.
-// (Units of a pair's equal shares, dispatched largest first, left the last SMs
-// working alone and paid a kernel start per unit: PERS.)
 //
 // The codes of a tile are 33 KB against the 64 KB of a bf16 tile, so HBM asks
 // for a tile every 0.74 us per SM; on the way to the tensor core every code
-// becomes a 16-bit number in shared memory.  That, not the MMAs (1088 cycles a
-// tile), is the longest queue of an SM, so most warps do nothing else:
+// becomes a 16-bit number in shared memory.  Most warps do nothing else.  The two
+// MMAs are the longest queue, about 2560 cycles a tile:
 //
 //   warps 0-7    softmax, two threads per TMEM lane (accumulator row); the Q
 //                tile into TMEM at a segment's start, O out at its end
@@ -73,9 +71,9 @@ constexpr uint32_t O_COL = 256, Q_COL = 384, TMEM_COLS = 512;
 // staged query rows (at most 64) and, between segments, 32 channels of the
 // lanes' O on their way out
 constexpr uint32_t Q_PITCH = HD * 2 + 16;
-constexpr int X_LD = 33;
-constexpr uint32_t QX_BYTES = 64 * Q_PITCH;
-static_assert(QX_BYTES >= 128 * X_LD * 4, "exchange");
+constexpr int X_LD = 36;
+constexpr uint32_t QX_BYTES = 128 * X_LD * 4;
+static_assert(QX_BYTES >= 64 * Q_PITCH, "query rows");
 constexpr size_t kSmem = 1024 + 4 * TILE + RING * SLOT + QX_BYTES + 4 * TK + 512 + 9 * TK * 4;
 constexpr float kRescale = 8.f;           // log2 units
 constexpr float kLift = 7.f;              // fp16 P = 2^(score - max + 7)
@@ -213,7 +211,8 @@ struct Shared {
   uint64_t *s_full;        // S(g) complete: K(g)'s stage is free
   uint64_t *p_full;
   uint64_t *o_done;        // PV(g) complete: V(g)'s stage and S(g)'s buffer are free
-  uint64_t *q_staged;      // per segment: its query rows are in shared memory
+  int4* mode;              // [2] by segment: half, k0, v0
+  uint64_t *q_staged;      // per segment: its mode and query rows are in shared memory
   uint64_t *q_full;        // per segment: Q is in TMEM
   uint64_t *o_free;        // per segment: O has been read, the exchange is over
   volatile int* abort;
@@ -279,48 +278,53 @@ DF_DEV uint32_t live_scales(uint32_t s, bool is_k, bool live, uint32_t& bits) {
   return s & ~nan;
 }
 
-// Decode a warp's rows of half a tile of K or of V (`slot` of the ring, its
-// first key key0) into `tile`.  All reads come before the first store: the
-// compiler cannot tell that they never meet.
-template <int FMT, bool HALF16>
-DF_DEV void decode_rows(const uint8_t* slot, uint8_t* tile, const DecodeLane& l, bool is_k,
-                        int key0, int lo, int hi, int unit0, uint32_t (&bits)[2]) {
+// A warp's rows of half a tile, as they come out of a ring slot.
+struct Codes {
   uint4 c[2][2];
   uint32_t bytes[2];
+};
+
+DF_DEV void read_codes(Codes& x, const uint8_t* slot, const DecodeLane& l) {
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
-    bytes[o] = *reinterpret_cast<const uint32_t*>(slot + HK * HD + l.row[o] * 4);
+    x.bytes[o] = *reinterpret_cast<const uint32_t*>(slot + HK * HD + l.row[o] * 4);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      c[o][p] = *reinterpret_cast<const uint4*>(slot + (l.src[o] ^ (p * 64)));
+      x.c[o][p] = *reinterpret_cast<const uint4*>(slot + (l.src[o] ^ (p * 64)));
   }
-  const bool edge = key0 < lo || key0 + HK > hi;
-  if (HALF16 && edge) {
+}
+
+// Decode them (first key key0) into `tile`.
+template <int FMT, bool HALF16>
+DF_DEV void decode_rows(Codes& x, uint8_t* tile, const DecodeLane& l, bool is_k, int key0, int lo,
+                        int hi, int unit0, uint32_t (&bits)[2]) {
+  if (HALF16 && (key0 < lo || key0 + HK > hi)) {
 #pragma unroll
     for (int o = 0; o < 2; ++o)
       if (key0 + l.row[o] < lo || key0 + l.row[o] >= hi) {  // codes and scale of zero
         constexpr uint32_t zero = FMT == Q8_INT8 ? 0x80808080u : 0u;
-        c[o][0] = c[o][1] = make_uint4(zero, zero, zero, zero);
-        bytes[o] = 0u;
+        x.c[o][0] = x.c[o][1] = make_uint4(zero, zero, zero, zero);
+        x.bytes[o] = 0u;
       }
   }
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     HalfScales hs;
     if (HALF16)
-      hs = half_scales(bytes[o], unit0);
+      hs = half_scales(x.bytes[o], unit0);
     else
-      bytes[o] = live_scales(bytes[o], is_k, key0 + l.row[o] >= lo && key0 + l.row[o] < hi,
-                             bits[o]);
+      x.bytes[o] = live_scales(x.bytes[o], is_k, key0 + l.row[o] >= lo && key0 + l.row[o] < hi,
+                               bits[o]);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
+      const uint4 c = x.c[o][p];
       uint4 a, b;
       if (HALF16) {
-        half_decode16<FMT>(c[o][p], hs, half_select(l.group[p]), a, b);
+        half_decode16<FMT>(c, hs, half_select(l.group[p]), a, b);
       } else {
-        const float s = bf16_scale((bytes[o] >> (l.group[p] * 8)) & 0xffu);
-        a = bf16_decode8<FMT>(c[o][p].x, c[o][p].y, s);
-        b = bf16_decode8<FMT>(c[o][p].z, c[o][p].w, s);
+        const float s = bf16_scale((x.bytes[o] >> (l.group[p] * 8)) & 0xffu);
+        a = bf16_decode8<FMT>(c.x, c.y, s);
+        b = bf16_decode8<FMT>(c.z, c.w, s);
       }
       const int dst = l.dst[o] ^ (p * (int)HALF);
       *reinterpret_cast<uint4*>(tile + dst) = a;
@@ -329,7 +333,8 @@ DF_DEV void decode_rows(const uint8_t* slot, uint8_t* tile, const DecodeLane& l,
   }
 }
 
-// One segment's tiles: K, then V.
+// One segment's tiles: K, then V.  A slot is free as soon as its codes are in
+// registers, before the tile's stage is: the ring stays in flight.
 template <int FMT, bool HALF16>
 DF_DEV bool decode_segment(const Segment& w, const Mode& mode, const Shared& sm, int* err,
                            int half, int lane, const DecodeLane& l, int& g) {
@@ -339,13 +344,16 @@ DF_DEV bool decode_segment(const Segment& w, const Mode& mode, const Shared& sm,
     for (int kv = 0; kv < 2; ++kv) {
       const bool is_k = kv == 0;
       const int n = 4 * g + 2 * kv + half, slot = n % RING;
-      const bool ok =
-          wait(&sm.ring_full[slot], (n / RING) & 1, sm, err) &&
-          wait(is_k ? &sm.s_full[st] : &sm.o_done[st], ((g >> 1) & 1) ^ 1, sm, err);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      if (!warp_wait(&sm.ring_full[slot], (n / RING) & 1, sm, err)) return false;
+      Codes x;
+      read_codes(x, sm.ring + slot * SLOT, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
+      if (!warp_wait(is_k ? &sm.s_full[st] : &sm.o_done[st], ((g >> 1) & 1) ^ 1, sm, err))
+        return false;
       uint32_t bits[2] = {0u, 0u};
-      decode_rows<FMT, HALF16>(sm.ring + slot * SLOT, (is_k ? sm.k : sm.v) + st * TILE, l, is_k,
-                               t * TK + half * HK, w.lo, w.hi, is_k ? mode.k0 : mode.v0, bits);
+      decode_rows<FMT, HALF16>(x, (is_k ? sm.k : sm.v) + st * TILE, l, is_k, t * TK + half * HK,
+                               w.lo, w.hi, is_k ? mode.k0 : mode.v0, bits);
       if (!HALF16) {
         // The softmax of tile g - 2 has read these marks before PV(g - 2) was
         // issued; K's marks wait for that here.
@@ -356,10 +364,7 @@ DF_DEV bool decode_segment(const Segment& w, const Mode& mode, const Shared& sm,
         if ((bits[0] | bits[1]) != 0u) sm.nan_tile[st] = g;
       }
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.ring_empty[slot]);
-        mbar_arrive(is_k ? &sm.k_full[st] : &sm.v_full[st]);
-      }
+      if (lane == 0) mbar_arrive(is_k ? &sm.k_full[st] : &sm.v_full[st]);
     }
   }
   return true;
@@ -391,7 +396,8 @@ DF_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
       : "memory");
 }
 
-// Lane 0 copies the tiles, every lane its query rows.  On an abort the copies
+// Lane 0 copies the tiles, every lane its query rows; how the segment is
+// decoded goes to the softmax warps with them.  On an abort the copies
 // in flight are still waited for, with a limit: no CTA may leave before they
 // have landed.
 DF_DEV void copy_all(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, bool stage_q,
@@ -403,13 +409,20 @@ DF_DEV void copy_all(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, boo
   bool alive = true;
   while (alive && walk.next(a, p, w)) {
     if (w.t1 == w.t0) continue;
+    // the rows of segment seg - 1 have been read, and the exchange that
+    // followed (of segment seg - 2's O) is over
+    if (seg == 1) alive = warp_wait(sm.q_full, 0, sm, a.err);
+    if (seg >= 2) alive = warp_wait(sm.o_free, seg & 1, sm, a.err);
+    if (!alive) break;
+    if (lane == 0) {
+      const Mode m = mode_of(a.st, w.b, w.h);
+      sm.mode[seg & 1] = make_int4(m.half ? 1 : 0, m.k0, m.v0, 0);
+      if (stage_q)
+        mbar_arrive_expect_tx(sm.q_staged, (uint32_t)w.rows * HD * 2);
+      else
+        mbar_arrive(sm.q_staged);
+    }
     if (stage_q) {
-      // the rows of segment seg - 1 have been read, and the exchange that
-      // followed (of segment seg - 2's O) is over
-      if (seg == 1) alive = warp_wait(sm.q_full, 0, sm, a.err);
-      if (seg >= 2) alive = warp_wait(sm.o_free, seg & 1, sm, a.err);
-      if (!alive) break;
-      if (lane == 0) mbar_arrive_expect_tx(sm.q_staged, (uint32_t)w.rows * HD * 2);
       __syncwarp();
       const uint16_t* q = a.q + (long long)w.b * a.q_seq + (long long)w.h * a.q_head;
       for (int r = lane; r < w.rows; r += 32) {
@@ -446,7 +459,7 @@ DF_DEV void copy_all(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, boo
       while (!mbar_try_wait(&sm.ring_full[i % RING], (i / RING) & 1) &&
              global_ns() - t0 < kWaitLimitNs) {
       }
-    while (stage_q && seg > 0 && !mbar_try_wait(sm.q_staged, (seg - 1) & 1) &&
+    while (seg > 0 && !mbar_try_wait(sm.q_staged, (seg - 1) & 1) &&
            global_ns() - t0 < kWaitLimitNs) {
     }
   }
@@ -460,8 +473,7 @@ DF_DEV void copy_all(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, boo
 DF_DEV uint32_t f16_mask(const Mode& m) { return m.half ? ~((1u << 7) | (1u << 10)) : ~0u; }
 
 DF_DEV void issue_s(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, uint32_t tmem) {
-  uint64_t desc[2];
-  for (int st = 0; st < 2; ++st) desc[st] = sdesc_sw128(smem_u32(sm.k + st * TILE), 16, 1024);
+  const uint64_t desc0 = sdesc_sw128(smem_u32(sm.k), 16, 1024);
   Walk walk(a, p);
   Segment w;
   int g = 0, seg = 0;
@@ -477,10 +489,11 @@ DF_DEV void issue_s(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, uint
         return;
       fence_proxy_async_smem();
       tc_fence_after();
+      const uint64_t desc = desc0 + (uint32_t)(st * (TILE >> 4));  // (in 16-byte units)
 #pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)  // descriptors count 16-byte units
+      for (int kk = 0; kk < HD / 16; ++kk)
         tc_mma_bf16_ta(tmem + (uint32_t)(st * TK), tmem + Q_COL + kk * 8,
-                       desc[st] + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), idesc,
+                       desc + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), idesc,
                        kk > 0 ? 1u : 0u);
       tc_commit(&sm.s_full[st]);
     }
@@ -489,8 +502,7 @@ DF_DEV void issue_s(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, uint
 }
 
 DF_DEV void issue_pv(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, uint32_t tmem) {
-  uint64_t desc[2];
-  for (int st = 0; st < 2; ++st) desc[st] = sdesc_sw128(smem_u32(sm.v + st * TILE), HALF, 1024);
+  const uint64_t desc0 = sdesc_sw128(smem_u32(sm.v), HALF, 1024);
   Walk walk(a, p);
   Segment w;
   int g = 0, seg = 0;
@@ -504,11 +516,11 @@ DF_DEV void issue_pv(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, uin
       fence_proxy_async_smem();
       if (!wait(&sm.p_full[st], (g >> 1) & 1, sm, a.err)) return;
       tc_fence_after();
+      const uint64_t desc = desc0 + (uint32_t)(st * (TILE >> 4));
 #pragma unroll
       for (int kk = 0; kk < TK / 16; ++kk)
         tc_mma_bf16_ta(tmem + O_COL, tmem + (uint32_t)(st * TK) + kk * 8,
-                       desc[st] + ((kk * 16 * 128) >> 4), idesc,
-                       (t > w.t0 || kk > 0) ? 1u : 0u);
+                       desc + ((kk * 16 * 128) >> 4), idesc, (t > w.t0 || kk > 0) ? 1u : 0u);
       tc_commit(&sm.o_done[st]);
     }
     ++seg;
@@ -805,42 +817,55 @@ DF_DEV void finish_segment(const Q8AttnArgs& a, const Segment& w, const Mode& mo
 #pragma unroll
     for (int c = 0; c < COPIES; ++c) sm.row_f[c * RW + at.qr] = f[c] == 0.f ? 0.f : f[c] * scale;
   }
+  // This thread's share of what goes out: four channels of the rows r0, r0 +
+  // 32, ... in every pass.
   float* x = reinterpret_cast<float*>(sm.qx);
-  const int tid = (at.hh * 4 + at.quarter) * 32 + at.lane;
+  constexpr int ITEMS = RW / 32;
+  const int r0 = at.hh * 16 + at.quarter * 4 + (at.lane >> 3), c4 = (at.lane & 7) * 4;
+  size_t to[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int qr = r0 + i * 32;
+    to[i] = qr >= w.rows ? 0
+            : (w.slot >= 0 ? (size_t)w.slot * 128 + qr
+                           : out_row(a, w.b, w.h, w.qt, w.tokens, qr)) * HD + c4;
+  }
 #pragma unroll 1
   for (int c = 0; c < HD / 32; ++c) {
     if (have) {
       float o[16];
       tmem_load<16>(at.trow + O_COL + c * 32 + at.hh * 16, o);
+      float4* d = reinterpret_cast<float4*>(x + at.r * X_LD + at.hh * 16);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[at.r * X_LD + at.hh * 16 + i] = o[i];
+      for (int i = 0; i < 4; ++i)
+        d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     }
     named_bar_sync(1, N);
-    for (int it = tid; it < w.rows * 8; it += N) {
-      const int qr = it >> 3, c4 = (it & 7) * 4;
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int qr = r0 + i * 32;
+      if (qr >= w.rows) continue;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (have) {
 #pragma unroll
         for (int k = 0; k < COPIES; ++k) {
           const float f = sm.row_f[k * RW + qr];
-          const float* y = x + (k * RW + qr) * X_LD + c4;
+          const float4 y = *reinterpret_cast<const float4*>(x + (k * RW + qr) * X_LD + c4);
           if (f != 0.f) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] += f * y[i];
+            o.x += f * y.x;
+            o.y += f * y.y;
+            o.z += f * y.z;
+            o.w += f * y.w;
           }
         }
       }
       const int nan = sm.row_nan[qr];
-      if (((nan >> c) & 1) || (nan & kNanK)) o[0] = o[1] = o[2] = o[3] = nan_f();
-      if (w.slot >= 0) {
-        __stcg(reinterpret_cast<float4*>(a.part_o + ((size_t)w.slot * 128 + qr) * HD + c * 32 +
-                                         c4),
-               make_float4(o[0], o[1], o[2], o[3]));
-      } else {
-        const size_t dst = out_row(a, w.b, w.h, w.qt, w.tokens, qr) * HD + c * 32 + c4;
-        *reinterpret_cast<uint2*>(a.out + dst) =
-            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-      }
+      if (((nan >> c) & 1) || (nan & kNanK)) o.x = o.y = o.z = o.w = nan_f();
+      if (w.slot >= 0)
+        __stcg(reinterpret_cast<float4*>(a.part_o + to[i] + c * 32), o);
+      else
+        *reinterpret_cast<uint2*>(a.out + to[i] + c * 32) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     }
     named_bar_sync(1, N);
   }
@@ -881,13 +906,14 @@ DF_DEV void softmax_all(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm, 
   Mode mode{};
   SoftmaxRow row{};
   auto begin = [&]() {
-    mode = mode_of(a.st, w.b, w.h);
     row = begin_row(a, w, at.qr);
     if (w.t1 == w.t0) return;
-    if (COPIES > 1) {
-      ok = warp_wait(sm.q_staged, staged & 1, sm, a.err) && ok;
-      ++staged;
-    }
+    ok = warp_wait(sm.q_staged, staged & 1, sm, a.err) && ok;
+    const int4 m = sm.mode[staged & 1];
+    mode.half = m.x != 0;
+    mode.k0 = m.y;
+    mode.v0 = m.z;
+    ++staged;
     load_q<COPIES>(a, w, mode, sm, at, row);
     warp_arrive(sm.q_full, lane);
   };
@@ -938,6 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm.q_full = sm.q_staged + 1;
   sm.o_free = sm.q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm.o_free + 1);
+  sm.mode = reinterpret_cast<int4*>(bars + 48);
   sm.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   sm.nan_tile = sm.abort + 1;
   sm.pair = reinterpret_cast<float*>(bars + 64);
