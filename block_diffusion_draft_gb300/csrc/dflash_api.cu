@@ -1240,14 +1240,6 @@ int q8_rows(const dflash_q8_cache* c, const int32_t* host_first, const int32_t* 
   return DFLASH_OK;
 }
 
-// Query tiles of an attention call over an 8-bit cache: as few as hold the
-// block's rows, of near-equal size.
-void q8_tiles(int groups, int q_len, int* tokens, int* tiles) {
-  const int most = 128 / groups;
-  *tiles = (q_len + most - 1) / most;
-  *tokens = (q_len + *tiles - 1) / *tiles;
-}
-
 // Attention of a block over the cached rows (lengths `len`); q and its
 // strides, scale, out and lse are set in `a`.
 int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>& len, int q_len,
@@ -1256,7 +1248,7 @@ int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>
   a.batch = c->batch;
   a.groups = at->g;
   a.q_len = q_len;
-  q8_tiles(at->g, q_len, &a.tile_tokens, &a.n_q_tiles);
+  a.n_q_tiles = (q_len * at->g + kQ8TileRows - 1) / kQ8TileRows;
   a.window = at->cfg.sliding_window;
   a.causal = at->cfg.causal != 0;
   a.part_o = c->part_o;
@@ -1272,7 +1264,7 @@ int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>
   if (!plan_q8_attention(p, c->batch, c->nkv, a.n_q_tiles, c->num_sms))
     return fail(DFLASH_ERR_SHAPE, "too many key tiles");
   TraceScope tr(at, DFLASH_K_ATTN, s);
-  DF_CUDA(launch_q8_attention(c->fmt, a, p, s), "8-bit cache attention launch");
+  DF_CUDA(launch_q8_attention(c->fmt, c->tm_k, a, p, s), "8-bit cache attention launch");
   return DFLASH_OK;
 }
 
@@ -1302,7 +1294,8 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   if (batch <= 0 || capacity_rows <= 0)
     return fail(DFLASH_ERR_ARG, "batch and capacity_rows must be positive");
   if (batch > kMaxBatch) return fail(DFLASH_ERR_SHAPE, "batch above %d", kMaxBatch);
-  if (capacity_rows > (1 << 30)) return fail(DFLASH_ERR_SHAPE, "capacity_rows above 2^30");
+  if ((long long)batch * a->nkv * ((capacity_rows + 127LL) / 128 * 128) >= (1LL << 31))
+    return fail(DFLASH_ERR_SHAPE, "too many cache rows");
   if (format != DFLASH_Q8_E4M3 && format != DFLASH_Q8_INT8)
     return fail(DFLASH_ERR_ARG, "format must be DFLASH_Q8_E4M3 or DFLASH_Q8_INT8");
   if (int r = check_device(a->device)) return r;
@@ -1326,8 +1319,8 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   const size_t codes = rows * 128, scales = rows * 4, slots = q8_attention_slots(c->num_sms);
   const size_t ranges = (size_t)batch * a->nkv * 4 * sizeof(int);
   cudaError_t e = cudaMalloc(&c->data, 2 * (codes + scales) + ranges);
-  if (e == cudaSuccess) e = cudaMalloc(&c->part_o, slots * 128 * 128 * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&c->part_ml, slots * 256 * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->part_o, slots * kQ8TileRows * 128 * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&c->part_ml, slots * 2 * kQ8TileRows * sizeof(float));
   // zeroed: rows past a sequence's end are read with its last tile (and
   // decoded to zero); finished before any other stream can use the cache
   if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales) + ranges);
@@ -1344,6 +1337,10 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   c->st.range = reinterpret_cast<int*>(p + 2 * (codes + scales));
   c->st.n_kv = c->nkv;
   c->st.cap = c->rows;
+  if (make_tmap_bf16_rows(&c->tm_k, c->st.k, (long long)rows, 64, 64) != 0) {
+    dflash_q8_cache_destroy(c);
+    return fail(DFLASH_ERR_CUDA, "tensor map encoding failed");
+  }
   *out = c;
   return DFLASH_OK;
 }

@@ -326,41 +326,47 @@ int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source
 int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
                    cudaStream_t s);
 
+constexpr int kQ8TileRows = 64;
+
 // Attention over an 8-bit cache (attn_q8.cu).  Query row (b, h, g, t) starts
 // at q + b * q_seq + h * q_head + g * q_group + t * q_tok elements.
 struct Q8AttnArgs {
   Q8Store st;
   int batch, groups;
   int q_len;           // block rows per sequence
-  int tile_tokens;     // block rows per query tile
-  int n_q_tiles;       // query tiles per (sequence, kv head)
+  int n_q_tiles;       // query tiles of kQ8TileRows rows per (sequence, kv head)
   int window, causal;  // as AttnArgs
   float scale;         // of a score, in log2 units
   const uint16_t* q;
   long long q_seq, q_head, q_group, q_tok;
   uint16_t* out;       // [B * q_len][n_kv * groups * 128]
   float* lse;          // [B * q_len][n_kv * groups] natural log, or null
-  float* part_o;       // pairs across CTAs: [slot][128 rows][128] fp32
-  float* part_ml;      // [slot][2][128] running max (log2 units) and sum
+  float* part_o;       // pairs across CTAs: [slot][kQ8TileRows][128] fp32
+  float* part_ml;      // [slot][2][kQ8TileRows] reference (log2 units) and sum
   int* err;
 };
 
+constexpr int kQ8MaxCtas = 256;
+
 // Work split of one call: the key tiles of all (sequence, query tile, kv head)
-// pairs in one line, `share` consecutive tiles per CTA.
+// pairs in one line, `share` consecutive places per CTA.
 struct Q8Plan {
   int len[kMaxBatch];        // keys of the sequence
   int lo[kMaxBatch];         // first key any query of the block can see
-  int first[kMaxBatch + 1];  // its first tile in the line
+  int first[kMaxBatch + 1];  // its first place in the line
   int share;
+  uint16_t start[kQ8MaxCtas];  // the sequence that a CTA begins in
 };
 
 constexpr int kQ8MaxSplits = 32;  // CTAs that a pair can lie across
 
-// slots of 128 rows that a plan can need on this GPU
+// partial slots that a plan can need on this GPU
 size_t q8_attention_slots(int num_sms);
 // fills first and share from len and lo; false if there are too many tiles
 bool plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sms);
-int launch_q8_attention(int fmt, const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t s);
+// tm_k: K's codes as rows of 64 bf16 numbers, boxes of 64 rows
+int launch_q8_attention(int fmt, const CUtensorMap& tm_k, const Q8AttnArgs& a, const Q8Plan& p,
+                        cudaStream_t s);
 
 // ------------------------------------------- verification of drafted tokens
 // One call of dflash_verify (verify.cu); strides in elements.
