@@ -1420,7 +1420,8 @@ int dflash_q8_cache_append(dflash_q8_cache* c, const void* k, const void* v,
   if (int r = check_device(c->device)) return r;
   Q8Source src{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), 0, c->d,
                k_row_stride, v_row_stride, 1};
-  DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, static_cast<cudaStream_t>(stream)),
+  DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, c->num_sms,
+                           static_cast<cudaStream_t>(stream)),
           "8-bit cache append launch");
   for (int b = 0; b < c->batch; ++b) c->len[b] += host_n[b];
   return DFLASH_OK;
@@ -1523,7 +1524,8 @@ int dflash_attn_forward_q8(dflash_attn* a, dflash_q8_cache* c, int batch, int q_
                  (long long)c->nkv * most * c->d, (long long)most * c->d, c->d, c->d, 0};
     {
       TraceScope tr(a, DFLASH_K_MISC, s);
-      DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, s), "8-bit cache append launch");
+      DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, c->num_sms, s),
+              "8-bit cache append launch");
     }
     // Q as the projection leaves it: [batch][n_kv][groups][q_len][d], scaled
     Q8AttnArgs qa{};

@@ -322,7 +322,7 @@ struct Q8Source {
 };
 
 int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
-                     cudaStream_t s);
+                     int num_sms, cudaStream_t s);
 int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
                    cudaStream_t s);
 

@@ -8,13 +8,20 @@
 // rows are whole 256-byte runs and those to the codes whole 128-byte lines.
 // When writing, a group's four lanes agree on its largest magnitude with two
 // shuffles.
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace df {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = kThreads / 16;  // (row, kv head) pairs per CTA
+constexpr int kItems = kThreads / 16;  // (row, kv head) pairs that a CTA has in work
+// CTAs of a large append, per SM: four times what runs at a time, so that they do
+// not end together.  32768 rows of 8 KV heads (407 MB) take 84 us, 4.8 TB/s, with
+// 24, 92 us with 6 and 118 us with a CTA per 16 items, each of which then looks
+// at the ranges by itself.
+constexpr int kAppendCtas = 24;
 
 // The (row, kv head) that item `it` of a call stands for: row `local` of
 // sequence b, which is row r of the call's packed rows and row `store` of the
@@ -27,7 +34,7 @@ struct Item {
 
 DF_DEV Item item_of(const Q8Rows& t, const Q8Store& st, long long it) {
   Item w;
-  w.r = it / st.n_kv;
+  w.r = (uint32_t)it / (uint32_t)st.n_kv;  // (a cache has fewer than 2^31 of them)
   w.h = (int)(it - w.r * st.n_kv);
   int lo = 0, hi = t.n;  // off: prefix sums of the sequences' rows
   while (hi - lo > 1) {
@@ -63,19 +70,36 @@ DF_DEV Coded encode8(uint4 x) {
   return r;
 }
 
-// A row's smallest and largest scale byte, over the four groups (zero groups
-// do not count), into the (sequence, kv head)'s range, read beforehand: most
-// rows lie in it already, so an atomic is rare.
-DF_DEV void widen(int* range, int now_lo, int now_hi, uint32_t byte, bool writer) {
-  int lo = byte != 0u ? (int)byte : 255, hi = (int)byte;
+// Smallest and largest scale bytes that a group of 16 lanes has met of K and of
+// V in one (sequence, kv head); zero groups do not count.
+struct Span {
+  int* range;  // of the (sequence, kv head), or null
+  int4 seen;   // this lane's
+  int4 known;  // as the range was when the first row came
+
+  // Into the range.  Only a lane whose span is wider than the range issues
+  // atomics, and looks at the range again before: of the many lanes that find
+  // a range empty at the same time only the first ones need to.
+  DF_DEV void flush(bool writer) {
 #pragma unroll
-  for (int d = 4; d <= 8; d <<= 1) {
-    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+    for (int d = 4; d <= 8; d <<= 1) {
+      seen.x = min(seen.x, __shfl_xor_sync(0xffffffffu, seen.x, d));
+      seen.y = max(seen.y, __shfl_xor_sync(0xffffffffu, seen.y, d));
+      seen.z = min(seen.z, __shfl_xor_sync(0xffffffffu, seen.z, d));
+      seen.w = max(seen.w, __shfl_xor_sync(0xffffffffu, seen.w, d));
+    }
+    if (!writer || range == nullptr) return;
+    auto wider = [&]() {
+      return seen.x < known.x || seen.y > known.y || seen.z < known.z || seen.w > known.w;
+    };
+    if (!wider()) return;
+    known = __ldcg(reinterpret_cast<const int4*>(range));
+    if (seen.x < known.x) atomicMin(range, seen.x);
+    if (seen.y > known.y) atomicMax(range + 1, seen.y);
+    if (seen.z < known.z) atomicMin(range + 2, seen.z);
+    if (seen.w > known.w) atomicMax(range + 3, seen.w);
   }
-  if (writer && lo < now_lo) atomicMin(range, lo);
-  if (writer && hi > now_hi) atomicMax(range + 1, hi);
-}
+};
 
 // Ranges of the sequences whose rows begin anew.
 __global__ void q8_reset_kernel(const __grid_constant__ Q8Store st,
@@ -88,34 +112,51 @@ __global__ void q8_reset_kernel(const __grid_constant__ Q8Store st,
     reinterpret_cast<int4*>(st.range)[i] = make_int4(255, 0, 255, 0);
 }
 
+// A CTA takes `per` items per group of lanes, kItems apart: with a power of two
+// of up to 16 KV heads a group stays with one head, and its span goes to the
+// range once.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
     q8_append_kernel(const __grid_constant__ Q8Store st, const __grid_constant__ Q8Rows t,
-                     const __grid_constant__ Q8Source src) {
+                     const __grid_constant__ Q8Source src, int per) {
   const int lane16 = threadIdx.x & 15;
-  const long long it = (long long)blockIdx.x * kItems + (threadIdx.x >> 4);
-  const bool live = it < (long long)t.off[t.n] * st.n_kv;
-  const Item w = item_of(t, st, live ? it : 0);
-  const long long row = src.packed ? w.r : (long long)w.local;
-  const long long base = (long long)w.b * src.seq_stride + (long long)w.h * src.head_stride +
-                         lane16 * 8;
+  const long long items = (long long)t.off[t.n] * st.n_kv;
+  long long it = (long long)blockIdx.x * per * kItems + (threadIdx.x >> 4);
+  Span span;
+  span.range = nullptr;
+  span.seen = make_int4(255, 0, 255, 0);
+  span.known = span.seen;
   grid_dep_sync();
-  const uint4 k =
-      *reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride);
-  const uint4 v =
-      *reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride);
-  int* range = st.range + ((size_t)w.b * st.n_kv + w.h) * 4;
-  const int4 now = __ldcg(reinterpret_cast<const int4*>(range));
-  const Coded ck = encode8<FMT>(k), cv = encode8<FMT>(v);
-  widen(range, now.x, now.y, ck.byte, live && lane16 == 0);
-  widen(range + 2, now.z, now.w, cv.byte, live && lane16 == 0);
-  if (!live) return;
-  *reinterpret_cast<uint2*>(st.k + w.store * 128 + lane16 * 8) = ck.codes;
-  *reinterpret_cast<uint2*>(st.v + w.store * 128 + lane16 * 8) = cv.codes;
-  if ((lane16 & 3) == 0) {
-    st.ks[w.store * 4 + (lane16 >> 2)] = (uint8_t)ck.byte;
-    st.vs[w.store * 4 + (lane16 >> 2)] = (uint8_t)cv.byte;
+#pragma unroll 2
+  for (int i = 0; i < per; ++i, it += kItems) {
+    const bool live = it < items;
+    const Item w = item_of(t, st, live ? it : 0);
+    const long long row = src.packed ? w.r : (long long)w.local;
+    const long long base = (long long)w.b * src.seq_stride + (long long)w.h * src.head_stride +
+                           lane16 * 8;
+    const uint4 k = *reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride);
+    const uint4 v = *reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride);
+    int* range = st.range + ((size_t)w.b * st.n_kv + w.h) * 4;
+    if (__any_sync(0xffffffffu, live && range != span.range)) {
+      span.flush(lane16 == 0);
+      span.range = live ? range : nullptr;
+      span.seen = make_int4(255, 0, 255, 0);
+      span.known = __ldcg(reinterpret_cast<const int4*>(range));
+    }
+    const Coded ck = encode8<FMT>(k), cv = encode8<FMT>(v);
+    if (!live) continue;
+    if (ck.byte != 0u) span.seen.x = min(span.seen.x, (int)ck.byte);
+    if (cv.byte != 0u) span.seen.z = min(span.seen.z, (int)cv.byte);
+    span.seen.y = max(span.seen.y, (int)ck.byte);
+    span.seen.w = max(span.seen.w, (int)cv.byte);
+    *reinterpret_cast<uint2*>(st.k + w.store * 128 + lane16 * 8) = ck.codes;
+    *reinterpret_cast<uint2*>(st.v + w.store * 128 + lane16 * 8) = cv.codes;
+    if ((lane16 & 3) == 0) {
+      st.ks[w.store * 4 + (lane16 >> 2)] = (uint8_t)ck.byte;
+      st.vs[w.store * 4 + (lane16 >> 2)] = (uint8_t)cv.byte;
+    }
   }
+  span.flush(lane16 == 0);
 }
 
 template <int FMT>
@@ -144,7 +185,7 @@ unsigned blocks_of(const Q8Rows& t, const Q8Store& st) {
 }  // namespace
 
 int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
-                     cudaStream_t s) {
+                     int num_sms, cudaStream_t s) {
   if (t.off[t.n] == 0) return cudaSuccess;
   bool anew = false;
   for (int b = 0; b < t.n; ++b) anew = anew || (t.first[b] == 0 && t.off[b + 1] > t.off[b]);
@@ -153,9 +194,12 @@ int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source
                                      dim3(256), 0, s, st, t);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid(blocks_of(t, st)), block(kThreads);
-  return fmt == Q8_E4M3 ? launch_pdl(q8_append_kernel<Q8_E4M3>, grid, block, 0, s, st, t, src)
-                        : launch_pdl(q8_append_kernel<Q8_INT8>, grid, block, 0, s, st, t, src);
+  const unsigned blocks = blocks_of(t, st);
+  const unsigned per = std::max(1u, blocks / (unsigned)(num_sms * kAppendCtas));
+  const dim3 grid((blocks + per - 1) / per), block(kThreads);
+  return fmt == Q8_E4M3
+             ? launch_pdl(q8_append_kernel<Q8_E4M3>, grid, block, 0, s, st, t, src, (int)per)
+             : launch_pdl(q8_append_kernel<Q8_INT8>, grid, block, 0, s, st, t, src, (int)per);
 }
 
 int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
