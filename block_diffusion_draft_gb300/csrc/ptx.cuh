@@ -393,6 +393,15 @@ DF_DEV void cluster_sync() {
           : "memory");
 }
 
+// the two halves of cluster_sync
+DF_DEV void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+DF_DEV void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // the shared::cluster address of the same shared-memory offset in CTA `rank`
 DF_DEV uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -425,10 +434,8 @@ DF_DEV float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-DF_DEV unsigned long long ld_cluster_u64(uint32_t addr) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
+DF_DEV void st_cluster_u64(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
 // ---------------------------------------------------------------- misc

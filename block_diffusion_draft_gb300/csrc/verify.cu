@@ -22,8 +22,9 @@
 // the rejection itself (a gather of n probabilities), each warp sums its
 // contiguous share of the row, the CTAs exchange their sums through
 // distributed shared memory, and the one warp whose share holds the drawn
-// point goes over it again (from L2) to find the token.  Latency bounds a
-// call of few sequences, HBM one of many.
+// point goes over it again (from L2) to find the step, eight steps' loads at a
+// time, and then the token.  Latency bounds a call of few sequences, HBM one of
+// many.
 #include <algorithm>
 #include <atomic>
 
@@ -35,19 +36,32 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
-constexpr unsigned long long kOne = 1ull << 44;
+// 16 CTAs are the most that this GPU puts into a cluster, beyond the portable 8:
+// one sequence of 15 drafts and 150000 tokens takes 11.6 us, with 8 14.4 us.
+constexpr int kMaxCluster = 16;
 
-// min(max(p, 0), 1) in multiples of 2^-44, cut off below; NaN counts as 0
-DF_DEV unsigned long long fixed(float p) {
-  if (!(p > 0.f)) return 0ull;
-  if (p >= 1.f) return kOne;
-  const uint32_t b = __float_as_uint(p);
-  // p = mant * 2^(field - 150): mant * 2^21 is p * 2^44 for field 127
-  const uint32_t k = 127u - (b >> 23);
-  const unsigned long long m = (unsigned long long)((b & 0x7fffffu) | 0x800000u) << 21;
-  return k > 63u ? 0ull : m >> k;
+// min(max(p, 0), 1) in multiples of 2^-44, cut off below, as hi * 2^22 + lo; NaN
+// counts as 0.  Adding 2 towards zero leaves the multiples of 2^-22 in the
+// mantissa; what is left over is exact, and adding 2^-21 to it leaves its
+// multiples of 2^-44.  (Conversions to 64-bit integers took 35 us, shifts of the
+// mantissa 29 us where this takes 21 us, on 32 sequences of 15 drafts and 150000
+// tokens.)
+struct Fixed {
+  int hi, lo;
+};
+
+DF_DEV Fixed fixed(float p) {
+  p = fminf(fmaxf(p, 0.f), 1.f);
+  const float t = __fadd_rz(p, 2.f);
+  const float rest = __fadd_rn(p, -__fadd_rn(t, -2.f));
+  constexpr float unit = 4.76837158203125e-07f;  // 2^-21
+  Fixed f;
+  f.hi = __float_as_int(t) - 0x40000000;
+  f.lo = __float_as_int(__fadd_rz(rest, unit)) - 0x35000000;
+  return f;
 }
+
+DF_DEV long long whole(int hi, int lo) { return (long long)hi * (1 << 22) + lo; }
 
 template <typename T>
 DF_DEV float prob(const T* p, long long i);
@@ -58,9 +72,10 @@ DF_DEV float prob<uint16_t>(const uint16_t* p, long long i) {
   return __uint_as_float((uint32_t)__ldg(p + i) << 16);
 }
 
-// E consecutive probabilities of a row (16 bytes), zero past its end
+// E = 16 / sizeof(T) probabilities of a row, `by` apart, zero past its end: 16
+// bytes in one load where the row's start is aligned and they are neighbours
 template <typename T, bool VEC>
-DF_DEV void load_row(const T* row, int i, int vocab, float (&x)[16 / sizeof(T)]) {
+DF_DEV void load_row(const T* row, int i, int by, int vocab, float (&x)[16 / sizeof(T)]) {
   constexpr int E = 16 / sizeof(T);
   if (VEC && i + E <= vocab) {
     const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i));
@@ -76,7 +91,7 @@ DF_DEV void load_row(const T* row, int i, int vocab, float (&x)[16 / sizeof(T)])
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = i + e < vocab ? prob<T>(row, i + e) : 0.f;
+    for (int e = 0; e < E; ++e) x[e] = i + e * by < vocab ? prob<T>(row, i + e * by) : 0.f;
   }
 }
 
@@ -90,22 +105,26 @@ struct Row {
 };
 
 template <typename T, bool VEC>
-DF_DEV void weights(const Row<T>& r, int i, int vocab,
+DF_DEV void weights(const Row<T>& r, int i, int by, int vocab,
                     unsigned long long (&w)[16 / sizeof(T)]) {
   constexpr int E = 16 / sizeof(T);
   float x[E];
-  load_row<T, VEC>(r.p, i, vocab, x);
+  load_row<T, VEC>(r.p, i, by, vocab, x);
   if (r.q != nullptr) {
     float y[E];
-    load_row<T, VEC>(r.q, i, vocab, y);
+    load_row<T, VEC>(r.q, i, by, vocab, y);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const long long d = (long long)fixed(x[e]) - (long long)fixed(y[e]);
+      const Fixed f = fixed(x[e]), g = fixed(y[e]);
+      const long long d = whole(f.hi - g.hi, f.lo - g.lo);
       w[e] = d > 0 ? (unsigned long long)d : 0ull;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = i + e == r.out ? 0ull : fixed(x[e]);
+    for (int e = 0; e < E; ++e) {
+      const Fixed f = fixed(x[e]);
+      w[e] = i + e * by == r.out ? 0ull : (unsigned long long)whole(f.hi, f.lo);
+    }
   }
 }
 
@@ -114,27 +133,29 @@ __global__ void __launch_bounds__(kThreads)
     verify_kernel(const __grid_constant__ VerifyArgs a, int cluster) {
   constexpr int E = 16 / sizeof(T), STEP = 32 * E;
   __shared__ unsigned long long warp_sum[2][kWarps];
-  __shared__ unsigned long long cta_sum[2];
+  __shared__ unsigned long long cta_sum[2][kMaxCluster];
   __shared__ int first_bad;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
   const int b = blockIdx.x / cluster;
+  // what a CTA exchanges with its cluster goes to CTAs that must have started
+  if (cluster > 1) cluster_arrive();
   grid_dep_sync();
 
   // the first rejected draft
-  int n = a.n_draft;
-  if (a.seq_drafts != nullptr) n = min(max(__ldg(a.seq_drafts + b), 0), n);
-  if (threadIdx.x == 0) first_bad = n;
-  __syncthreads();
   const T* target = static_cast<const T*>(a.target) + (long long)b * a.target_batch;
   const T* draft = a.draft == nullptr
                        ? nullptr
                        : static_cast<const T*>(a.draft) + (long long)b * a.draft_batch;
   const int* drafts = a.draft_tokens + (long long)b * a.n_draft;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  const float u_sample = __ldg(a.u_sample + b);
+  const int n_seq = a.seq_drafts != nullptr ? __ldg(a.seq_drafts + b) : a.n_draft;
+  if (threadIdx.x == 0) first_bad = a.n_draft;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n_draft; i += kThreads) {
     const int x = __ldg(drafts + i);
     const double u = (double)__ldg(a.u_accept + (long long)b * a.n_draft + i);
-    bool ok = x >= 0 && x < a.vocab;
+    bool ok = x >= 0 && x < a.vocab && i < n_seq;
     if (ok) {
       const double p = (double)prob<T>(target, (long long)i * a.target_row + x);
       const double q = draft == nullptr ? 1.0
@@ -144,6 +165,7 @@ __global__ void __launch_bounds__(kThreads)
     if (!ok) atomicMin(&first_bad, i);
   }
   __syncthreads();
+  const int n = min(max(n_seq, 0), a.n_draft);
   const int k = first_bad;
   int* tokens = a.tokens + (long long)b * (a.n_draft + 1);
   if (rank == 0) {
@@ -166,10 +188,13 @@ __global__ void __launch_bounds__(kThreads)
   // pass 1 only when the difference left no weight at all: the target's row
   for (int pass = 0; pass < 2; ++pass) {
     unsigned long long sum = 0ull;
+    // (the order of a sum does not matter: a step's elements side by side where
+    // they are loaded one by one)
+    const int first = VEC ? lane * E : lane, by = VEC ? 1 : 32;
 #pragma unroll 4
     for (int s = s0; s < s1; ++s) {
       unsigned long long w[E];
-      weights<T, VEC>(r, s * STEP + lane * E, a.vocab, w);
+      weights<T, VEC>(r, s * STEP + first, by, a.vocab, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) sum += w[e];
     }
@@ -177,24 +202,30 @@ __global__ void __launch_bounds__(kThreads)
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane == 0) warp_sum[pass][warp] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      unsigned long long t = 0ull;
-      for (int i = 0; i < kWarps; ++i) t += warp_sum[pass][i];
-      cta_sum[pass] = t;
+    if (cluster > 1 && pass == 0) cluster_wait();
+    if (warp == 0) {
+      unsigned long long t = lane < kWarps ? warp_sum[pass][lane] : 0ull;
+#pragma unroll
+      for (int d = kWarps / 2; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+      // to every CTA of the cluster, this one among them
+      if (cluster == 1) {
+        if (lane == 0) cta_sum[pass][0] = t;
+      } else {
+        if (lane < cluster)
+          st_cluster_u64(cluster_map(smem_u32(&cta_sum[pass][rank]), (uint32_t)lane), t);
+      }
     }
-    unsigned long long before = 0ull, total = 0ull;
     if (cluster > 1) {
       __syncwarp();
       cluster_sync();
-      for (int c = 0; c < cluster; ++c) {
-        const unsigned long long t =
-            ld_cluster_u64(cluster_map(smem_u32(&cta_sum[pass]), (uint32_t)c));
-        if (c < rank) before += t;
-        total += t;
-      }
     } else {
       __syncthreads();
-      total = cta_sum[pass];
+    }
+    unsigned long long before = 0ull, total = 0ull;
+    for (int c = 0; c < cluster; ++c) {
+      const unsigned long long t = cta_sum[pass][c];
+      if (c < rank) before += t;
+      total += t;
     }
     if (total == 0ull && (r.q != nullptr || r.out >= 0)) {
       r.q = nullptr;
@@ -205,53 +236,78 @@ __global__ void __launch_bounds__(kThreads)
       if (rank == 0 && threadIdx.x == 0) tokens[k] = -1;
       break;
     }
-    const float u = __ldg(a.u_sample + b);
+    const float u = u_sample;
     unsigned long long t = u > 0.f ? (unsigned long long)((double)min(u, 1.f) * (double)total) : 0ull;
     t = min(t, total - 1ull);
     for (int i = 0; i < warp; ++i) before += warp_sum[pass][i];
     if (t >= before && t - before < sum) {
-      // the drawn point lies in this warp's share: the first token whose
-      // cumulative weight exceeds it
-      for (int s = s0; s < s1; ++s) {
-        unsigned long long w[E], own = 0ull;
-        const int i = s * STEP + lane * E;
-        weights<T, VEC>(r, i, a.vocab, w);
+      // the drawn point lies in this warp's share: the step that holds it, and
+      // there the first token whose cumulative weight exceeds it
+      constexpr int AHEAD = 8;
+      int step = s0;
+      for (bool found = false; !found; ) {
+        unsigned long long own[AHEAD];
 #pragma unroll
-        for (int e = 0; e < E; ++e) own += w[e];
-        unsigned long long upto = own;
+        for (int j = 0; j < AHEAD; ++j) {
+          own[j] = 0ull;
+          if (step + j < s1) {
+            unsigned long long w[E];
+            weights<T, VEC>(r, (step + j) * STEP + first, by, a.vocab, w);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const unsigned long long o = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += o;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, before + upto > t);
-        if (over != 0u) {
-          if (lane == __ffs(over) - 1) {
-            unsigned long long c = before + upto - own;
-            int e = 0;
-#pragma unroll
-            for (int f = 0; f < E - 1; ++f) {
-              c += w[f];
-              if (c <= t) e = f + 1;
-            }
-            tokens[k] = i + e;
+            for (int e = 0; e < E; ++e) own[j] += w[e];
           }
-          break;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+          for (int j = 0; j < AHEAD; ++j) own[j] += __shfl_xor_sync(0xffffffffu, own[j], d);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (found) continue;
+          if (t < before + own[j] || step + 1 >= s1) {
+            found = true;
+          } else {
+            before += own[j];
+            ++step;
+          }
+        }
+      }
+      unsigned long long w[E], own = 0ull;
+      const int i = step * STEP + lane * E;
+      weights<T, VEC>(r, i, 1, a.vocab, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) own += w[e];
+      unsigned long long upto = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, before + upto > t);
+      if (over != 0u && lane == __ffs(over) - 1) {
+        unsigned long long c = before + upto - own;
+        int e = 0;
+#pragma unroll
+        for (int f = 0; f < E - 1; ++f) {
+          c += w[f];
+          if (c <= t) e = f + 1;
+        }
+        tokens[k] = i + e;
       }
     }
     break;
-  }
-  if (cluster > 1) {
-    // no CTA leaves while another may still read its sum
-    __syncwarp();
-    cluster_sync();
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_t(const VerifyArgs& a, int cluster, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  if (!done_on_device(done)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        verify_kernel<T, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    mark_device(done);
+  }
   return launch_pdl_cluster(verify_kernel<T, VEC>, dim3((unsigned)(a.batch * cluster)),
                             dim3(kThreads), 0, s, (unsigned)cluster, a, cluster);
 }
@@ -259,11 +315,12 @@ cudaError_t launch_t(const VerifyArgs& a, int cluster, cudaStream_t s) {
 }  // namespace
 
 int launch_verify(const VerifyArgs& a, int bf16, int num_sms, cudaStream_t s) {
-  // CTAs per sequence: enough for the whole GPU, as long as a warp keeps a
-  // step of 32 16-byte loads
+  // CTAs per sequence: as many as run at a time (two per SM), as long as a
+  // warp keeps a step of 32 16-byte loads (128 sequences of 50001 tokens in two
+  // waves of four CTAs each took 26 us, in one of two 21 us)
   const int step = 32 * (bf16 ? 8 : 4);
   int cluster = 1;
-  while (cluster < kMaxCluster && (long long)a.batch * cluster < 2LL * num_sms &&
+  while (cluster < kMaxCluster && (long long)a.batch * cluster * 2 <= 2LL * num_sms &&
          (long long)cluster * kWarps * step < a.vocab)
     cluster *= 2;
   const size_t size = bf16 ? 2 : 4;
