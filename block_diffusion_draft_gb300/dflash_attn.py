@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from array import array
 from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_void_p
 from typing import Dict, Optional, Sequence, Tuple
 
@@ -156,34 +157,35 @@ def _stream(dev: torch.device):
 
 
 def _int32_array(xs: Sequence[int]):
-    arr = (c_int32 * len(xs))(*[int(x) for x in xs])
-    return arr
+    try:
+        return (c_int32 * len(xs)).from_buffer(array("i", xs))
+    except TypeError:  # numbers that are not integers by type
+        return (c_int32 * len(xs))(*[int(x) for x in xs])
 
 
-class _Current:
-    """Makes ``device`` current around a library call and gives its current
-    stream, as torch.cuda.device and torch.cuda.current_stream do, in a tenth of
-    their time: the calls below take less of it than those two together."""
-    __slots__ = ("index", "before")
-
-    def __init__(self, device: torch.device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch._C._cuda_getDevice()
-        if self.index is None:
-            self.index = self.before
-        elif self.index != self.before:
-            torch._C._cuda_setDevice(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *_):
-        if self.index != self.before:
-            torch._C._cuda_setDevice(self.before)
+def _call(device: torch.device, f, *args) -> None:
+    """f(*args, stream) with ``device`` current and its current stream, as under
+    torch.cuda.device and torch.cuda.current_stream, in a tenth of their time:
+    the small calls of a serving step take less of it than those two."""
+    before = torch._C._cuda_getDevice()
+    index = device.index
+    if index is None or index == before:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(before))
+    else:
+        torch._C._cuda_setDevice(index)
+        try:
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+        finally:
+            torch._C._cuda_setDevice(before)
+    if rc != 0:
+        check(rc)
 
 
-def _require(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device) -> None:
-    """A dense tensor of this type on this device."""
+def _require(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device,
+             shape: Optional[tuple] = None) -> None:
+    """A dense tensor of this type (and shape) on this device."""
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype or not t.is_cuda or (
             device.index is not None and t.get_device() != device.index):
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
@@ -296,16 +298,16 @@ class DFlashAttention:
         after norm and RoPE) over the rows an 8-bit cache holds.  Returns (out
         like q, lse [B, q_len, n_heads] fp32, natural log; a row that sees no
         key has out 0 and lse -inf)."""
-        if q.dim() != 4 or q.shape[0] != cache.batch or q.shape[2:] != (self.n_heads,
-                                                                        self.head_dim):
+        shape = q.shape
+        if len(shape) != 4 or shape[0] != cache.batch or shape[2] != self.n_heads or (
+                shape[3] != self.head_dim):
             raise ValueError(f"q must be [{cache.batch}, q_len, {self.n_heads}, "
-                             f"{self.head_dim}], got {list(q.shape)}")
+                             f"{self.head_dim}], got {list(shape)}")
         _require("q", q, torch.bfloat16, self.device)
         out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
-        with _Current(self.device) as stream:
-            check(lib().dflash_q8_attn_core(self.handle, cache.handle, q.shape[0], q.shape[1],
-                                            q.data_ptr(), out.data_ptr(), lse.data_ptr(), stream))
+        lse = q.new_empty(shape[:3], dtype=torch.float32)
+        _call(self.device, lib().dflash_q8_attn_core, self.handle, cache.handle, shape[0],
+              shape[1], q.data_ptr(), out.data_ptr(), lse.data_ptr())
         return out, lse
 
     def forward_q8(self, cache: "Q8Cache", noise: torch.Tensor,
@@ -331,10 +333,8 @@ class DFlashAttention:
         elif out.shape != noise.shape:
             raise ValueError("out must have the shape of noise")
         _require("out", out, torch.bfloat16, self.device)
-        with _Current(self.device) as stream:
-            check(lib().dflash_attn_forward_q8(
-                self.handle, cache.handle, B, q_len, _p(noise), _p(th),
-                _int32_array(n_ctx), _p(positions), _p(out), stream))
+        _call(self.device, lib().dflash_attn_forward_q8, self.handle, cache.handle, B, q_len,
+              noise.data_ptr(), _p(th), _int32_array(n_ctx), positions.data_ptr(), out.data_ptr())
         return out
 
     def forward_packed(self, noise: torch.Tensor, target_hidden: torch.Tensor,
@@ -561,9 +561,8 @@ class Q8Cache:
             if rows > 0 and not dense:
                 raise ValueError(f"{name}: a row's heads must be dense")
             strides.append(s[0] if rows > 1 else a.n_kv_heads * a.head_dim)
-        with _Current(a.device) as stream:
-            check(lib().dflash_q8_cache_append(self.handle, k.data_ptr(), v.data_ptr(),
-                                               strides[0], strides[1], _int32_array(n), stream))
+        _call(a.device, lib().dflash_q8_cache_append, self.handle, k.data_ptr(), v.data_ptr(),
+              strides[0], strides[1], _int32_array(n))
 
     def read(self, first: Optional[Sequence[int]] = None, n: Optional[Sequence[int]] = None):
         """K and V [sum n, n_kv, d] bf16 of rows first[b] .. first[b] + n[b] - 1
@@ -574,10 +573,9 @@ class Q8Cache:
             n = [length - f for length, f in zip(self.lengths(), first)]
         shape = (max(0, sum(_counts("n", n, self.batch))), a.n_kv_heads, a.head_dim)
         k = torch.empty(shape, device=a.device, dtype=torch.bfloat16)
-        v = torch.empty(shape, device=a.device, dtype=torch.bfloat16)
-        with _Current(a.device) as stream:
-            check(lib().dflash_q8_cache_read(self.handle, _int32_array(first), _int32_array(n),
-                                             k.data_ptr(), v.data_ptr(), stream))
+        v = torch.empty_like(k)
+        _call(a.device, lib().dflash_q8_cache_read, self.handle, _int32_array(first),
+              _int32_array(n), k.data_ptr(), v.data_ptr())
         return k, v
 
     def close(self) -> None:
@@ -609,36 +607,38 @@ def verify_draft(draft_tokens: torch.Tensor, draft_probs: Optional[torch.Tensor]
     V, dev, dt = target_probs.shape[2], target_probs.device, target_probs.dtype
     if dt not in (torch.float32, torch.bfloat16):
         raise ValueError("probabilities must be float32 or bfloat16")
-    if dev.type != "cuda":
+    if not target_probs.is_cuda:
         raise ValueError("the library runs on CUDA devices only")
-    shapes = [("target_probs", target_probs, (B, D + 1, V)),
-              ("draft_probs", draft_probs, (B, D, V)), ("u_accept", u_accept, (B, D)),
-              ("u_sample", u_sample, (B,)), ("n_draft", n_draft, (B,))]
-    for name, t, shape in shapes:
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    for name, t, want in (("draft_tokens", draft_tokens, torch.int32),
-                          ("u_accept", u_accept, torch.float32),
-                          ("u_sample", u_sample, torch.float32),
-                          ("n_draft", n_draft, torch.int32)):
-        if t is not None:
-            _require(name, t, want, dev)
-    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if t is not None:
-            if t.dtype != dt or t.device != dev:
-                raise ValueError(f"{name} must be {dt} on {dev}, got {t.dtype} on {t.device}")
-            if t.numel() and t.stride(2) != 1 and V > 1:
-                raise ValueError(f"{name}: a row's values must be dense")
-    q = draft_probs
-    accepted = torch.empty(B, device=dev, dtype=torch.int32)
-    tokens = torch.empty(B, D + 1, device=dev, dtype=torch.int32)
-    with _Current(dev) as stream:
-        check(lib().dflash_verify(
-            B, D, V, DFLASH_BF16 if dt == torch.bfloat16 else DFLASH_FP32, _p(draft_tokens),
-            _p(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
-            _p(target_probs), target_probs.stride(0), target_probs.stride(1), _p(u_accept),
-            _p(u_sample), _p(n_draft), accepted.data_ptr(), tokens.data_ptr(), stream))
+    _require("draft_tokens", draft_tokens, torch.int32, dev)
+    _require("u_accept", u_accept, torch.float32, dev, (B, D))
+    _require("u_sample", u_sample, torch.float32, dev, (B,))
+    if n_draft is not None:
+        _require("n_draft", n_draft, torch.int32, dev, (B,))
+    q, q_strides = None, (0, 0)
+    if draft_probs is not None:
+        q_strides = _probabilities("draft_probs", draft_probs, dt, dev, (B, D, V))
+        q = draft_probs.data_ptr()
+    p_strides = _probabilities("target_probs", target_probs, dt, dev, (B, D + 1, V))
+    accepted = u_sample.new_empty((B,), dtype=torch.int32)
+    tokens = u_sample.new_empty((B, D + 1), dtype=torch.int32)
+    _call(dev, lib().dflash_verify, B, D, V, DFLASH_BF16 if dt == torch.bfloat16 else DFLASH_FP32,
+          draft_tokens.data_ptr(), q, q_strides[0], q_strides[1], target_probs.data_ptr(),
+          p_strides[0], p_strides[1], u_accept.data_ptr(), u_sample.data_ptr(), _p(n_draft),
+          accepted.data_ptr(), tokens.data_ptr())
     return accepted, tokens
+
+
+def _probabilities(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device,
+                   shape: Tuple[int, int, int]) -> Tuple[int, ...]:
+    """The strides of a tensor of rows of probabilities, each row dense."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    strides = t.stride()
+    if strides[2] != 1 and shape[2] > 1 and t.numel():
+        raise ValueError(f"{name}: a row's values must be dense")
+    return strides
 
 
 class KVGroup:
