@@ -181,13 +181,17 @@ def _call(device: torch.device, f, *args) -> None:
         check(rc)
 
 
+def _on(t: torch.Tensor, device: torch.device) -> bool:
+    index = t.get_device()  # -1: not on a CUDA device
+    return index == device.index or (device.index is None and index >= 0)
+
+
 def _require(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch.device,
              shape: Optional[tuple] = None) -> None:
     """A dense tensor of this type (and shape) on this device."""
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda or (
-            device.index is not None and t.get_device() != device.index):
+    if t.dtype is not dtype or not _on(t, device):
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -552,8 +556,7 @@ class Q8Cache:
         for name, t in (("k", k), ("v", v)):
             if t.shape != shape:
                 raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-            if t.dtype != torch.bfloat16 or not t.is_cuda or (
-                    a.device.index is not None and t.get_device() != a.device.index):
+            if t.dtype is not torch.bfloat16 or not _on(t, a.device):
                 raise ValueError(f"{name} must be bfloat16 on {a.device}, "
                                  f"got {t.dtype} on {t.device}")
             s = t.stride()
@@ -633,7 +636,7 @@ def _probabilities(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch
     """The strides of a tensor of rows of probabilities, each row dense."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or not _on(t, device):
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     strides = t.stride()
     if strides[2] != 1 and shape[2] > 1 and t.numel():
