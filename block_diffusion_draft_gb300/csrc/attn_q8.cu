@@ -236,7 +236,7 @@ struct SegmentTable {
   int n, t0, rows, slot;       // n: tiles, -1 behind the last segment
   int lo, hi, lo_all, hi_all;
   int same, half, k0, v0;
-  int uneven;                  // the rows' scores have scales sc, not `scale`
+  int uneven;                  // the rows' scores have scales sc, not `scale`, or may be large
   float scale;                 // of a score, in log2 units
   int top[4], low[4];          // exponents of the rows, per warp
   int2 seen[QR];               // keys a row sees
@@ -266,7 +266,7 @@ struct Shared {
                            // are free
   uint64_t *p_full;        // P(g) written, and S(g) read
   uint64_t *o_done;        // PV(g) complete
-  uint64_t *o_last;        // by segment: its last PV complete
+  uint64_t *o_last;        // by segment, of those with tiles: its last PV complete
   uint64_t *l_full;        // by segment: the softmax is through, its m and sums written
   uint64_t *q_raw;         // by segment: its query rows and what is known of them
   uint64_t *q_full;        // by segment: its table and Q tile are complete
@@ -668,7 +668,7 @@ DF_DEV void fetch_queries(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm
     if (real) {
 #pragma unroll
       for (int c = 0; c < 16; ++c)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                          smem_u32(q_chunk(sm, seg, row, c))),
                      "l"(q + c * 8)
                      : "memory");
@@ -753,7 +753,8 @@ DF_DEV void convert_queries(const Q8AttnArgs& a, const Shared& sm, int seg, int 
     tab.nan[row] = finite ? 0 : (int)kNanK;
   }
   if (warp == 0 && lane == 0) {
-    tab.uneven = half && low < top - 10 ? 1 : 0;
+    // |S| < 2^35, so that scale <= 2^-15 keeps scores below 2^20
+    tab.uneven = !half || low < top - 10 || scale_of(top) > 3.0517578125e-05f ? 1 : 0;
     tab.scale = scale_of(top);
   }
   if (half || !finite) {
@@ -907,6 +908,8 @@ DF_DEV void store_columns8(uint32_t col, const float* v) {
       : "memory");
 }
 
+DF_DEV float score_of(float s, float scale) { return fminf(__fmul_rn(s, scale), 3.4028235e38f); }
+
 // largest of the warp's x
 DF_DEV float warp_max(float x) {
   float y;
@@ -980,8 +983,10 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
     };
     auto relate = [&]() {
       if (uneven) {
+        // not fused: the largest score becomes its row's reference exactly,
+        // however large it is
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) v[i] = __fmaf_rn(v[i], tab.sc[at.query(i)], off[i]);
+        for (int i = 0; i < NQ; ++i) v[i] = __fadd_rn(score_of(v[i], tab.sc[at.query(i)]), off[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < NQ; i += 2) {
@@ -1019,7 +1024,7 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
           const float x = warp_max(v[i]);
           if (at.lane == i) highest = x;
         }
-        if (at.lane < NQ) sm.top[at.quarter * QR + mine] = highest * tab.sc[mine];
+        if (at.lane < NQ) sm.top[at.quarter * QR + mine] = score_of(highest, tab.sc[mine]);
         softmax_sync();
         if (at.tid < QR) {
           const int q = at.tid;
@@ -1135,8 +1140,9 @@ DF_DEV float row_lse(float M, float L, bool half) {
 // A segment's rows out of TMEM, to the output or unnormalised to the segment's
 // partial slot, by four warps (thread = channel) while the softmax is at the
 // next segment.  Lane i works out what queries i and i + 32 need.
+// o_phase: bit i is the phase of o_last[i].
 DF_DEV void write_rows(const Q8AttnArgs& a, const Shared& sm, uint32_t tmem, int seg, int quarter,
-                       int lane) {
+                       int lane, uint32_t& o_phase) {
   const int st = seg & 1;
   const uint32_t phase = (seg >> 1) & 1;
   const SegmentTable& tab = sm.table(seg);
@@ -1164,7 +1170,10 @@ DF_DEV void write_rows(const Q8AttnArgs& a, const Shared& sm, uint32_t tmem, int
       }
     }
   }
-  if (n > 0) ok = warp_wait(&sm.o_last[st], phase, sm, a.err) && ok;
+  if (n > 0) {
+    ok = warp_wait(&sm.o_last[st], (o_phase >> st) & 1, sm, a.err) && ok;
+    o_phase ^= 1u << st;
+  }
   tc_fence_after();
   const uint32_t col = tmem + ((uint32_t)(quarter * 32) << 16) + O_COL + st * QR;
   const int d = quarter * 32 + lane;
@@ -1198,6 +1207,7 @@ DF_DEV void convert_and_write(const Q8AttnArgs& a, const Shared& sm, uint32_t tm
                               int lane) {
   int ready = 0;     // segments converted
   bool more = true;  // none seen without one
+  uint32_t o_phase = 0u;
   for (int seg = 0;; ++seg) {
     for (; more && ready <= seg + 1; ++ready) {
       if (!all_of(2, 128, patient_wait(&sm.q_raw[ready & 1], (ready >> 1) & 1, sm, a.err)))
@@ -1208,7 +1218,7 @@ DF_DEV void convert_and_write(const Q8AttnArgs& a, const Shared& sm, uint32_t tm
       if (lane == 0) mbar_arrive(&sm.q_full[ready & 1]);
     }
     if (!more && seg == ready - 1) return;
-    write_rows(a, sm, tmem, seg, warp, lane);
+    write_rows(a, sm, tmem, seg, warp, lane, o_phase);
   }
 }
 
@@ -1418,7 +1428,7 @@ bool plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sm
     const int n = tiles_of(p, b);
     longest = std::max(longest, n);
     total += (long long)(n + kPairCost) * n_kv * n_q_tiles;
-    if (total >= (1LL << 31) - 1) return false;
+    if (total >= (1LL << 30)) return false;
   }
   p.first[batch] = (int)total;
   p.share = (int)std::max<long long>((total + num_sms - 1) / num_sms,

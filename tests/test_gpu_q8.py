@@ -354,6 +354,81 @@ def test_scales_far_apart(fmt):
         check_attention(a, cache, q, out, lse, ck, cv, [n], 0, True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_query_rows_far_apart(fmt):
+    """Queries of one tile whose magnitudes lie 2^-60 to 2^100 apart, zero rows
+    and rows with infinities and NaN among them: no row's result depends on
+    another's."""
+    for n_heads, q_len in ((4, 16), (7, 5)):
+        a = layer(n_heads, 1)
+        n = 300
+        cache = Q8Cache(a, 1, n, fmt)
+        k, v = rows(n, 1, 1).cuda(), rows(n, 1, 2).cuda()
+        cache.append(k, v, [n])
+        q = rows(q_len, n_heads, 3, 0.2)
+        for i, e in enumerate((-60, -30, -11, -10, -9, 0, 5, 30, 100)):
+            q[i % q_len, i % n_heads] *= 2.0 ** e
+        q[1, 2] = 0
+        q[2, 0, 5], q[3, 1, 127], q[4, 2, 0] = math.nan, math.inf, -math.inf
+        out, lse = a.q8_core(cache, q[None].cuda())
+        ck, cv = cache.read()
+        for t, h in ((2, 0), (3, 1), (4, 2)):
+            assert bool(out[0, t, h].isnan().all()) and bool(lse[0, t, h].isnan())
+            q[t, h], out[0, t, h], lse[0, t, h] = 0, 0, 0
+        whole = torch.ones(q_len, n_heads, dtype=torch.bool)
+        for t, h in ((2, 0), (3, 1), (4, 2)):
+            whole[t, h] = False
+        assert bool(out[0][whole.cuda()].isfinite().all())
+        ref, rl, tol, noise = bounds(T.f64(q), T.f64(ck), T.f64(cv), 0, False)
+        assert np.all((np.abs(T.f64(out[0]) - ref) <= tol)[whole.numpy()])
+        diff = np.abs(T.f64(lse[0]) - rl)[whole.numpy()]
+        assert np.all(diff <= (noise + 2.0 ** -21 * np.abs(rl))[whole.numpy()])
+
+
+@pytest.mark.parametrize("n_heads,n_kv,q_len,counts", [
+    (2, 1, 1, [0] * 300), (8, 8, 3, [0, 0, 0, 1] * 40), (2, 2, 2, [i % 3 for i in range(512)]),
+    (4, 2, 1, [0, 0, 0, 130, 0, 0, 0, 0, 257, 1] * 12), (4, 1, 40, [0, 5, 0, 0, 129] * 9)])
+def test_many_short_and_empty_sequences(n_heads, n_kv, q_len, counts):
+    """Many segments to a block, runs of them without a key."""
+    a = layer(n_heads, n_kv)
+    cache = Q8Cache(a, len(counts), 300, "int8")
+    k, v = rows(sum(counts), n_kv, 1).cuda(), rows(sum(counts), n_kv, 2).cuda()
+    cache.append(k, v, counts)
+    q = rows(len(counts) * q_len, n_heads, 3, 0.2).view(-1, q_len, n_heads, 128).cuda()
+    out, lse = a.q8_core(cache, q)
+    ck, cv = cache.read()
+    check_attention(a, cache, q, out, lse, ck, cv, counts, 0, False)
+    assert a.device_error() == 0
+
+
+@pytest.mark.parametrize("n_heads,n_kv,n", [(8, 8, 16000), (3, 3, 45000)])
+def test_a_large_append_is_many_small_ones(n_heads, n_kv, n):
+    """Codes, scales and what the attention makes of them."""
+    a = layer(n_heads, n_kv)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn(n, n_kv, 128, device="cuda", generator=g).bfloat16()
+    v = torch.randn(n, n_kv, 128, device="cuda", generator=g).bfloat16()
+    k[n - 3, 1] *= 2.0 ** 6  # the largest scale, met once
+    v[777, 0] *= 2.0 ** -9
+    k[5000:5100] = 0
+    once, often = Q8Cache(a, 2, n, "int8"), Q8Cache(a, 2, n, "int8")
+    m = n // 3
+    once.append(k, v, [n - m, m])
+    for i in range(0, m, 1000):
+        j = min(i + 1000, m)
+        at = torch.cat([torch.arange(i, j), n - m + torch.arange(i, j)]).cuda()
+        often.append(k[at], v[at], [j - i, j - i])
+    for i in range(m, n - m, 1000):
+        j = min(i + 1000, n - m)
+        often.append(k[i:j], v[i:j], [j - i, 0])
+    assert once.lengths() == often.lengths()
+    for x, y in zip(storage(once), storage(often)):
+        assert torch.equal(x, y)
+    q = torch.randn(2, 2, n_heads, 128, device="cuda", generator=g).bfloat16()
+    for x, y in zip(a.q8_core(once, q), a.q8_core(often, q)):
+        assert torch.equal(x, y) and bool(x.isfinite().all())
+
+
 def test_nan_through_split_units():
     a = layer(2, 1)
     n = 6000
