@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kThreads)
     const long long row = src.packed ? w.r : (long long)w.local;
     const long long base = (long long)w.b * src.seq_stride + (long long)w.h * src.head_stride +
                            lane16 * 8;
-    const uint4 k = *reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride);
-    const uint4 v = *reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride);
+    const uint4 k = __ldcg(reinterpret_cast<const uint4*>(src.k + base + row * src.k_row_stride));
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src.v + base + row * src.v_row_stride));
     int* range = st.range + ((size_t)w.b * st.n_kv + w.h) * 4;
     if (__any_sync(0xffffffffu, live && range != span.range)) {
       span.flush(lane16 == 0);

@@ -66,10 +66,10 @@ DF_DEV long long whole(int hi, int lo) { return (long long)hi * (1 << 22) + lo; 
 template <typename T>
 DF_DEV float prob(const T* p, long long i);
 template <>
-DF_DEV float prob<float>(const float* p, long long i) { return __ldg(p + i); }
+DF_DEV float prob<float>(const float* p, long long i) { return __ldcg(p + i); }
 template <>
 DF_DEV float prob<uint16_t>(const uint16_t* p, long long i) {
-  return __uint_as_float((uint32_t)__ldg(p + i) << 16);
+  return __uint_as_float((uint32_t)__ldcg(p + i) << 16);
 }
 
 // E = 16 / sizeof(T) probabilities of a row, `by` apart, zero past its end: 16
@@ -78,7 +78,7 @@ template <typename T, bool VEC>
 DF_DEV void load_row(const T* row, int i, int by, int vocab, float (&x)[16 / sizeof(T)]) {
   constexpr int E = 16 / sizeof(T);
   if (VEC && i + E <= vocab) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i));
+    const uint4 w = __ldcg(reinterpret_cast<const uint4*>(row + i));
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(kThreads)
                        ? nullptr
                        : static_cast<const T*>(a.draft) + (long long)b * a.draft_batch;
   const int* drafts = a.draft_tokens + (long long)b * a.n_draft;
-  const float u_sample = __ldg(a.u_sample + b);
-  const int n_seq = a.seq_drafts != nullptr ? __ldg(a.seq_drafts + b) : a.n_draft;
+  const float u_sample = __ldcg(a.u_sample + b);
+  const int n_seq = a.seq_drafts != nullptr ? __ldcg(a.seq_drafts + b) : a.n_draft;
   if (threadIdx.x == 0) first_bad = a.n_draft;
   __syncthreads();
   for (int i = threadIdx.x; i < a.n_draft; i += kThreads) {
-    const int x = __ldg(drafts + i);
-    const double u = (double)__ldg(a.u_accept + (long long)b * a.n_draft + i);
+    const int x = __ldcg(drafts + i);
+    const double u = (double)__ldcg(a.u_accept + (long long)b * a.n_draft + i);
     bool ok = x >= 0 && x < a.vocab && i < n_seq;
     if (ok) {
       const double p = (double)prob<T>(target, (long long)i * a.target_row + x);
@@ -171,13 +171,13 @@ __global__ void __launch_bounds__(kThreads)
   if (rank == 0) {
     if (threadIdx.x == 0) a.accepted[b] = k;
     for (int i = threadIdx.x; i <= a.n_draft; i += kThreads)
-      if (i != k) tokens[i] = i < k ? __ldg(drafts + i) : -1;
+      if (i != k) tokens[i] = i < k ? __ldcg(drafts + i) : -1;
   }
 
   Row<T> r;
   r.p = target + (long long)k * a.target_row;
   r.q = k < n && draft != nullptr ? draft + (long long)k * a.draft_row : nullptr;
-  r.out = k < n && draft == nullptr ? __ldg(drafts + k) : -1;
+  r.out = k < n && draft == nullptr ? __ldcg(drafts + k) : -1;
   // this warp's share of the row: whole steps, in order
   const int shares = cluster * kWarps;
   const int steps = (a.vocab + STEP - 1) / STEP;
