@@ -32,9 +32,9 @@
 //   warps 16-23  decode: K from the ring into TMEM, V into the tensor core's
 //                128-byte-swizzled layout in shared memory, two stages each
 //   warp 24      TMEM allocator; issues S^T(g) and O^T
-//   warp 25      copies codes (K by TMA, swizzled, because a thread reads a
-//                row of its own; V in bulk) and scales: a slot of the ring has
-//                half of K(g) and half of V(g - 1)
+//   warp 25      copies codes (by TMA, swizzled, because a thread reads a row of
+//                its own) and scales: a slot of the ring has half of K(g) and
+//                half of V(g - 1)
 //   warps 26-27  the next segment's queries and tables
 //   warps 28-31  those queries to the products' type; the last segment's O out
 //
@@ -71,7 +71,7 @@ constexpr int kWarpCopy = kWarpMma + 1, kWarpQ = kWarpMma + 2;  // (and the next
 constexpr int kWarpOut = kWarpQ + 2;
 constexpr int kThreads = (kWarpOut + 4) * 32;
 // registers per thread: 64 at launch, and the same total after the split
-constexpr int kSoftmaxRegs = 72, kDecodeRegs = 64, kOtherRegs = 48;
+constexpr int kSoftmaxRegs = 72, kDecodeRegs = 56, kOtherRegs = 56;
 static_assert(4 * kSoftmaxRegs + 2 * kDecodeRegs + 2 * kOtherRegs <= 8 * 64, "register split");
 constexpr int HK = TK / 2;                // keys of half a tile
 constexpr int RING = 5;                   // slots of half a tile's K and V codes
@@ -394,68 +394,27 @@ DF_DEV void decode_k(const uint4 (&c)[4], uint32_t bytes, int ch, int unit0, uin
   tmem_st_wait();
 }
 
-// V: a lane's share of its warp's 16 rows of half a tile: it owns two rows and
-// takes 16 codes of each in each of two passes.  Lanes 0-3 of eight take the
-// one half of an even row, lanes 4-7 the other half of the odd row, so that
-// the eight 16-byte reads and stores of a phase fall into different banks.
-struct LaneV {
-  int row[2];          // rows of the half tile
-  int src[2];          // pass 0 within a slot's V; pass 1 is 64 bytes away (xor)
-  int dst[2];          // pass 0's first store within a tile; the second is 16
-                       // bytes away (xor), pass 1 in the other half
-  uint32_t group[2];   // scale byte of each pass
-};
-
-DF_DEV LaneV lane_v(int half, int sixteenth, int lane) {
-  LaneV l;
-  const int sub = (lane >> 2) & 1, u4 = lane & 3;
-  for (int o = 0; o < 2; ++o) {
-    const int r = sixteenth * 16 + o * 8 + (lane >> 3) * 2 + sub;
-    l.row[o] = r;
-    l.src[o] = r * HD + sub * 64 + u4 * 16;
-    l.dst[o] = sub * (int)VHALF + (half * HK + r) * 128 + ((2 * u4) ^ (r & 7)) * 16;
-  }
-  for (int p = 0; p < 2; ++p) l.group[p] = (uint32_t)((sub ^ p) * 2 + (u4 >> 1));
-  return l;
-}
-
-// The warp's rows as they came out of a slot into `tile`.  `edge`: some of
-// them may not be live (fp16: codes and scales of zero then).
+// V: the same half of a row, to `at`, its first chunk's place in a tile: chunk c
+// of a half lies at c ^ (row & 7) of the row's 128 bytes.  Eight lanes write
+// eight rows' chunks to different banks.
 template <int FMT, bool HALF16>
-DF_DEV void decode_v(uint4 (&c)[2][2], uint32_t (&bytes)[2], uint8_t* tile, const LaneV& l,
-                     bool edge, const int4& live, int unit0, uint32_t (&bits)[2]) {
-  if (HALF16 && edge) {
+DF_DEV void decode_v(const uint4 (&c)[4], uint32_t bytes, int ch, int unit0, uint8_t* tile,
+                     uint32_t at) {
+  HalfScales hs{};
+  if (HALF16) hs = half_scales(bytes, unit0);
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
-      if (live.x + l.row[o] < live.y || live.x + l.row[o] >= live.z) {
-        constexpr uint32_t zero = FMT == Q8_INT8 ? 0x80808080u : 0u;
-        c[o][0] = c[o][1] = make_uint4(zero, zero, zero, zero);
-        bytes[o] = 0u;
-      }
-  }
-#pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    HalfScales hs{};
-    if (HALF16)
-      hs = half_scales(bytes[o], unit0);
-    else
-      bytes[o] = live_scales(bytes[o], false,
-                             live.x + l.row[o] >= live.y && live.x + l.row[o] < live.z, bits[o]);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint4 x = c[o][p];
-      uint4 a, b;
-      if (HALF16) {
-        half_decode16<FMT>(x, hs, half_select(l.group[p]), a, b);
-      } else {
-        const float s = bf16_scale((bytes[o] >> (l.group[p] * 8)) & 0xffu);
-        a = bf16_decode8<FMT>(x.x, x.y, s);
-        b = bf16_decode8<FMT>(x.z, x.w, s);
-      }
-      const int dst = l.dst[o] ^ (p * (int)VHALF);
-      *reinterpret_cast<uint4*>(tile + dst) = a;
-      *reinterpret_cast<uint4*>(tile + (dst ^ 16)) = b;
+  for (int i = 0; i < 4; ++i) {
+    const int g = ch * 2 + (i >> 1);
+    uint4 a, b;
+    if (HALF16) {
+      half_decode16<FMT>(c[i], hs, half_select(g), a, b);
+    } else {
+      const float s = bf16_scale((bytes >> (g * 8)) & 0xffu);
+      a = bf16_decode8<FMT>(c[i].x, c[i].y, s);
+      b = bf16_decode8<FMT>(c[i].z, c[i].w, s);
     }
+    *reinterpret_cast<uint4*>(tile + (at ^ (uint32_t)(2 * i * 16))) = a;
+    *reinterpret_cast<uint4*>(tile + (at ^ (uint32_t)((2 * i + 1) * 16))) = b;
   }
 }
 
@@ -465,8 +424,8 @@ DF_DEV void decode_v(uint4 (&c)[2][2], uint32_t (&bytes)[2], uint8_t* tile, cons
 template <int FMT>
 DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int lane) {
   const int quarter = warp & 3, half = quarter >> 1, ch = warp >> 2;
-  const int rr = (quarter & 1) * 32 + lane;  // K row within the slot
-  const LaneV l = lane_v(half, (quarter & 1) * 2 + ch, lane);
+  const int rr = (quarter & 1) * 32 + lane;  // the thread's row within the slot
+  const uint32_t v_at = ch * VHALF + (quarter * 32 + lane) * 128 + ((rr & 7) << 4);
   const uint32_t k_col = tmem + ((uint32_t)(quarter * 32) << 16) + K_COL + ch * 32;
   int slot = half;
   uint32_t phase = 0;
@@ -478,19 +437,16 @@ DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int 
     const int4 head = *reinterpret_cast<const int4*>(meta);
     const int flags = uniform(head.x);
     int4 k_live, v_live;
-    uint4 kc[4], vc[2][2];
-    uint32_t kb, vb[2];
-    kb = *reinterpret_cast<const uint32_t*>(scales + rr * 4);
+    uint4 kc[4], vc[4];
+    uint32_t kb = *reinterpret_cast<const uint32_t*>(scales + rr * 4);
+    uint32_t vb = *reinterpret_cast<const uint32_t*>(scales + SCALES + rr * 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i)  // (16-byte chunk c of a row lies at c ^ (rr & 7))
       kc[i] = *reinterpret_cast<const uint4*>(codes + rr * HD + (((ch * 4 + i) ^ (rr & 7)) << 4));
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      vb[o] = *reinterpret_cast<const uint32_t*>(scales + SCALES + l.row[o] * 4);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        vc[o][p] = *reinterpret_cast<const uint4*>(codes + CODES + (l.src[o] ^ (p * 64)));
-    }
+    for (int i = 0; i < 4; ++i)
+      vc[i] = *reinterpret_cast<const uint4*>(codes + CODES + rr * HD +
+                                              (((ch * 4 + i) ^ (rr & 7)) << 4));
     v_live = *(reinterpret_cast<const int4*>(meta) + 2);
     if ((flags & (kHasK | kHalfK)) == kHasK) k_live = *(reinterpret_cast<const int4*>(meta) + 1);
     __syncwarp();
@@ -515,15 +471,21 @@ DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int 
       const int g = u - 1;
       if (!warp_wait(&sm.s_full[g & 1], (g >> 1) & 1, sm, err)) return;
       uint8_t* tile = sm.v + (g & 1) * VT;
-      uint32_t bits[2] = {0u, 0u};
+      const int key = v_live.x + rr;
+      const bool live = key >= v_live.y && key < v_live.z;
       if (flags & kHalfV) {
-        decode_v<FMT, true>(vc, vb, tile, l, (flags & kEdgeV) != 0, v_live, head.z, bits);
+        if ((flags & kEdgeV) && !live) {  // codes and scales of zero
+          constexpr uint32_t zero = FMT == Q8_INT8 ? 0x80808080u : 0u;
+          for (int i = 0; i < 4; ++i) vc[i] = make_uint4(zero, zero, zero, zero);
+          vb = 0u;
+        }
+        decode_v<FMT, true>(vc, vb, ch, head.z, tile, v_at);
       } else {
-        decode_v<FMT, false>(vc, vb, tile, l, true, v_live, 0, bits);
-        if ((lane & 3) == 0)
-          for (int o = 0; o < 2; ++o)
-            sm.nan_bits[(4 + (g & 3)) * TK + half * HK + l.row[o]] = (uint8_t)bits[o];
-        if ((bits[0] | bits[1]) != 0u) sm.nan_tile[g & 3] = g;
+        uint32_t bits = 0u;
+        vb = live_scales(vb, false, live, bits);
+        if (ch == 0) sm.nan_bits[(4 + (g & 3)) * TK + quarter * 32 + lane] = (uint8_t)bits;
+        if (bits != 0u) sm.nan_tile[g & 3] = g;
+        decode_v<FMT, false>(vc, vb, ch, 0, tile, v_at);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[g & 1]);
@@ -560,7 +522,7 @@ DF_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
 // The ring (one elected lane copies).  On an abort the copies in flight are
 // still waited for, with a limit: no CTA may leave before they have landed.
 DF_DEV void copy_codes(const Q8AttnArgs& a, const Q8Plan& p, const CUtensorMap* tm_k,
-                       const Shared& sm) {
+                       const CUtensorMap* tm_v, const Shared& sm) {
   const uint64_t once = policy_evict_first();
   Walk walk(a, p);
   Segment w{};
@@ -615,7 +577,7 @@ DF_DEV void copy_codes(const Q8AttnArgs& a, const Q8Plan& p, const CUtensorMap* 
         }
         if (m.flags & kHasV) {
           const int row = v_row + half * HK;
-          bulk_load(codes + CODES, a.st.v + (size_t)row * HD, CODES, bar, once);
+          tma_load_2d(codes + CODES, tm_v, bar, 0, row, once);
           bulk_load(scales + SCALES, a.st.vs + (size_t)row * 4, SCALES, bar, once);
         }
       }
@@ -1224,7 +1186,8 @@ DF_DEV void convert_and_write(const Q8AttnArgs& a, const Shared& sm, uint32_t tm
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Q8AttnArgs a,
+    attn_q8_kernel(const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Q8AttnArgs a,
                    const __grid_constant__ Q8Plan plan) {
   extern __shared__ uint8_t smem_raw[];
   // (an offset from the array, not a cast: the compiler has to know that all
@@ -1289,6 +1252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *sm.abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
   if (warp == kWarpMma) {
     tmem_alloc(tmem_slot, TMEM_COLS);
@@ -1311,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kWarpOut) {
       convert_and_write(a, sm, tmem, warp - kWarpOut, lane);
     } else if (warp == kWarpCopy) {
-      copy_codes(a, plan, &tm_k, sm);
+      copy_codes(a, plan, &tm_k, &tm_v, sm);
     } else if (warp >= kWarpQ) {
       fetch_queries(a, plan, sm, warp - kWarpQ, lane);
     } else {
@@ -1441,14 +1405,14 @@ bool plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sm
   return true;
 }
 
-int launch_q8_attention(int fmt, const CUtensorMap& tm_k, const Q8AttnArgs& a, const Q8Plan& p,
-                        cudaStream_t s) {
+int launch_q8_attention(int fmt, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                        const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t s) {
   if (const cudaError_t e = set_attrs()) return e;
   const int total = p.first[a.batch];
   const dim3 grid((unsigned)((total - 1) / p.share + 1)), block(kThreads);
   const cudaError_t e =
-      fmt == Q8_E4M3 ? launch_pdl(attn_q8_kernel<Q8_E4M3>, grid, block, kSmem, s, tm_k, a, p)
-                     : launch_pdl(attn_q8_kernel<Q8_INT8>, grid, block, kSmem, s, tm_k, a, p);
+      fmt == Q8_E4M3 ? launch_pdl(attn_q8_kernel<Q8_E4M3>, grid, block, kSmem, s, tm_k, tm_v, a, p)
+                     : launch_pdl(attn_q8_kernel<Q8_INT8>, grid, block, kSmem, s, tm_k, tm_v, a, p);
   if (e != cudaSuccess) return e;
   bool cut = false;
   for (unsigned c = 1; c < grid.x && !cut; ++c) {

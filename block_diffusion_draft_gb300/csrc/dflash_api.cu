@@ -1264,7 +1264,7 @@ int run_q8_attention(dflash_attn* at, dflash_q8_cache* c, const std::vector<int>
   if (!plan_q8_attention(p, c->batch, c->nkv, a.n_q_tiles, c->num_sms))
     return fail(DFLASH_ERR_SHAPE, "too many key tiles");
   TraceScope tr(at, DFLASH_K_ATTN, s);
-  DF_CUDA(launch_q8_attention(c->fmt, c->tm_k, a, p, s), "8-bit cache attention launch");
+  DF_CUDA(launch_q8_attention(c->fmt, c->tm_k, c->tm_v, a, p, s), "8-bit cache attention launch");
   return DFLASH_OK;
 }
 
@@ -1337,7 +1337,8 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   c->st.range = reinterpret_cast<int*>(p + 2 * (codes + scales));
   c->st.n_kv = c->nkv;
   c->st.cap = c->rows;
-  if (make_tmap_bf16_rows(&c->tm_k, c->st.k, (long long)rows, 64, 64) != 0) {
+  if (make_tmap_bf16_rows(&c->tm_k, c->st.k, (long long)rows, 64, 64) != 0 ||
+      make_tmap_bf16_rows(&c->tm_v, c->st.v, (long long)rows, 64, 64) != 0) {
     dflash_q8_cache_destroy(c);
     return fail(DFLASH_ERR_CUDA, "tensor map encoding failed");
   }

@@ -115,7 +115,7 @@ struct dflash_paged_cache {
 struct dflash_q8_cache {
   int batch = 0, cap = 0, rows = 0, nkv = 0, d = 0, fmt = 0, device = 0, num_sms = 0;
   df::Q8Store st{};
-  CUtensorMap tm_k;
+  CUtensorMap tm_k, tm_v;
   void* data = nullptr;
   float* part_o = nullptr;
   float* part_ml = nullptr;

@@ -364,9 +364,9 @@ constexpr int kQ8MaxSplits = 32;  // CTAs that a pair can lie across
 size_t q8_attention_slots(int num_sms);
 // fills first and share from len and lo; false if there are too many tiles
 bool plan_q8_attention(Q8Plan& p, int batch, int n_kv, int n_q_tiles, int num_sms);
-// tm_k: K's codes as rows of 64 bf16 numbers, boxes of 64 rows
-int launch_q8_attention(int fmt, const CUtensorMap& tm_k, const Q8AttnArgs& a, const Q8Plan& p,
-                        cudaStream_t s);
+// tm_k, tm_v: the codes as rows of 64 bf16 numbers, boxes of 64 rows
+int launch_q8_attention(int fmt, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                        const Q8AttnArgs& a, const Q8Plan& p, cudaStream_t s);
 
 // ------------------------------------------- verification of drafted tokens
 // One call of dflash_verify (verify.cu); strides in elements.
