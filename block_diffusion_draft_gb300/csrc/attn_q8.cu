@@ -257,7 +257,6 @@ struct Shared {
   float *top, *sum;        // [4][QR] per quarter of the keys; [2 by segment][QR][4]
   int2* out_rows;          // [4 by warp][QR]
   int* open;               // [2] rows without a key so far
-  volatile int* flag;      // [2] the last tile of this parity to move an m
   volatile int* nan_tile;  // [4] the last tile of this number (mod 4) with a NaN
   volatile int* abort;
   uint64_t *ring_full, *ring_empty;  // [RING]
@@ -838,6 +837,7 @@ constexpr int kParts = kSoftmaxWarps / 4, NQ = QR / kParts;  // its queries: NQ
 struct Place {
   int r, part, lane, quarter, tid;
   uint32_t trow;  // the lane's TMEM address
+  uint32_t p_at;  // its first chunk's place in a P tile: chunk c at c ^ (r & 7)
   DF_DEV int query(int i) const { return ((i >> 3) * kParts + part) * 8 + (i & 7); }
 };
 
@@ -958,6 +958,20 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
         }
       }
     };
+    uint8_t* p_tile = sm.p + st * PT;
+    auto store_p = [&]() {
+#pragma unroll
+      for (int j = 0; j < NQ / 8; ++j) {
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = 8 * j + 2 * k;
+          y[k] = HALF16 ? pack_f16x2(v[i], v[i + 1]) : pack_bf16x2(v[i], v[i + 1]);
+        }
+        *reinterpret_cast<uint4*>(p_tile + (at.p_at ^ (uint32_t)(j * kParts * 16))) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    };
     bool moves = open;
     if (!open) {
       scores();
@@ -966,12 +980,10 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
 #pragma unroll
       for (int i = 1; i < NQ - 1; i += 2) top = max3f(top, v[i], v[i + 1]);
       top = fmaxf(top, v[NQ - 1]);
-      const bool over = __any_sync(0xffffffffu, top > lift + kRescale);
-      if (over && at.lane == 0) sm.flag[st] = g;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) v[i] = fast_exp2(v[i]);
-      softmax_sync();
-      moves = uniform(sm.flag[st]) == g;
+      store_p();
+      moves = !all_of(1, kSoftmaxThreads, !(top > lift + kRescale));
     }
     if (moves) {
       // references from this tile's scores on, and what depended on the old
@@ -1022,21 +1034,13 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
       relate();
 #pragma unroll
       for (int i = 0; i < NQ; ++i) v[i] = fast_exp2(v[i]);
+      store_p();
     }
-    uint8_t* prow = sm.p + st * PT + at.r * (QR * 2);
 #pragma unroll
-    for (int j = 0; j < NQ / 8; ++j) {
-      uint32_t y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = 8 * j + 2 * k;
-        const float2 s = add_f32x2(make_float2(l[i], l[i + 1]), make_float2(v[i], v[i + 1]));
-        l[i] = s.x;
-        l[i + 1] = s.y;
-        y[k] = HALF16 ? pack_f16x2(v[i], v[i + 1]) : pack_bf16x2(v[i], v[i + 1]);
-      }
-      *reinterpret_cast<uint4*>(prow + (((j * kParts + at.part) ^ (at.r & 7)) << 4)) =
-          make_uint4(y[0], y[1], y[2], y[3]);
+    for (int i = 0; i < NQ; i += 2) {
+      const float2 s = add_f32x2(make_float2(l[i], l[i + 1]), make_float2(v[i], v[i + 1]));
+      l[i] = s.x;
+      l[i + 1] = s.y;
     }
     if (!HALF16) {
       // V(g)'s NaN marks, and K(g)'s, which the same warps set before
@@ -1066,6 +1070,7 @@ DF_DEV void softmax_all(const Shared& sm, int* err, uint32_t tmem, int warp, int
   at.lane = lane;
   at.tid = warp * 32 + lane;
   at.trow = tmem + ((uint32_t)(at.quarter * 32) << 16);
+  at.p_at = at.r * (QR * 2) + ((at.part ^ (at.r & 7)) << 4);
   int g = 0;
   for (int seg = 0;; ++seg) {
     if (!all_of(1, kSoftmaxThreads, warp_wait(&sm.q_full[seg & 1], (seg >> 1) & 1, sm, err)))
@@ -1217,7 +1222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* words = reinterpret_cast<int*>(bars + 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   sm.abort = words + 1;
-  sm.flag = words + 2;
   sm.nan_tile = words + 4;
   sm.open = words + 8;
   sm.seg = smem + OFF_SEG;
@@ -1246,7 +1250,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.q_raw[i], 2);
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.o_free[i], 4 + 1);
-      sm.flag[i] = -1;
     }
     for (int i = 0; i < 4; ++i) sm.nan_tile[i] = -1;
     *sm.abort = 0;
