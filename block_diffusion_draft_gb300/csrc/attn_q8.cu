@@ -20,13 +20,13 @@
 // shared memory.
 //
 // The codes of a tile are 33 KB against the 64 KB of a bf16 tile, so HBM asks
-// for a tile every 0.74 us (1430 cycles) per SM.  A tile takes 2100 cycles: the
+// for a tile every 0.74 us (1430 cycles) per SM.  A tile takes 2000 cycles: the
 // two steps that it spends on its way through the decoding warps (16384 codes
-// each of K and V, about 300 instructions per warp) follow one another without
-// a gap, while the softmax warps wait a third of their time.  6520 warp
-// instructions a tile keep the issue slots 60% busy; shared memory moves about
-// 178 KB a tile (copies in, codes out, V in and out, P in and out, Q out).
-// 76 us for 4 sequences of 32800 keys (8 KV heads): 3.7 TB/s.
+// each of K and V, 270 instructions per warp) follow one another without a gap,
+// while the softmax warps wait a third of their time.  5900 warp instructions a
+// tile keep the issue slots 63% busy; shared memory moves about 178 KB a tile
+// (copies in, codes out, V in and out, P in and out, Q out).  70 us for 4
+// sequences of 32800 keys (8 KV heads): 4.0 TB/s.
 //
 //   warps 0-15   softmax, thread = key (TMEM lane) and a quarter of the queries
 //   warps 16-23  decode: K from the ring into TMEM, V into the tensor core's
@@ -39,9 +39,12 @@
 //   warps 28-31  those queries to the products' type; the last segment's O out
 //
 // All of them run on across segments.  Tried and slower: eight softmax warps
-// with 32 queries a thread (fewer instructions, 78 us), eight warps each for K
-// and V beside them (78 us), Q and O handled by the softmax warps (a segment
-// cost 13000 cycles instead of 6500).
+// with 32 queries a thread (fewer instructions, 78 us when this took 74 us), and
+// eight warps each for K and V beside them (78 us); K decoded by the softmax
+// warps (96 us); codes read from the ring one step ahead (76 us against 70 us);
+// Q and O handled by the softmax warps (a segment cost 13000 cycles instead of
+// 6500); the merge in the CTA that comes last (29 us against 21 us for one block
+// over 4128 keys).
 //
 // Softmax.  m_q, the reference of query q's exponentials, is shared by all
 // threads and moves only when a score exceeds it by more than 2^8: each thread
@@ -959,6 +962,8 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
       }
     };
     uint8_t* p_tile = sm.p + st * PT;
+    // rounded to the products' type (2^-12 relative in fp16, 2^-9 in bf16), the
+    // one rounding of the probabilities; their sums take them unrounded
     auto store_p = [&]() {
 #pragma unroll
       for (int j = 0; j < NQ / 8; ++j) {
