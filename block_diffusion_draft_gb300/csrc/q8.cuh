@@ -42,34 +42,40 @@ constexpr int kHalfMinUnit = 15;  // smallest k0: bytes from kQ8MinByte are in i
 // scale byte of a group whose largest magnitude has the bf16 bits `amax`
 template <int FMT>
 DF_DEV uint32_t q8_scale_byte(uint32_t amax) {
-  if (amax >= 0x7f80u) return kQ8NanByte;
-  if (amax == 0u) return 0u;
-  amax = min(amax, kBf16MaxStored);
   // amax = (1 + mant / 128) * 2^(field - 127): 448 = 1.75 * 2^8 and
-  // 127 = (1 + 126 / 128) * 2^6
-  const int field = (int)(amax >> 7), mant = (int)(amax & 0x7fu);
-  const int byte = FMT == Q8_E4M3 ? field - 8 + (mant > 96) : field - 6 + (mant > 126);
-  return (uint32_t)max(byte, (int)kQ8MinByte);
+  // 127 = (1 + 126 / 128) * 2^6, so that the byte is field - 8 + (mant > 96) and
+  // field - 6 + (mant > 126); the comparison is a carry into the field
+  const int t = (int)min(amax, kBf16MaxStored);
+  const int byte = FMT == Q8_E4M3 ? ((t + 31) >> 7) - 8 : ((t + 1) >> 7) - 6;
+  const uint32_t b = (uint32_t)max(byte, (int)kQ8MinByte);
+  return amax >= 0x7f80u ? kQ8NanByte : amax == 0u ? 0u : b;
 }
 
-// codes of two bf16 values (packed in `w`) scaled by `inv` = 2^-e, in the low
-// 16 bits of the result
+// two bf16 values, their magnitudes at most 2^126 (NaN and infinity, too)
+DF_DEV uint32_t q8_clamp2(uint32_t w) {
+  return (w & 0x80008000u) | __vminu2(w & 0x7fff7fffu, 0x7e807e80u);
+}
+
+// codes of four bf16 values (two in each word) scaled by `inv` = 2^-e, exactly
+// but for what is far below half a code
 template <int FMT>
-DF_DEV uint32_t q8_encode2(uint32_t w, float inv) {
-  constexpr float top = 8.507059173023462e37f;  // 2^126
-  float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
-  lo = fminf(fmaxf(lo, -top), top) * inv;
-  hi = fminf(fmaxf(hi, -top), top) * inv;
+DF_DEV uint32_t q8_encode4(uint32_t w0, uint32_t w1, float inv) {
+  const float a = __uint_as_float(w0 << 16), b = __uint_as_float(w0 & 0xffff0000u);
+  const float c = __uint_as_float(w1 << 16), d = __uint_as_float(w1 & 0xffff0000u);
   if (FMT == Q8_E4M3) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
-    return c;
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inv), "f"(a * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inv), "f"(c * inv));
+    return lo | (uint32_t)hi << 16;
   }
-  // |y| <= 127: adding 2^23 + 128 rounds to the nearest even integer, and
-  // the low byte of the sum is that integer plus 128
-  const uint32_t a = __float_as_uint(lo + 8388736.f) & 0xffu;
-  const uint32_t b = __float_as_uint(hi + 8388736.f) & 0xffu;
-  return a | (b << 8);
+  // |y| <= 127: adding 2^23 + 128 rounds to the nearest even integer (the
+  // product is exact), and the low byte of the sum is that integer plus 128
+  constexpr float add = 8388736.f;
+  const uint32_t ab = __byte_perm(__float_as_uint(__fmaf_rn(a, inv, add)),
+                                  __float_as_uint(__fmaf_rn(b, inv, add)), 0x0040u);
+  const uint32_t cd = __byte_perm(__float_as_uint(__fmaf_rn(c, inv, add)),
+                                  __float_as_uint(__fmaf_rn(d, inv, add)), 0x0040u);
+  return __byte_perm(ab, cd, 0x5410u);
 }
 
 DF_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
