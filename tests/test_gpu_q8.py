@@ -486,6 +486,31 @@ def test_other_stream_and_captured_calls():
     assert torch.equal(out1[0], now[0]) and torch.equal(out1[1], now[1])
 
 
+def test_two_caches_on_two_streams():
+    """Calls on different caches may run at the same time, also of one layer."""
+    a = layer(8, 2)
+    sizes = ([3000, 0, 70], [900] * 5)
+    caches, queries, want = [], [], []
+    for i, counts in enumerate(sizes):
+        c = Q8Cache(a, len(counts), max(counts), FMTS[i])
+        c.append(rows(sum(counts), 2, i).cuda(), rows(sum(counts), 2, i + 5).cuda(), counts)
+        q = rows(len(counts) * 16, 8, i + 9, 0.2).view(len(counts), 16, 8, 128).cuda()
+        caches.append(c)
+        queries.append(q)
+        want.append(a.q8_core(c, q))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(a.q8_core(caches[i], queries[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    assert a.device_error() == 0
+
+
 # ---------------------------------------------------------------- the layer
 def _layer_step(sp, w, cfg, lw, attn, cache, step, n_ctx, L, q_len):
     th = [W.hidden_rows(sp, 5, "hidden", step, b, n) for b, n in enumerate(n_ctx)]
