@@ -159,7 +159,7 @@ def _stream(dev: torch.device):
 def _int32_array(xs: Sequence[int]):
     try:
         return (c_int32 * len(xs)).from_buffer(array("i", xs))
-    except TypeError:  # numbers that are not integers by type
+    except (TypeError, OverflowError):  # as ctypes takes them: by int(), modulo 2^32
         return (c_int32 * len(xs))(*[int(x) for x in xs])
 
 
