@@ -25,8 +25,8 @@
 // each of K and V, 270 instructions per warp) follow one another without a gap,
 // while the softmax warps wait a third of their time.  5900 warp instructions a
 // tile keep the issue slots 63% busy; shared memory moves about 178 KB a tile
-// (copies in, codes out, V in and out, P in and out, Q out).  70 us for 4
-// sequences of 32800 keys (8 KV heads): 4.0 TB/s.
+// (copies in, codes out, V in and out, P in and out, Q out).  74 us for 4
+// sequences of 32800 keys (8 KV heads): 3.8 TB/s.
 //
 //   warps 0-15   softmax, thread = key (TMEM lane) and a quarter of the queries
 //   warps 16-23  decode: K from the ring into TMEM, V into the tensor core's
@@ -51,6 +51,17 @@
 // looks at its own scores, a barrier per tile makes the finding common, and
 // then (the first tile of a segment, and seldom later) the tile's largest
 // scores are taken over the keys and O is rescaled.
+//
+// Hand-overs.  Every buffer goes from its writers to its readers and back
+// through an mbarrier's phase.  Where one side is the async proxy (copies, the
+// tensor core's reads of shared memory) and the other a thread's own loads or
+// stores, the thread puts fence.proxy.async between its accesses and its
+// arrival: the storing warps for Q, V and P, the decoding warps for a slot of
+// the ring that they have read.  What the tensor core has read or a copy has
+// written is handed over by the commit or by the transaction bytes.  In TMEM the
+// tcgen05 fences stand on both sides.  The fences of V, P and the slots cost 4%
+// on 4 sequences of 32800 keys (74 us against 70 us); with a fence only in the
+// warp that issues the MMAs, what others had stored could come too late.
 //
 // Rows behind the sequence's end decode to zero in V, so nothing stale can
 // reach O through a zero probability.  A group that reads NaN is decoded as
@@ -421,7 +432,9 @@ DF_DEV void decode_v(const uint4 (&c)[4], uint32_t bytes, int ch, int unit0, uin
 }
 
 // Step u: K(u), then V(u - 1).  A slot is free as soon as its codes are in
-// registers.  One wait besides the slot's is enough: s_full(u - 1) frees
+// registers: it is released behind K's, because the fence before that waits for
+// the loads of V's (released before K's: 76 us against 74 us on 4 sequences of
+// 32800 keys).  One wait besides the slot's is enough: s_full(u - 1) frees
 // V(u - 1)'s stage, and K(u + 1)'s for the next step.
 template <int FMT>
 DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int lane) {
@@ -451,8 +464,6 @@ DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int 
                                               (((ch * 4 + i) ^ (rr & 7)) << 4));
     v_live = *(reinterpret_cast<const int4*>(meta) + 2);
     if ((flags & (kHasK | kHalfK)) == kHasK) k_live = *(reinterpret_cast<const int4*>(meta) + 1);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
     if (flags & kHasK) {
       const uint32_t col = k_col + (u & 1) * 64;
       tc_fence_after();
@@ -469,6 +480,10 @@ DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int 
       }
       warp_arrive(&sm.k_full[u & 1], lane);
     }
+    // the slot's codes are in registers, K's have been used
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.ring_empty[slot]);
     if (flags & kHasV) {
       const int g = u - 1;
       if (!warp_wait(&sm.s_full[g & 1], (g >> 1) & 1, sm, err)) return;
@@ -489,6 +504,7 @@ DF_DEV void decode_all(const Shared& sm, int* err, uint32_t tmem, int warp, int 
         if (bits != 0u) sm.nan_tile[g & 3] = g;
         decode_v<FMT, false>(vc, vb, ch, 0, tile, v_at);
       }
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[g & 1]);
     }
@@ -664,6 +680,7 @@ DF_DEV void fetch_queries(const Q8AttnArgs& a, const Q8Plan& p, const Shared& sm
       tab.v0 = mode.v0;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_raw[seg & 1]);
   }
@@ -735,16 +752,16 @@ DF_DEV void convert_queries(const Q8AttnArgs& a, const Shared& sm, int seg, int 
       *at = finite ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
+  fence_proxy_async_smem();
 }
 
 // ---------------------------------------------------------------- products
 // One elected lane each: with elect.sync the compiler knows that a single
 // thread issues, and keeps the descriptors in uniform registers (behind a test
 // of the lane number the eight MMAs of a product took 800-950 cycles to issue).
-// What other warps stored to shared memory, ordered before
-// this by a barrier, becomes visible to the tensor core through the issuing
-// thread's proxy fence (in a storing warp the fence would wait for its loads
-// as well).
+// Q, V and P reach the tensor core through the async proxy: every thread that
+// stores a part of them fences its own stores before it arrives.  (A fence in
+// this warp alone, behind the barriers, does not drain other warps' stores.)
 // One warp issues both products, and PV(g - 2) before S(g): the tensor core
 // takes them in that order, so one barrier tells of both.  (The O buffer of a
 // segment is free when its table is there.)
@@ -766,7 +783,6 @@ DF_DEV void issue_all(const Shared& sm, int* err, uint32_t tmem) {
     --pending;
     if (!warp_wait(&sm.v_full[st], ph, sm, err) || !warp_wait(&sm.p_full[st], ph, sm, err))
       return false;
-    fence_proxy_async_smem();
     tc_fence_after();
     const uint64_t dv = desc_v + (uint32_t)(st * (VT >> 4));
     const uint64_t dp = desc_p + (uint32_t)(st * (PT >> 4));
@@ -796,7 +812,6 @@ DF_DEV void issue_all(const Shared& sm, int* err, uint32_t tmem) {
     if (left == 0) {
       ++seg;
       if (!warp_wait(&sm.q_full[seg & 1], (seg >> 1) & 1, sm, err)) return;
-      fence_proxy_async_smem();
       const SegmentTable& tab = sm.table(seg);
       left = uniform(tab.n);
       const bool half = uniform(tab.half) != 0;
@@ -1062,6 +1077,7 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
         }
       }
     }
+    fence_proxy_async_smem();
     warp_arrive(&sm.p_full[st], at.lane);
   }
   return ok;
