@@ -869,12 +869,23 @@ DF_DEV void load_columns8(uint32_t col, uint32_t* r) {
                : "r"(col));
 }
 
+// Waits for two such loads.  The registers go through the wait, so that nothing
+// that takes their values can be placed before it.
+DF_DEV void columns16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // this thread's columns (query(0), query(1), ...) of the 64 at `col` of its lane
 DF_DEV void load_columns(uint32_t col, int part, float (&v)[NQ]) {
   uint32_t r[NQ];
 #pragma unroll
   for (int j = 0; j < NQ / 8; ++j) load_columns8(col + (j * kParts + part) * 8, r + 8 * j);
-  tmem_ld_wait();
+  columns16_wait(r);
 #pragma unroll
   for (int i = 0; i < NQ; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -1171,7 +1182,7 @@ DF_DEV void write_rows(const Q8AttnArgs& a, const Shared& sm, uint32_t tmem, int
     uint32_t v[16];
     load_columns8(col + j, v);
     load_columns8(col + j + 8, v + 8);
-    tmem_ld_wait();
+    columns16_wait(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int2 r = row[j + i];
