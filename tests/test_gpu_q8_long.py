@@ -121,3 +121,77 @@ def test_every_pass_gives_the_same_bits(fmt, n_heads, n_kv, q_len, counts):
             same = torch.stack([(x == y).all() for i, r in got for x, y in zip(r, want[i])])
             assert bool(same.all()), same.tolist()
     assert a.device_error() == 0
+
+
+def make_wide(v):
+    """Groups of V 2^40 apart: the head's codes are then decoded to bf16."""
+    v[len(v) // 2, :, 32:64] *= 2.0 ** -40
+    return v
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_references_rise_within_long_segments(fmt, wide):
+    """Every CTA has one whole pair of 13 tiles, whose scores rise by more
+    than 2^8 at the 2nd, the 5th and the last tile for some rows, fall or stay
+    for others."""
+    sms, tiles = sm_count(), 13
+    a = layer(4, 1)
+    n = tiles * TK - 37
+    counts = [n] * sms
+    assert plan_share(counts, 1, 1, sms) == tiles + PAIR_COST
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = uneven_rows(sum(counts), 1, gen)
+    tile = torch.arange(n, device="cuda") // TK
+    level = 9.4 * ((tile >= 1).float() + (tile >= 4).float() + (tile >= tiles - 1).float())
+    k[:, 0, 0] = level.repeat(sms).bfloat16()
+    v = v.view(sms, n, 1, 128)
+    if wide:
+        for b in range(sms):
+            make_wide(v[b])
+    v = v.view(-1, 1, 128)
+    q = 0.3 * torch.randn(sms, 16, 4, 128, device="cuda", generator=gen)
+    lead = torch.tensor([8.0, -8.0, 4.0, 0.0, 12.0, -3.0, 9.0], device="cuda")
+    q[..., 0] = lead[torch.arange(sms * 64, device="cuda") % 7].view(sms, 16, 4)
+    q = q.bfloat16()
+    cache = Q8Cache(a, sms, n, fmt)
+    cache.append(k, v, counts)
+    out, lse = a.q8_core(cache, q)
+    ck, cv = cache.read()
+    # the rises, in log2 units, of a row whose first channel is 8
+    s = (ck[:n, 0].double() @ q[0, 0, 0].double()) / math.sqrt(128) / math.log(2)
+    top = torch.stack([s[tile == t].max() for t in range(tiles)]).tolist()
+    assert q[0, 0, 0, 0] == 8 and all(top[t] - max(top[:t]) > 8 for t in (1, 4, tiles - 1))
+    check(a, q, out, lse, ck, cv, counts, not wide)
+
+
+@pytest.mark.parametrize("fmt,wide,window,causal", [
+    ("int8", False, 0, False), ("e4m3", False, 0, False), ("int8", True, 0, False),
+    ("e4m3", True, 0, True), ("int8", False, 2100, True), ("e4m3", False, 1900, False),
+    ("int8", True, 2000, False)])
+def test_levels_that_wander_and_ctas_that_go_from_pair_to_pair(fmt, wide, window, causal):
+    """Pairs of 13 to 20 tiles, about two to a CTA, the level of the scores
+    another one in every tile."""
+    sms = sm_count()
+    r = random.Random(3)
+    counts = [r.randint(1600, 2500) for _ in range(sms // 4 + 1)]
+    a = layer(32, 8, window, causal)
+    assert plan_share(counts, 8, 1, sms) >= 2 * (13 + PAIR_COST)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    k, v = uneven_rows(sum(counts), 8, gen)
+    begin = 0
+    for n in counts:
+        step = torch.tensor([r.choice([-6.0, 0.0, 0.0, 9.0]) for _ in range(-(-n // TK))])
+        level = step.cumsum(0).repeat_interleave(TK)[:n].cuda()
+        k[begin:begin + n, :, 64] = level.bfloat16()[:, None]
+        if wide:
+            make_wide(v[begin:begin + n])
+        begin += n
+    q = 0.3 * torch.randn(len(counts), 16, 32, 128, device="cuda", generator=gen)
+    q[..., 64] = torch.linspace(-10, 10, 32, device="cuda")
+    q = q.bfloat16()
+    cache = Q8Cache(a, len(counts), max(counts), fmt)
+    cache.append(k, v, counts)
+    out, lse = a.q8_core(cache, q)
+    ck, cv = cache.read()
+    check(a, q, out, lse, ck, cv, counts, not wide, window, causal)
