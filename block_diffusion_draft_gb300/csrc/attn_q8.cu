@@ -250,7 +250,7 @@ struct SegmentTable {
   int n, t0, rows, slot;       // n: tiles, -1 behind the last segment
   int lo, hi, lo_all, hi_all;
   int same, half, k0, v0;
-  int uneven;                  // the rows' scores have scales sc, not `scale`, or may be large
+  int uneven;                  // the rows' scores have scales sc, not `scale`, or may be 2^20
   float scale;                 // of a score, in log2 units
   int top[4], low[4];          // exponents of the rows, per warp
   int2 seen[QR];               // keys a row sees
@@ -734,8 +734,11 @@ DF_DEV void convert_queries(const Q8AttnArgs& a, const Shared& sm, int seg, int 
     tab.nan[row] = finite ? 0 : (int)kNanK;
   }
   if (warp == 0 && lane == 0) {
-    // |S| < 2^35, so that scale <= 2^-15 keeps scores below 2^20
-    tab.uneven = !half || low < top - 10 || scale_of(top) > 3.0517578125e-05f ? 1 : 0;
+    // Even rows have one scale and scores below 2^20: fp16, |S| < 2^35, so
+    // that scale <= 2^-15; bf16, |S| < 2^(top - 126) 2^(9 + k0 + 5 - 127) 2^7 (the
+    // largest scale byte of K is k0 + 5 at most, or 255 with a NaN), scale < 1.
+    tab.uneven = half ? low < top - 10 || scale_of(top) > 3.0517578125e-05f
+                      : top + tab.k0 > 252;
     tab.scale = scale_of(top);
   }
   if (half || !finite) {
@@ -940,7 +943,7 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
   // every row sees all of the tiles [clear0, clear1)
   const int clear0 = uniform((tab.lo_all + TK - 1) / TK) - t0;
   const int clear1 = uniform(tab.hi_all / TK) - t0;
-  const bool uneven = HALF16 && uniform(tab.uneven) != 0;
+  const bool uneven = uniform(tab.uneven) != 0;
   const uint32_t o_col = at.trow + O_COL + (seg & 1) * QR;
   float* row_m = sm.m + (seg & 1) * QR;
   bool ok = true, open = true;  // open: some row has no reference yet

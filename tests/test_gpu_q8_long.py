@@ -195,3 +195,50 @@ def test_levels_that_wander_and_ctas_that_go_from_pair_to_pair(fmt, wide, window
     out, lse = a.q8_core(cache, q)
     ck, cv = cache.read()
     check(a, q, out, lse, ck, cv, counts, not wide, window, causal)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("why", ["wide", "hidden nan"])
+def test_large_scores_of_a_head_decoded_to_bf16(fmt, why):
+    """Queries 2^-60 to 2^100 apart, and keys 2^60 apart, on a head whose
+    codes are decoded to bf16: rows whose scores are far apart read their one
+    key, none loses its result."""
+    a = layer(4, 1, 0, True)
+    n, T = 900, 16
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    k, v = uneven_rows(n, 1, gen)
+    q = 0.3 * torch.randn(1, T, 4, 128, device="cuda", generator=gen)
+    for i, e in enumerate((-60, -11, 0, 5, 20, 26, 30, 31, 33, 40, 64, 100)):
+        q[0, i, i % 4] *= 2.0 ** e
+    q = q.bfloat16()
+    if why == "wide":
+        make_wide(v)
+        k[n // 3] *= 2.0 ** 20
+    else:
+        v[n - 1, 0, 5] = math.nan  # seen by the last block row only
+    cache = Q8Cache(a, 1, n, fmt)
+    cache.append(k, v, [n])
+    out, lse = a.q8_core(cache, q)
+    ck, cv = cache.read()
+    rows = T - 1
+    if why != "wide":
+        assert bool(out[0, rows, :, :32].isnan().all())
+    ref, rl, A, Q = reference(q[0], torch.nan_to_num(ck), torch.nan_to_num(cv), 0, True)
+    out, lse = out[0, :rows], lse[0, :rows]
+    assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    noise = 2 * (2.0 ** -17 * Q + n * 2.0 ** -24 + 2.0 ** -18)[:rows]
+    far = (lse.double() - rl[:rows]).abs() - noise - 2.0 ** -21 * rl[:rows].abs()
+    assert bool((far <= 0).all()), float(far.max())
+    sure = 0
+    for t in range(rows):
+        seen = n - T + t + 1
+        s = ck[:seen, 0].double() @ q[0, t].double().T / math.sqrt(128)  # [keys, heads]
+        first, at = s.max(0)
+        second = s.scatter(0, at[None], -math.inf).max(0).values
+        for h in range(4):
+            tol = 1.01 * 2.0 ** -8 * (A[t, h] + ref[t, h].abs()) + noise[t, h] * A[t, h]
+            assert bool(((out[t, h].double() - ref[t, h]).abs() <= tol).all()), (t, h)
+            if first[h] - second[h] > 200 + 2 * noise[t, h]:  # exp(-200) of the others
+                assert torch.equal(out[t, h], cv[at[h], 0]), (t, h)
+                sure += 1
+    assert sure >= 6
