@@ -1,6 +1,7 @@
 // dflash_api.cu -- the C ABI (include/dflash_attn.h): handles, argument
 // checks, scratch management and the launch sequence of each call.
 #include <algorithm>
+#include <array>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -83,6 +84,21 @@ struct TraceScope {
 
 int check_attn(const dflash_attn* a) {
   if (a == nullptr) return fail(DFLASH_ERR_ARG, "null layer handle");
+  return DFLASH_OK;
+}
+
+std::array<Buf*, 15> scratch_of(dflash_attn* a) {
+  return {&a->qbuf, &a->attn_out, &a->gemm_partial, &a->gemm_counters, &a->part_o,
+          &a->part_ml, &a->attn_counters, &a->zbuf, &a->proj_noise, &a->proj_ctx,
+          &a->packed_k, &a->packed_v, &a->packed_pos, &a->bwd_do, &a->bwd_stats};
+}
+
+// Whether work on `s` goes into a CUDA graph, which then keeps the addresses
+// of the scratch that it uses.
+int is_captured(cudaStream_t s, bool* captured) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  DF_CUDA(cudaStreamIsCapturing(s, &status), "capture status");
+  *captured = status != cudaStreamCaptureStatusNone;
   return DFLASH_OK;
 }
 
@@ -443,10 +459,7 @@ int dflash_attn_destroy(dflash_attn* a) {
     cudaEventDestroy(r.e1);
   }
   for (cudaEvent_t e : a->event_pool) cudaEventDestroy(e);
-  for (Buf* b : {&a->qbuf, &a->attn_out, &a->gemm_partial, &a->gemm_counters, &a->part_o,
-                 &a->part_ml, &a->attn_counters, &a->zbuf, &a->proj_noise, &a->proj_ctx,
-                 &a->packed_k, &a->packed_v, &a->packed_pos, &a->bwd_do, &a->bwd_stats})
-    b->release();
+  for (Buf* b : scratch_of(a)) b->release();
   delete a;
   return DFLASH_OK;
 }
@@ -1496,6 +1509,12 @@ int dflash_attn_forward_q8(dflash_attn* a, dflash_q8_cache* c, int batch, int q_
     return fail(DFLASH_ERR_ARG, "bf16 tensors must be 16-byte aligned");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t qd = (size_t)a->nq * a->d;
+  bool captured = false;
+  if (int r = is_captured(s, &captured)) return r;
+  if (captured) {
+    for (Buf* b : scratch_of(a)) b->held = true;
+    c->stage_k.held = c->stage_v.held = true;
+  }
   if (int r = dflash_q8_cache_reserve(c, most)) return r;
   DF_CUDA(a->qbuf.ensure(rows_noise * qd * 2), "scratch allocation");
   DF_CUDA(a->attn_out.ensure(rows_noise * qd * 2), "scratch allocation");

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <vector>
 
 #include "../../include/dflash_attn.h"
@@ -11,21 +12,37 @@
 
 namespace df {
 
-// device buffer that only grows
+// Device buffer that only grows.  Once a call that uses it has been captured
+// into a CUDA graph it is `held`: the graph keeps its address, so a block that
+// a larger call replaces stays allocated until release().  The new block then
+// has at least twice the size, so that all replaced ones together are smaller
+// than it.
 struct Buf {
   void* p = nullptr;
   size_t bytes = 0;
+  bool held = false;
+  std::vector<void*> replaced;
   cudaError_t ensure(size_t need, bool zero = false) {
     if (need <= bytes) return cudaSuccess;
-    if (p) {
+    if (p && held) {
+      need = std::max(need, 2 * bytes);
+      try {
+        replaced.reserve(replaced.size() + 1);
+      } catch (...) {
+        return cudaErrorMemoryAllocation;
+      }
+    } else if (p) {
       cudaDeviceSynchronize();
       cudaFree(p);
       p = nullptr;
       bytes = 0;
     }
     need = (need + 255) & ~size_t(255);
-    cudaError_t e = cudaMalloc(&p, need);
+    void* block = nullptr;
+    cudaError_t e = cudaMalloc(&block, need);
     if (e != cudaSuccess) return e;
+    if (p) replaced.push_back(p);
+    p = block;
     bytes = need;
     if (zero) {
       // the memset runs on the legacy default stream, which a non-blocking
@@ -37,8 +54,11 @@ struct Buf {
   }
   void release() {
     if (p) cudaFree(p);
+    for (void* block : replaced) cudaFree(block);
+    replaced.clear();
     p = nullptr;
     bytes = 0;
+    held = false;
   }
 };
 
@@ -110,8 +130,7 @@ struct dflash_paged_cache {
 // 8-bit draft KV cache: codes [batch][nkv][rows][d] and scale bytes
 // [batch][nkv][rows][d / 32] of K and of V (q8.cuh).  `rows` is the capacity
 // rounded up to whole 128-key tiles, so that every tile lies in the storage.
-// The attention's partial slots are sized once for every plan, so that a
-// captured call never holds memory a later call has replaced.
+// The attention's partial slots are sized once for every plan.
 struct dflash_q8_cache {
   int batch = 0, cap = 0, rows = 0, nkv = 0, d = 0, fmt = 0, device = 0, num_sms = 0;
   df::Q8Store st{};

@@ -486,7 +486,8 @@ int dflash_q8_cache_data(const dflash_q8_cache* cache, void** k_codes,
 
 /* Size the cache's scratch for dflash_attn_forward_q8 calls that append at
  * most max_new_rows rows (context and block) to any sequence, so that they
- * allocate nothing for it. */
+ * allocate nothing for it: 4 * batch * n_kv_heads * 128 * max_new_rows bytes
+ * (K and V in bf16, every sequence's rows at the same distance). */
 int dflash_q8_cache_reserve(dflash_q8_cache* cache, int max_new_rows);
 
 /* Encode host_n[b] rows of K and V behind the rows sequence b holds.
@@ -528,7 +529,12 @@ int dflash_q8_attn_core(dflash_attn* attn, dflash_q8_cache* cache, int batch,
 /* dflash_attn_forward over an 8-bit cache: arguments, outputs, appended rows,
  * lengths and errors are those of dflash_attn_forward.  K (after k_norm and
  * RoPE) and V are rounded to bf16 and encoded as they are appended, and the
- * queries see the encoded rows, the block's own included.  Any q_len. */
+ * queries see the encoded rows, the block's own included.  Any q_len.
+ * Before a call is captured into a CUDA graph its scratch has to have the size
+ * it needs (a call of that size before, or dflash_attn_reserve and
+ * dflash_q8_cache_reserve).  The scratch of the layer and of the cache that a
+ * captured call uses stays allocated until they are destroyed, also when a
+ * larger call later needs more; they have to outlive the graph. */
 int dflash_attn_forward_q8(dflash_attn* attn, dflash_q8_cache* cache, int batch,
                            int q_len, const void* noise_hidden,
                            const void* target_hidden, const int32_t* host_n_ctx,

@@ -1,0 +1,63 @@
+"""Calls over the 8-bit cache captured into CUDA graphs and replayed between
+other calls."""
+import pytest
+import torch
+
+from block_diffusion_draft_gb300 import Q8Cache
+from block_diffusion_draft_gb300 import workloads as W
+
+import helpers as T
+
+pytestmark = pytest.mark.gpu
+
+
+def small_layer():
+    sp = W.spec("qwen3_8b_single", hidden=512, n_heads=8, n_kv_heads=2, n_target_layers=1,
+                max_position=4096)
+    return T.gpu_layer(sp, W.weights(sp, 3, with_fc=False)), sp
+
+
+def step_inputs(sp, n_ctx, q_len, L, seed):
+    th = torch.cat([W.hidden_rows(sp, seed, "hidden", 0, b, n) for b, n in enumerate(n_ctx)])
+    nz = torch.stack([W.hidden_rows(sp, seed, "noise", 0, b, q_len) for b in range(len(n_ctx))])
+    pos = torch.cat([W.window_positions(L[b], n, q_len) for b, n in enumerate(n_ctx)])
+    return nz.cuda(), th.cuda(), n_ctx, pos.cuda()
+
+
+def test_a_captured_step_survives_larger_ones():
+    """A step captured at a small size is replayed after steps that need far
+    more scratch of the cache and of the layer."""
+    attn, sp = small_layer()
+    cache = Q8Cache(attn, 2, 2000, "int8")
+    held = [30, 5]
+    first = step_inputs(sp, held, 1, [0, 0], 1)
+    attn.forward_q8(cache, *first)
+    cache.crop(held)
+    args = step_inputs(sp, [3, 2], 8, held, 2)
+    want = attn.forward_q8(cache, *args).clone()
+    rows = [x.clone() for x in cache.read()]
+    cache.crop(held)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = attn.forward_q8(cache, *args)
+    for n, q_len in ((40, 16), (300, 16), (900, 64)):
+        cache.crop([0, 0])
+        big = Q8Cache(attn, 2, 2000, "int8")
+        attn.forward_q8(big, *step_inputs(sp, [n, n], q_len, [0, 0], 3))
+        attn.forward_q8(cache, *step_inputs(sp, [n, n // 2], q_len, [0, 0], 4))
+        cache.crop([0, 0])
+        attn.forward_q8(cache, *first)
+        cache.crop(held)
+        fill = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        cache.crop([0, 0])
+        attn.forward_q8(cache, *first)
+        cache.crop(held)
+        assert torch.equal(attn.forward_q8(cache, *args), want)
+        assert all(torch.equal(x, y) for x, y in zip(cache.read(), rows))
+        del fill, big
+    assert attn.device_error() == 0
