@@ -1313,7 +1313,9 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
     return fail(DFLASH_ERR_ARG, "format must be DFLASH_Q8_E4M3 or DFLASH_Q8_INT8");
   if (int r = check_device(a->device)) return r;
   dflash_q8_cache* c = nullptr;
+  std::vector<int4> range;  // of no scale
   try {
+    range.assign((size_t)batch * a->nkv, make_int4(255, 0, 255, 0));
     c = new dflash_q8_cache();
     c->len.assign(batch, 0);
   } catch (...) {
@@ -1330,13 +1332,16 @@ int dflash_q8_cache_create(const dflash_attn* a, int batch, int capacity_rows, i
   c->num_sms = a->num_sms;
   const size_t rows = (size_t)batch * a->nkv * c->rows;
   const size_t codes = rows * 128, scales = rows * 4, slots = q8_attention_slots(c->num_sms);
-  const size_t ranges = (size_t)batch * a->nkv * 4 * sizeof(int);
+  const size_t ranges = range.size() * sizeof(int4);
   cudaError_t e = cudaMalloc(&c->data, 2 * (codes + scales) + ranges);
   if (e == cudaSuccess) e = cudaMalloc(&c->part_o, slots * kQ8TileRows * 128 * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&c->part_ml, slots * 2 * kQ8TileRows * sizeof(float));
   // zeroed: rows past a sequence's end are read with its last tile (and
   // decoded to zero); finished before any other stream can use the cache
-  if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales) + ranges);
+  if (e == cudaSuccess) e = cudaMemset(c->data, 0, 2 * (codes + scales));
+  if (e == cudaSuccess)
+    e = cudaMemcpy(static_cast<uint8_t*>(c->data) + 2 * (codes + scales), range.data(), ranges,
+                   cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     dflash_q8_cache_destroy(c);
@@ -1434,8 +1439,10 @@ int dflash_q8_cache_append(dflash_q8_cache* c, const void* k, const void* v,
   if (int r = check_device(c->device)) return r;
   Q8Source src{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), 0, c->d,
                k_row_stride, v_row_stride, 1};
-  DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, c->num_sms,
-                           static_cast<cudaStream_t>(stream)),
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  if (int r = is_captured(s, &captured)) return r;
+  DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, !captured, c->num_sms, s),
           "8-bit cache append launch");
   for (int b = 0; b < c->batch; ++b) c->len[b] += host_n[b];
   return DFLASH_OK;
@@ -1544,7 +1551,7 @@ int dflash_attn_forward_q8(dflash_attn* a, dflash_q8_cache* c, int batch, int q_
                  (long long)c->nkv * most * c->d, (long long)most * c->d, c->d, c->d, 0};
     {
       TraceScope tr(a, DFLASH_K_MISC, s);
-      DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, c->num_sms, s),
+      DF_CUDA(launch_q8_append(c->fmt, c->st, t, src, !captured, c->num_sms, s),
               "8-bit cache append launch");
     }
     // Q as the projection leaves it: [batch][n_kv][groups][q_len][d], scaled

@@ -321,7 +321,8 @@ struct Q8Source {
   int packed;
 };
 
-int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
+// anew: the scale ranges of sequences whose rows begin at row 0 start again
+int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src, bool anew,
                      int num_sms, cudaStream_t s);
 int launch_q8_read(int fmt, const Q8Store& st, const Q8Rows& t, void* k_dst, void* v_dst,
                    cudaStream_t s);

@@ -139,7 +139,9 @@ struct Span {
   }
 };
 
-// Ranges of the sequences whose rows begin anew.
+// Ranges of the sequences whose rows begin anew.  Not in a CUDA graph: when it
+// is replayed the sequence may hold other rows behind the ones it writes, so
+// there a range only widens.
 __global__ void q8_reset_kernel(const __grid_constant__ Q8Store st,
                                 const __grid_constant__ Q8Rows t) {
   grid_dep_sync();
@@ -245,11 +247,11 @@ unsigned blocks_of(const Q8Rows& t, const Q8Store& st, int items) {
 }  // namespace
 
 int launch_q8_append(int fmt, const Q8Store& st, const Q8Rows& t, const Q8Source& src,
-                     int num_sms, cudaStream_t s) {
+                     bool anew, int num_sms, cudaStream_t s) {
   if (t.off[t.n] == 0) return cudaSuccess;
-  bool anew = false;
-  for (int b = 0; b < t.n; ++b) anew = anew || (t.first[b] == 0 && t.off[b + 1] > t.off[b]);
-  if (anew) {
+  bool any = false;
+  for (int b = 0; b < t.n; ++b) any = any || (t.first[b] == 0 && t.off[b + 1] > t.off[b]);
+  if (anew && any) {
     const cudaError_t e = launch_pdl(q8_reset_kernel, dim3((t.n * st.n_kv + 255) / 256),
                                      dim3(256), 0, s, st, t);
     if (e != cudaSuccess) return e;

@@ -464,7 +464,16 @@ int dflash_packed_attn_core_backward(dflash_attn* attn, int batch, int seq,
  * one (_ARG).  The cache owns the scratch of the attention over it, sized once
  * at creation: calls on one cache must not run concurrently on different
  * streams.  In a CUDA graph a call keeps the lengths, and so the rows it
- * writes and reads, of the moment of its capture. */
+ * writes and reads, of the moment of its capture; what a replayed call reads has
+ * to be rows that the cache still holds or that a replay wrote.
+ *
+ * The cache keeps the range of the scales written to every (sequence, KV head).
+ * The attention reads a head's codes as fp16 numbers while its scales lie within
+ * 20 binades of one another (K and V each) and no group reads NaN, otherwise as
+ * bf16 numbers, which takes about 1.4 times as long.  Either is exact; the
+ * probabilities are rounded to the same type.  A range widens with every row
+ * that is written, also with one that is cropped later, and starts again when an
+ * append outside a CUDA graph begins at row 0. */
 enum { DFLASH_Q8_E4M3 = 0, DFLASH_Q8_INT8 = 1 };
 
 int dflash_q8_cache_create(const dflash_attn* attn, int batch,

@@ -61,3 +61,31 @@ def test_a_captured_step_survives_larger_ones():
         assert all(torch.equal(x, y) for x, y in zip(cache.read(), rows))
         del fill, big
     assert attn.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_a_replayed_append_keeps_what_is_known_of_other_rows(fmt):
+    """An append captured at row 0 is replayed after rows of larger and smaller
+    scales came behind it: they read as before."""
+    attn, _ = small_layer()
+    cache = Q8Cache(attn, 2, 600, fmt)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda n: torch.randn(n, 2, 128, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    k, v = rand(20), rand(20)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.append(k, v, [15, 5])
+    g.replay()
+    more, tiny = rand(400) * 64, rand(40) * 2.0 ** -9
+    more[100:200, :, :64] = 0
+    cache.append(torch.cat([more, tiny]), torch.cat([tiny, more]), [400, 40])
+    q = torch.randn(2, 4, 8, 128, device="cuda", generator=gen).bfloat16()
+    want = attn.q8_core(cache, q)
+    ref = Q8Cache(attn, 2, 600, fmt)
+    ref.append(torch.cat([k[:15], more, k[15:], tiny]), torch.cat([v[:15], tiny, more[:360],
+                                                                    v[15:], more[360:]]), [415, 45])
+    assert all(torch.equal(x, y) for x, y in zip(cache.read(), ref.read()))
+    assert all(torch.equal(x, y) for x, y in zip(want, attn.q8_core(ref, q)))
+    for _ in range(2):
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(attn.q8_core(cache, q), want))
