@@ -157,10 +157,12 @@ def _stream(dev: torch.device):
 
 
 def _int32_array(xs: Sequence[int]):
-    try:
-        return (c_int32 * len(xs)).from_buffer(array("i", xs))
-    except (TypeError, OverflowError):  # as ctypes takes them: by int(), modulo 2^32
-        return (c_int32 * len(xs))(*[int(x) for x in xs])
+    if not isinstance(xs, (bytes, bytearray)):  # (an array would read those as machine words)
+        try:
+            return (c_int32 * len(xs)).from_buffer(array("i", xs))
+        except (TypeError, OverflowError):
+            pass
+    return (c_int32 * len(xs))(*[int(x) for x in xs])  # as ctypes takes them: modulo 2^32
 
 
 def _call(device: torch.device, f, *args) -> None:
