@@ -61,6 +61,19 @@ DF_DEV Fixed fixed(float p) {
   return f;
 }
 
+// floor(min(max(u, 0), 1) * total) without rounding, NaN as 0, for a total below
+// 2^63: u is a 24-bit number times a power of two, their product has 87 bits.  (In
+// 64-bit floats it is rounded to 53, up to the next whole number at times.)
+DF_DEV unsigned long long scaled(float u, unsigned long long total) {
+  if (!(u > 0.f)) return 0ull;
+  const uint32_t bits = __float_as_uint(fminf(u, 1.f)), field = bits >> 23;
+  const unsigned long long m = (bits & 0x7fffffu) | (field != 0u ? 0x800000u : 0u);
+  const int shift = 150 - (int)max(field, 1u);  // 23 to 149
+  const unsigned long long hi = __umul64hi(m, total);
+  if (shift >= 64) return hi >> min(shift - 64, 63);  // (hi < 2^23)
+  return hi << (64 - shift) | (m * total) >> shift;
+}
+
 DF_DEV long long whole(int hi, int lo) { return (long long)hi * (1 << 22) + lo; }
 
 template <typename T>
@@ -236,9 +249,7 @@ __global__ void __launch_bounds__(kThreads)
       if (rank == 0 && threadIdx.x == 0) tokens[k] = -1;
       break;
     }
-    const float u = u_sample;
-    unsigned long long t = u > 0.f ? (unsigned long long)((double)min(u, 1.f) * (double)total) : 0ull;
-    t = min(t, total - 1ull);
+    const unsigned long long t = min(scaled(u_sample, total), total - 1ull);
     for (int i = 0; i < warp; ++i) before += warp_sum[pass][i];
     if (t >= before && t - before < sum) {
       // the drawn point lies in this warp's share: the step that holds it, and

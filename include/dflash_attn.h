@@ -561,7 +561,7 @@ int dflash_attn_forward_q8(dflash_attn* attn, dflash_q8_cache* cache, int batch,
  * With a the number of accepted drafts, one more token follows them: drawn
  * from max(p_a - q_a, 0) when draft a was rejected, from p_n when a = n, as
  * the first token whose cumulative weight exceeds floor(u_sample * sum of the
- * weights).  Weights are whole multiples of 2^-44: a probability is taken as
+ * weights), the product not rounded before.  Weights are whole multiples of 2^-44: a probability is taken as
  * floor(min(max(p, 0), 1) * 2^44), NaN as 0.  If the difference leaves no
  * weight the token is drawn from p_a; if that has none either it is -1.  The
  * result does not depend on the GPU's order of summation.
