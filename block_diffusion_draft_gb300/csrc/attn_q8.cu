@@ -20,13 +20,20 @@
 // shared memory.
 //
 // The codes of a tile are 33 KB against the 64 KB of a bf16 tile, so HBM asks
-// for a tile every 0.74 us (1430 cycles) per SM.  A tile takes 2000 cycles: the
-// two steps that it spends on its way through the decoding warps (16384 codes
-// each of K and V, 270 instructions per warp) follow one another without a gap,
-// while the softmax warps wait a third of their time.  5900 warp instructions a
-// tile keep the issue slots 63% busy; shared memory moves about 178 KB a tile
-// (copies in, codes out, V in and out, P in and out, Q out).  74 us for 4
-// sequences of 32800 keys (8 KV heads): 3.8 TB/s.
+// for a tile every 0.76 us per SM.  A tile takes 1.06 us (2200 cycles; one pair
+// per SM, 9 to 257 tiles): the two steps that it spends on its way through the
+// decoding warps (16384 codes each of K and V, 270 instructions per warp) follow
+// one another without a gap, while the softmax warps wait a third of their time.
+// About 6100 warp instructions a tile keep the issue slots 63% busy; shared
+// memory moves about 178 KB a tile (copies in, codes out, V in and out, P in and
+// out, Q out).  74 us for 4 sequences of 32800 keys (8 KV heads): 3.8 TB/s.  The
+// scalar state that does not fit the register split is spilled: 24 and 32 bytes
+// a thread in the two instances.
+//
+// Rows beyond 64 per KV head are other query tiles, for which the keys are
+// copied and decoded again: 32 sequences of 512 to 8192 keys take 88 us with 64
+// rows, 157 us with 68 to 128, 300 us with 256.  Heads that are decoded to bf16
+// take 1.4 to 1.5 times as long (131 us, and 100 us for the 4 long sequences).
 //
 //   warps 0-15   softmax, thread = key (TMEM lane) and a quarter of the queries
 //   warps 16-23  decode: K from the ring into TMEM, V into the tensor core's
@@ -38,13 +45,13 @@
 //   warps 26-27  the next segment's queries and tables
 //   warps 28-31  those queries to the products' type; the last segment's O out
 //
-// All of them run on across segments.  Tried and slower: eight softmax warps
-// with 32 queries a thread (fewer instructions, 78 us when this took 74 us), and
-// eight warps each for K and V beside them (78 us); K decoded by the softmax
-// warps (96 us); codes read from the ring one step ahead (76 us against 70 us);
-// Q and O handled by the softmax warps (a segment cost 13000 cycles instead of
-// 6500); the merge in the CTA that comes last (29 us against 21 us for one block
-// over 4128 keys).
+// All of them run on across segments.  Tried and slower, each pair of times
+// without the fences of the hand-overs below: eight softmax warps with 32 queries
+// a thread (fewer instructions, 78 us when this took 74 us), and eight warps each
+// for K and V beside them (78 us); K decoded by the softmax warps (96 us); codes
+// read from the ring one step ahead (76 us against 70 us); Q and O handled by the
+// softmax warps (a segment cost 13000 cycles instead of 6500); the merge in the
+// CTA that comes last (29 us against 21 us for one block over 4128 keys).
 //
 // Softmax.  m_q, the reference of query q's exponentials, is shared by all
 // threads and moves only when a score exceeds it by more than 2^8: each thread
@@ -60,8 +67,8 @@
 // the ring that they have read.  What the tensor core has read or a copy has
 // written is handed over by the commit or by the transaction bytes.  In TMEM the
 // tcgen05 fences stand on both sides.  The fences of V, P and the slots cost 4%
-// on 4 sequences of 32800 keys (74 us against 70 us); with a fence only in the
-// warp that issues the MMAs, what others had stored could come too late.
+// on 4 sequences of 32800 keys (74 us against 70 us); a fence in the warp that
+// issues the MMAs alone is none for what the other warps have stored.
 //
 // Rows behind the sequence's end decode to zero in V, so nothing stale can
 // reach O through a zero probability.  A group that reads NaN is decoded as
@@ -109,8 +116,9 @@ constexpr float kRescale = 8.f;           // log2 units
 constexpr float kLift = 7.f;              // fp16 P = 2^(score - m + 7)
 // What a segment costs beside its tiles, in tiles: places of the line that a
 // pair takes up without having a tile there.  (A tile takes 2200 cycles, a
-// segment 6500 and more where segments are short: 32 sequences of 512 to 8192
-// keys took 122, 101, 95 and 101 us with 1, 2, 4 and 6.)
+// segment 6400 and more where segments are short: 32 sequences of 512 to 8192
+// keys take 97, 93, 89, 89 and 90 us with 2, 3, 4, 5 and 6, 4 of 32800 keys 74 us
+// with each, 7 of up to 1500 with a window 21 to 24 us, the least with 2.)
 constexpr int kPairCost = 4;
 constexpr uint32_t kNanK = 16;            // the key reads NaN in K
 
@@ -736,7 +744,7 @@ DF_DEV void convert_queries(const Q8AttnArgs& a, const Shared& sm, int seg, int 
   if (warp == 0 && lane == 0) {
     // Even rows have one scale and scores below 2^20: fp16, |S| < 2^35, so
     // that scale <= 2^-15; bf16, |S| < 2^(top - 126) 2^(9 + k0 + 5 - 127) 2^7 (the
-    // largest scale byte of K is k0 + 5 at most, or 255 with a NaN), scale < 1.
+    // largest scale byte of K is k0 + 5 at most, or 255 with a NaN), scale <= 1.
     tab.uneven = half ? low < top - 10 || scale_of(top) > 3.0517578125e-05f
                       : top + tab.k0 > 252;
     tab.scale = scale_of(top);
@@ -763,8 +771,7 @@ DF_DEV void convert_queries(const Q8AttnArgs& a, const Shared& sm, int seg, int 
 // thread issues, and keeps the descriptors in uniform registers (behind a test
 // of the lane number the eight MMAs of a product took 800-950 cycles to issue).
 // Q, V and P reach the tensor core through the async proxy: every thread that
-// stores a part of them fences its own stores before it arrives.  (A fence in
-// this warp alone, behind the barriers, does not drain other warps' stores.)
+// stores a part of them fences its own stores before it arrives.
 // One warp issues both products, and PV(g - 2) before S(g): the tensor core
 // takes them in that order, so one barrier tells of both.  (The O buffer of a
 // segment is free when its table is there.)
@@ -991,7 +998,7 @@ DF_DEV bool softmax_segment(SegmentTable& tab, int seg, const Shared& sm, int* e
       }
     };
     uint8_t* p_tile = sm.p + st * PT;
-    // rounded to the products' type (2^-12 relative in fp16, 2^-9 in bf16), the
+    // rounded to the products' type (2^-11 relative in fp16, 2^-8 in bf16), the
     // one rounding of the probabilities; their sums take them unrounded
     auto store_p = [&]() {
 #pragma unroll

@@ -24,8 +24,8 @@ constexpr int kReadItems = kThreads / 16;  // (row, kv head) pairs that a CTA re
 constexpr int kItems = kThreads / 8;       // and that it has in work when writing
 // CTAs of a large append, per SM: three times what runs at a time, so that they
 // do not end together, and few enough that not each looks at the ranges for
-// itself.  32768 rows of 8 KV heads, appended and read (407 MB): 76 us with 12,
-// 77 us with 8, 83 us with 24, 100 us with 48.
+// itself.  32768 rows of 8 KV heads, appended and read (407 MB): 72 us with 12;
+// in one comparison 76 us with 12, 77 us with 8, 83 us with 24, 100 us with 48.
 constexpr int kAppendCtas = 12;
 
 // The (row, kv head) that item `it` of a call stands for: row `local` of
@@ -99,7 +99,8 @@ DF_DEV void put(const Coded& c, uint8_t* codes, uint8_t* scales, int lane8, bool
   if (lane8 == 0) *reinterpret_cast<uint32_t*>(scales) = bytes;
 }
 
-// Smallest and largest scale bytes that eight lanes have met of K and of V in one (sequence, kv head); zero groups do not count.
+// Smallest and largest scale bytes that eight lanes have met of K and of V in
+// one (sequence, kv head); zero groups do not count.
 struct Span {
   int* range;  // of the (sequence, kv head), or null
   int4 seen;   // this lane's

@@ -529,8 +529,16 @@ int dflash_q8_cache_read(const dflash_q8_cache* cache, const int32_t* host_first
  * The q_len queries stand at the sequence's last q_len key indices (block row
  * t at length - q_len + t, which only a window or the causal flag look at); K
  * and V are the rows the cache holds.  A row that sees no key gets out = 0 and
- * lse = -infinity.  Any q_len; at most 128 query heads per KV head
- * (_UNSUPPORTED).  Errors: _ARG, _SHAPE, _UNSUPPORTED, _CUDA. */
+ * lse = -infinity; a row of q with an infinity or NaN, NaN.  Scores are held in
+ * fp32: beyond its range one counts as the largest number, or as not seen below.
+ * Any q_len; at most 128 query heads per KV head (_UNSUPPORTED).  The cached
+ * rows are decoded once per 64 query rows of a KV head (q_len * n_heads /
+ * n_kv_heads), which bounds long calls: up to 64 rows take one time, up to 128
+ * nearly twice that.
+ * After a bounded wait that ran out (DFLASH_DEV_WAIT_TIMEOUT, which only
+ * dflash_device_error() reports) rows of out and lse may be zero, -infinity or
+ * lack some of their keys.
+ * Errors: _ARG, _SHAPE, _UNSUPPORTED, _CUDA. */
 int dflash_q8_attn_core(dflash_attn* attn, dflash_q8_cache* cache, int batch,
                         int q_len, const void* q, void* out, float* lse,
                         dflash_stream stream);
