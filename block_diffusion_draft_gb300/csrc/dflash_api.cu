@@ -102,6 +102,14 @@ int is_captured(cudaStream_t s, bool* captured) {
   return DFLASH_OK;
 }
 
+// At the start of a forward: a layer whose call is captured keeps its scratch.
+int hold_if_captured(dflash_attn* a, cudaStream_t s, bool* captured) {
+  if (int r = is_captured(s, captured)) return r;
+  if (*captured)
+    for (Buf* b : scratch_of(a)) b->held = true;
+  return DFLASH_OK;
+}
+
 // scratch needed by the bf16 GEMM for a given shape
 int ensure_gemm_scratch(dflash_attn* a, int epi, int rows0, int rows1, int n, int k,
                         int q_cols) {
@@ -255,6 +263,8 @@ int forward_core(dflash_attn* a, const KvView& kv, int batch, int q_len, const v
     st.ctx_off[b + 1] = st.ctx_off[b] + host_n_ctx[b];
     st.cache_len[b] = len_before[b];
   }
+  bool captured = false;
+  if (int r = hold_if_captured(a, s, &captured)) return r;
   DF_CUDA(a->qbuf.ensure(rows_noise * qd * es), "scratch allocation");
   DF_CUDA(a->attn_out.ensure(rows_noise * qd * es), "scratch allocation");
   QkvOut o = make_qkv_out(a, positions, a->qbuf.p, kv.k, kv.v, kv.cap, q_len);
@@ -1517,11 +1527,8 @@ int dflash_attn_forward_q8(dflash_attn* a, dflash_q8_cache* c, int batch, int q_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t qd = (size_t)a->nq * a->d;
   bool captured = false;
-  if (int r = is_captured(s, &captured)) return r;
-  if (captured) {
-    for (Buf* b : scratch_of(a)) b->held = true;
-    c->stage_k.held = c->stage_v.held = true;
-  }
+  if (int r = hold_if_captured(a, s, &captured)) return r;
+  if (captured) c->stage_k.held = c->stage_v.held = true;
   if (int r = dflash_q8_cache_reserve(c, most)) return r;
   DF_CUDA(a->qbuf.ensure(rows_noise * qd * 2), "scratch allocation");
   DF_CUDA(a->attn_out.ensure(rows_noise * qd * 2), "scratch allocation");
@@ -1697,8 +1704,8 @@ int dflash_device_error(dflash_attn* a, int32_t* code) {
   if (h != 0) {
     // a kernel that gave up may have left split counters raised: clear them
     cudaMemset(a->err, 0, sizeof(int));
-    if (a->gemm_counters.p) cudaMemset(a->gemm_counters.p, 0, a->gemm_counters.bytes);
-    if (a->attn_counters.p) cudaMemset(a->attn_counters.p, 0, a->attn_counters.bytes);
+    a->gemm_counters.clear();
+    a->attn_counters.clear();
     cudaDeviceSynchronize();
     return fail(DFLASH_ERR_DEVICE, "device-side fault code %d", h);
   }

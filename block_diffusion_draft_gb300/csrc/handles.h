@@ -21,7 +21,8 @@ struct Buf {
   void* p = nullptr;
   size_t bytes = 0;
   bool held = false;
-  std::vector<void*> replaced;
+  struct Block { void* p; size_t bytes; };
+  std::vector<Block> replaced;
   cudaError_t ensure(size_t need, bool zero = false) {
     if (need <= bytes) return cudaSuccess;
     if (p && held) {
@@ -41,7 +42,7 @@ struct Buf {
     void* block = nullptr;
     cudaError_t e = cudaMalloc(&block, need);
     if (e != cudaSuccess) return e;
-    if (p) replaced.push_back(p);
+    if (p) replaced.push_back({p, bytes});
     p = block;
     bytes = need;
     if (zero) {
@@ -52,9 +53,13 @@ struct Buf {
     }
     return e;
   }
+  void clear() {
+    if (p) cudaMemset(p, 0, bytes);
+    for (const Block& b : replaced) cudaMemset(b.p, 0, b.bytes);
+  }
   void release() {
     if (p) cudaFree(p);
-    for (void* block : replaced) cudaFree(block);
+    for (const Block& b : replaced) cudaFree(b.p);
     replaced.clear();
     p = nullptr;
     bytes = 0;

@@ -145,6 +145,9 @@ int dflash_attn_destroy(dflash_attn* attn);
 
 /* Optional: size the layer's scratch for calls up to these sizes now, so
  * that later calls of at most that size allocate nothing.
+ * Scratch that a dflash_attn_forward, _paged or _q8 captured into a CUDA graph
+ * uses stays allocated until the layer is destroyed, also when a larger call
+ * later needs more.
  * max_rows = largest (batch*q_len + total new context rows) of a forward, or
  * rows of a ctx_project; max_keys = largest total key rows of one sequence;
  * max_batch = largest batch. */

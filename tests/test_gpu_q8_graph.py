@@ -3,7 +3,7 @@ other calls."""
 import pytest
 import torch
 
-from block_diffusion_draft_gb300 import Q8Cache
+from block_diffusion_draft_gb300 import DraftCache, Q8Cache
 from block_diffusion_draft_gb300 import workloads as W
 
 import helpers as T
@@ -60,6 +60,34 @@ def test_a_captured_step_survives_larger_ones():
         assert torch.equal(attn.forward_q8(cache, *args), want)
         assert all(torch.equal(x, y) for x, y in zip(cache.read(), rows))
         del fill, big
+    assert attn.device_error() == 0
+
+
+def test_a_captured_step_over_the_bf16_cache_survives_larger_8_bit_ones():
+    """The two kinds of steps share the layer's scratch."""
+    attn, sp = small_layer()
+    held = [30, 5]
+    cache, big = DraftCache(attn, 2, 200), Q8Cache(attn, 2, 2000, "e4m3")
+    attn.forward(cache, *step_inputs(sp, held, 1, [0, 0], 1))
+    cache.crop(held)
+    args = step_inputs(sp, [3, 2], 8, held, 2)
+    want = attn.forward(cache, *args).clone()
+    cache.crop(held)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = attn.forward(cache, *args)
+    for n, q_len in ((300, 16), (900, 64)):
+        attn.forward_q8(big, *step_inputs(sp, [n, n], q_len, [0, 0], 3))
+        big.crop([0, 0])
+        other = DraftCache(attn, 2, 2000)  # takes what was freed
+        torch.cuda.synchronize()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        cache.crop(held)
+        assert torch.equal(attn.forward(cache, *args), want)
+        assert all(not x.any() for x in other.read())
     assert attn.device_error() == 0
 
 
