@@ -341,6 +341,15 @@ int forward_core(dflash_attn* a, const KvView& kv, int batch, int q_len, const v
 
 }  // namespace
 
+int df::api_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(code, "%s", buf);
+}
+
 // error reporting for the allocation-free entry point (noalloc.cu)
 int dflash_noalloc_fail(int code, const char* msg) { return fail(code, "%s", msg); }
 
@@ -1626,6 +1635,132 @@ int dflash_verify(int batch, int n_draft, int vocab, int dtype, const int32_t* d
   DF_CUDA(launch_verify(a, dtype == DFLASH_BF16, num_sms, static_cast<cudaStream_t>(stream)),
           "verification launch");
   return DFLASH_OK;
+}
+
+namespace {
+
+// One tensor of a norm-and-rotation call: strides of axes of one element do
+// not matter; `write`: no two of its heads may overlap.
+int head_view(const dflash_attn* a, const dflash_heads* h, const char* name, int batch, int rows,
+              int heads, bool write, HeadView* v) {
+  if (h == nullptr || h->data == nullptr) return fail(DFLASH_ERR_ARG, "%s is null", name);
+  v->p = h->data;
+  v->batch = batch > 1 ? h->batch_stride : 0;
+  v->row = rows > 1 ? h->row_stride : 0;
+  v->head = heads > 1 ? h->head_stride : 0;
+  if (v->batch < 0 || v->row < 0 || v->head < 0)
+    return fail(DFLASH_ERR_ARG, "%s: strides must be >= 0", name);
+  if (a->dt == DFLASH_BF16) {
+    if (!aligned16(v->p)) return fail(DFLASH_ERR_ARG, "%s must be 16-byte aligned", name);
+    if (((v->batch | v->row | v->head) & 7) != 0)
+      return fail(DFLASH_ERR_ARG, "%s: strides must be multiples of 8", name);
+  } else if ((reinterpret_cast<uintptr_t>(v->p) & 3) != 0) {
+    return fail(DFLASH_ERR_ARG, "%s is not aligned to its type", name);
+  }
+  if (!write) return DFLASH_OK;
+  std::array<std::pair<long long, long long>, 3> axes = {
+      std::make_pair(v->batch, (long long)batch), std::make_pair(v->row, (long long)rows),
+      std::make_pair(v->head, (long long)heads)};
+  std::sort(axes.begin(), axes.end());
+  long long extent = a->d;  // of everything inside the axis
+  for (const auto& x : axes) {
+    if (x.second <= 1) continue;
+    if (x.first < extent) return fail(DFLASH_ERR_ARG, "%s: heads overlap", name);
+    extent = x.first * (x.second - 1) + extent;
+  }
+  return DFLASH_OK;
+}
+
+int run_qk_norm_rope(dflash_attn* a, int batch, int rows, const dflash_heads* const (&x)[2],
+                     const void* const (&gain)[2], const int32_t* positions,
+                     const dflash_heads* const (&dy)[2], const dflash_heads* const (&out)[2],
+                     bool bwd, float* const (&d_gain)[2], void* ws, size_t ws_bytes,
+                     cudaStream_t s) {
+  if (int r = check_attn(a)) return r;
+  if (batch < 0 || rows < 0) return fail(DFLASH_ERR_ARG, "batch and rows must be >= 0");
+  if (x[0] == nullptr && x[1] == nullptr) return fail(DFLASH_ERR_ARG, "no queries and no keys");
+  if ((long long)batch * rows > (1LL << 30) / (a->nq + a->nkv))
+    return fail(DFLASH_ERR_SHAPE, "too many rows");
+  const bool none = batch == 0 || rows == 0;
+  if (!none && positions == nullptr) return fail(DFLASH_ERR_ARG, "positions is null");
+  static const char* const names[2][3] = {{"q", "d_q", "q_out"}, {"k", "d_k", "k_out"}};
+  QkRopeArgs q{};
+  q.batch = batch;
+  q.rows = rows;
+  q.d = a->d;
+  q.max_pos = a->max_pos;
+  q.eps = a->cfg.rms_eps;
+  q.rope = a->rope;
+  q.positions = positions;
+  q.gain32[0] = a->q_norm;
+  q.gain32[1] = a->k_norm;
+  q.err = a->err;
+  for (int k = 0; k < 2; ++k) {
+    if (x[k] == nullptr) continue;
+    q.heads[k] = k == 0 ? a->nq : a->nkv;
+    q.gain[k] = gain[k];
+    if (bwd && d_gain[k] == nullptr) return fail(DFLASH_ERR_ARG, "a gain's gradient is null");
+    if (a->dt == DFLASH_BF16 ? !aligned16(gain[k])
+                             : (reinterpret_cast<uintptr_t>(gain[k]) & 3) != 0)
+      return fail(DFLASH_ERR_ARG, "gains not aligned");
+    if (none) continue;
+    if (int r = head_view(a, x[k], names[k][0], batch, rows, q.heads[k], false, &q.x[k])) return r;
+    if (bwd)
+      if (int r = head_view(a, dy[k], names[k][1], batch, rows, q.heads[k], false, &q.dy[k]))
+        return r;
+    if (int r = head_view(a, out[k], names[k][2], batch, rows, q.heads[k], true, &q.out[k]))
+      return r;
+  }
+  if (bwd) {
+    size_t need = 0;
+    if (int r = dflash_qk_norm_rope_workspace(a, &need)) return r;
+    if (ws == nullptr || !aligned16(ws)) return fail(DFLASH_ERR_ARG, "workspace null or unaligned");
+    if (ws_bytes < need)
+      return fail(DFLASH_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+    q.partial = static_cast<float*>(ws);
+  }
+  if (int r = check_device(a->device)) return r;
+  if (none) {
+    for (int k = 0; bwd && k < 2; ++k)
+      if (x[k] != nullptr)
+        DF_CUDA(cudaMemsetAsync(d_gain[k], 0, (size_t)a->d * sizeof(float), s), "memset");
+    return DFLASH_OK;
+  }
+  TraceScope tr(a, DFLASH_K_MISC, s);
+  DF_CUDA(launch_qk_rope(q, a->dt == DFLASH_BF16, bwd, a->num_sms, x[0] ? d_gain[0] : nullptr,
+                         x[1] ? d_gain[1] : nullptr, s),
+          "norm and rotation launch");
+  return DFLASH_OK;
+}
+
+}  // namespace
+
+int dflash_qk_norm_rope(dflash_attn* a, int batch, int rows, const dflash_heads* q,
+                        const dflash_heads* k, const void* q_norm_w, const void* k_norm_w,
+                        const int32_t* positions, const dflash_heads* q_out,
+                        const dflash_heads* k_out, dflash_stream stream) {
+  return run_qk_norm_rope(a, batch, rows, {q, k}, {q_norm_w, k_norm_w}, positions,
+                          {nullptr, nullptr}, {q_out, k_out}, false, {nullptr, nullptr}, nullptr,
+                          0, static_cast<cudaStream_t>(stream));
+}
+
+int dflash_qk_norm_rope_workspace(const dflash_attn* a, size_t* bytes) {
+  if (int r = check_attn(a)) return r;
+  if (bytes == nullptr) return fail(DFLASH_ERR_ARG, "bytes is null");
+  *bytes = (size_t)qk_rope_max_ctas(a->num_sms) * 2 * a->d * sizeof(float);
+  return DFLASH_OK;
+}
+
+int dflash_qk_norm_rope_backward(dflash_attn* a, int batch, int rows, const dflash_heads* q,
+                                 const dflash_heads* k, const void* q_norm_w,
+                                 const void* k_norm_w, const int32_t* positions,
+                                 const dflash_heads* d_q, const dflash_heads* d_k,
+                                 const dflash_heads* dq_out, const dflash_heads* dk_out,
+                                 float* d_q_norm, float* d_k_norm, void* workspace,
+                                 size_t workspace_bytes, dflash_stream stream) {
+  return run_qk_norm_rope(a, batch, rows, {q, k}, {q_norm_w, k_norm_w}, positions, {d_q, d_k},
+                          {dq_out, dk_out}, true, {d_q_norm, d_k_norm}, workspace,
+                          workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int dflash_wait_probe(dflash_attn* a, int64_t limit_ns, int arrive, dflash_stream stream) {

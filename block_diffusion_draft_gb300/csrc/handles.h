@@ -12,6 +12,9 @@
 
 namespace df {
 
+// Records the calling thread's error message and returns `code` (dflash_api.cu).
+int api_fail(int code, const char* fmt, ...);
+
 // Device buffer that only grows.  Once a call that uses it has been captured
 // into a CUDA graph it is `held`: the graph keeps its address, so a block that
 // a larger call replaces stays allocated until release().  The new block then

@@ -385,4 +385,30 @@ struct VerifyArgs {
 };
 int launch_verify(const VerifyArgs& a, int bf16, int num_sms, cudaStream_t s);
 
+// -------------------------------------- norm and rotation of queries and keys
+// A [batch][rows][heads][d] tensor, channels dense, strides in elements.
+struct HeadView {
+  void* p;
+  long long batch, row, head;
+};
+
+// One call of dflash_qk_norm_rope or its backward (qk_rope.cu); index 0: the
+// queries, 1: the keys (0 heads where a call has none).
+struct QkRopeArgs {
+  int batch, rows, d, max_pos;
+  int heads[2];
+  long long items;             // set by the launch: units of work of a warp
+  float eps;
+  const float2* rope;          // [max_pos][d / 2] (cos, sin)
+  const int* positions;        // [batch][rows]
+  const void* gain[2];         // [d] in the layer's type; null: gain32
+  const float* gain32[2];
+  HeadView x[2], dy[2], out[2];
+  float* partial;              // backward: [qk_rope_max_ctas][2][d]
+  int* err;
+};
+int qk_rope_max_ctas(int num_sms);
+int launch_qk_rope(const QkRopeArgs& a, int bf16, bool bwd, int num_sms, float* dq_gain,
+                   float* dk_gain, cudaStream_t s);
+
 }  // namespace df

@@ -10,7 +10,7 @@ import ctypes
 import os
 import re
 from array import array
-from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_void_p
+from ctypes import POINTER, byref, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
@@ -32,6 +32,11 @@ class Config(ctypes.Structure):
                 ("n_target_layers", c_int32), ("rms_eps", c_float),
                 ("rope_theta", c_float), ("sliding_window", c_int32),
                 ("max_position", c_int32), ("dtype", c_int32), ("causal", c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("row_stride", c_int64),
+                ("head_stride", c_int64)]
 
 
 class DFlashError(RuntimeError):
@@ -95,6 +100,16 @@ _SIGNATURES = {
                                 POINTER(c_int32), c_void_p, c_void_p, c_void_p], c_int),
     "dflash_verify": ([c_int] * 4 + [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64,
                                      c_int64] + [c_void_p] * 6, c_int),
+    "dflash_qk_norm_rope": ([c_void_p, c_int, c_int, POINTER(Heads), POINTER(Heads)] +
+                            [c_void_p] * 3 + [POINTER(Heads), POINTER(Heads), c_void_p], c_int),
+    "dflash_qk_norm_rope_workspace": ([c_void_p, POINTER(c_size_t)], c_int),
+    "dflash_qk_norm_rope_backward": ([c_void_p, c_int, c_int, POINTER(Heads), POINTER(Heads)] +
+                                     [c_void_p] * 3 + [POINTER(Heads)] * 4 + [c_void_p] * 3 +
+                                     [c_size_t, c_void_p], c_int),
+    "dflash_grad_norm_workspace": ([c_int, POINTER(c_size_t)], c_int),
+    "dflash_grad_norm": ([c_int] + [c_void_p] * 5 + [c_size_t, c_void_p], c_int),
+    "dflash_clip_grad_norm": ([c_int] + [c_void_p] * 4 + [ctypes.c_double] + [c_void_p] * 2 +
+                              [c_size_t, c_void_p], c_int),
     "dflash_device_error": ([c_void_p, POINTER(c_int32)], c_int),
     "dflash_wait_probe": ([c_void_p, ctypes.c_int64, c_int, c_void_p], c_int),
     "dflash_read_stream_probe": ([c_void_p, c_void_p, ctypes.c_int64, ctypes.c_int64, c_int,
@@ -212,6 +227,22 @@ def _block_shape(noise: torch.Tensor, attn: "DFlashAttention") -> Tuple[int, int
     return noise.shape[0], noise.shape[1]
 
 
+def _rows_of(q: Optional[torch.Tensor], k: Optional[torch.Tensor]) -> Tuple[int, int]:
+    x = q if q is not None else k
+    if x is None or x.dim() != 4:
+        raise ValueError("q or k must be given as [batch, rows, heads, head_dim]")
+    return x.shape[0], x.shape[1]
+
+
+def _like(x: Optional[torch.Tensor], out: Optional[torch.Tensor],
+          name: str) -> Optional[torch.Tensor]:
+    if x is None and out is not None:
+        raise ValueError(f"{name} given without its input")
+    if x is not None and out is None:
+        return torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    return out
+
+
 class DFlashAttention:
     """One draft attention layer held by the library.
 
@@ -249,6 +280,7 @@ class DFlashAttention:
                 _p(dev_w["wv"]), _p(dev_w["wo"]), _p(dev_w["q_norm"]),
                 _p(dev_w["k_norm"]), _p(fc), _p(hn), ctypes.byref(h)))
         self.handle = h
+        self._rope_ws: Optional[int] = None  # bytes of qk_norm_rope_backward's workspace
 
     # ---------------------------------------------------------------- calls
     def reserve(self, max_batch: int, max_rows: int, max_keys: int) -> None:
@@ -382,6 +414,80 @@ class DFlashAttention:
                 _p(out), _p(lse), _p(d_out), _p(anchors), _p(dq), _p(dk), _p(dv),
                 _stream(self.device)))
         return dq, dk, dv
+
+    def qk_norm_rope(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                     positions: torch.Tensor, q_norm: Optional[torch.Tensor] = None,
+                     k_norm: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None):
+        """Per-head RMSNorm (gains q_norm, k_norm [d]; None: the layer's) and
+        rotation of q [B, R, n_heads, d] and k [B, R, n_kv, d] at positions
+        [B, R] (int32).  Channels are dense, other strides free; q or k may be
+        None.  Results go to q_out and k_out (the inputs themselves, or any
+        tensor of that shape, such as rows of packed_core's keys, transposed),
+        by default dense tensors.  Returns (q_out, k_out)."""
+        B, R = _rows_of(q, k)
+        _require("positions", positions, torch.int32, self.device, (B, R))
+        qs, ks = self._heads("q", q, (B, R), self.n_heads), self._heads("k", k, (B, R),
+                                                                       self.n_kv_heads)
+        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
+        _call(self.device, lib().dflash_qk_norm_rope, self.handle, B, R, qs, ks,
+              self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
+              self._heads("q_out", q_out, (B, R), self.n_heads),
+              self._heads("k_out", k_out, (B, R), self.n_kv_heads))
+        return q_out, k_out
+
+    def qk_norm_rope_backward(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                              positions: torch.Tensor, q_norm: Optional[torch.Tensor],
+                              k_norm: Optional[torch.Tensor], d_q: Optional[torch.Tensor],
+                              d_k: Optional[torch.Tensor],
+                              dq_out: Optional[torch.Tensor] = None,
+                              dk_out: Optional[torch.Tensor] = None):
+        """Gradients of qk_norm_rope's inputs: q, k, positions and gains as
+        given there, d_q and d_k the gradients of its outputs.  Returns (dq, dk,
+        d_q_norm, d_k_norm), the gains' in fp32, None for q or k None."""
+        B, R = _rows_of(q, k)
+        _require("positions", positions, torch.int32, self.device, (B, R))
+        nq, nkv = self.n_heads, self.n_kv_heads
+        qs, ks = self._heads("q", q, (B, R), nq), self._heads("k", k, (B, R), nkv)
+        if (q is None) != (d_q is None) or (k is None) != (d_k is None):
+            raise ValueError("d_q and d_k must be given exactly where q and k are")
+        dq_out, dk_out = _like(q, dq_out, "dq_out"), _like(k, dk_out, "dk_out")
+        f32 = lambda t: None if t is None else torch.empty(  # noqa: E731
+            self.head_dim, device=self.device, dtype=torch.float32)
+        dgq, dgk = f32(q), f32(k)
+        if self._rope_ws is None:
+            n = c_size_t(0)
+            check(lib().dflash_qk_norm_rope_workspace(self.handle, byref(n)))
+            self._rope_ws = n.value
+        ws = torch.empty(self._rope_ws, device=self.device, dtype=torch.uint8)
+        _call(self.device, lib().dflash_qk_norm_rope_backward, self.handle, B, R, qs, ks,
+              self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
+              self._heads("d_q", d_q, (B, R), nq), self._heads("d_k", d_k, (B, R), nkv),
+              self._heads("dq_out", dq_out, (B, R), nq), self._heads("dk_out", dk_out, (B, R), nkv),
+              _p(dgq), _p(dgk), ws.data_ptr(), self._rope_ws)
+        return dq_out, dk_out, dgq, dgk
+
+    def _heads(self, name: str, t: Optional[torch.Tensor], rows: Tuple[int, int],
+               heads: int) -> Optional[Heads]:
+        if t is None:
+            return None
+        if t.shape != (*rows, heads, self.head_dim):
+            raise ValueError(f"{name} must be {[*rows, heads, self.head_dim]}, "
+                             f"got {list(t.shape)}")
+        if t.dtype is not self.dtype or not _on(t, self.device):
+            raise ValueError(f"{name} must be {self.dtype} on {self.device}, "
+                             f"got {t.dtype} on {t.device}")
+        s = t.stride()
+        if s[3] != 1 and t.numel():
+            raise ValueError(f"{name}: a head's channels must be dense")
+        return Heads(t.data_ptr() or 16, s[0], s[1], s[2])  # (no data: no rows)
+
+    def _gain(self, name: str, t: Optional[torch.Tensor]) -> Optional[int]:
+        if t is None:
+            return None
+        _require(name, t, self.dtype, self.device, (self.head_dim,))
+        return t.data_ptr()
 
     def trace(self, enable: bool) -> None:
         """Start (fresh) or stop recording CUDA events around each launch."""
@@ -644,6 +750,78 @@ def _probabilities(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch
     if strides[2] != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{name}: a row's values must be dense")
     return strides
+
+
+def grad_norm(grads: Sequence[torch.Tensor]) -> torch.Tensor:
+    """The norm of all values of the tensors (fp32 or bf16, dense, one device)
+    as an fp32 scalar on their device; see dflash_grad_norm."""
+    return _grad_norm(grads, None, None)
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
+                   out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
+    """Scale the tensors by max_norm / norm where their norm (as grad_norm) is
+    above max_norm, in place or into ``out`` (as grads).  Gradients whose norm
+    is not finite stay as they are.  Returns the norm before clipping, on the
+    device.  See dflash_clip_grad_norm in include/dflash_attn.h."""
+    return _grad_norm(grads, float(max_norm), out)
+
+
+_GRAD_TYPES = {torch.bfloat16: DFLASH_BF16, torch.float32: DFLASH_FP32}
+
+
+def _grad_norm(grads, max_norm, out) -> torch.Tensor:
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    dev, n = grads[0].device, len(grads)
+    if dev.type != "cuda":
+        raise ValueError("the library runs on CUDA devices only")
+    for i, g in enumerate(grads):
+        if g.dtype not in _GRAD_TYPES or g.device != dev:
+            raise ValueError(f"gradient {i} must be float32 or bfloat16 on {dev}, "
+                             f"got {g.dtype} on {g.device}")
+        if not _dense(g):
+            raise ValueError(f"gradient {i} must be dense")
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError(f"out must hold {n} tensors, got {len(out)}")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o.dtype is not g.dtype or o.device != dev or o.shape != g.shape or (
+                    o.stride() != g.stride() and g.numel() > 1):
+                raise ValueError(f"out {i} must have the shape, strides, type and device of "
+                                 f"gradient {i}")
+        outs = (c_void_p * n)(*[o.data_ptr() for o in out])
+    ptrs = (c_void_p * n)(*[g.data_ptr() for g in grads])
+    counts = (c_int64 * n)(*[g.numel() for g in grads])
+    types = (c_int32 * n)(*[_GRAD_TYPES[g.dtype] for g in grads])
+    size = c_size_t(0)
+    check(lib().dflash_grad_norm_workspace(n, byref(size)))
+    ws = torch.empty(size.value, device=dev, dtype=torch.uint8)
+    norm = torch.empty((), device=dev, dtype=torch.float32)
+    if max_norm is None:
+        _call(dev, lib().dflash_grad_norm, n, ptrs, counts, types, norm.data_ptr(), ws.data_ptr(),
+              size.value)
+    else:
+        _call(dev, lib().dflash_clip_grad_norm, n, ptrs, outs, counts, types, max_norm,
+              norm.data_ptr(), ws.data_ptr(), size.value)
+    return norm
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether a tensor's values fill one run of memory, in any order of axes."""
+    if t.is_contiguous():
+        return True
+    run = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size == 1:
+            continue
+        if stride != run:
+            return False
+        run *= size
+    return True
 
 
 class KVGroup:

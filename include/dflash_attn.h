@@ -46,6 +46,7 @@
 #ifndef DFLASH_ATTN_H
 #define DFLASH_ATTN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -605,6 +606,89 @@ int dflash_verify(int batch, int n_draft, int vocab, int dtype,
                   int64_t target_row_stride, const float* u_accept,
                   const float* u_sample, const int32_t* seq_drafts,
                   int32_t* accepted, int32_t* tokens, dflash_stream stream);
+
+/* Per-head RMSNorm and rotation of queries and keys, outside the QKV
+ * projection, and its gradient: with dflash_packed_attn_core what a training
+ * framework needs between its projections and the attention ([P3] step 1,
+ * [P4] apply_rotary_pos_emb; the pages leave the gradient to autograd).  Per
+ * head x of a row at position p, with r = 1 / sqrt(mean(x^2) + rms_eps):
+ *   y = rotation(p) (gain * x * r)      (pairs j, j + head_dim / 2)
+ * and back, with w = rotation(-p) d_y:
+ *   d_x = r * (w * gain - x * r^2 * mean(w * gain * x)),
+ *   d_gain = sum over rows and heads of w * x * r.
+ * The layer gives head counts, head_dim, rms_eps, rope_theta, max_position and
+ * its type; of its weights only the gains are used, and only where q_norm_w or
+ * k_norm_w is NULL. */
+typedef struct {
+  void* data;                /* [batch][rows][heads][head_dim], channels dense */
+  int64_t batch_stride, row_stride, head_stride; /* in elements, >= 0        */
+} dflash_heads;
+
+/*   q, k          device, n_heads and n_kv_heads heads; NULL: none of them
+ *                 (the keys of context rows, say), not both
+ *   q_norm_w      device [head_dim] in the layer's type, or NULL
+ *   positions     device int32 [batch][rows]; one outside [0, max_position) is
+ *                 clamped and recorded (DFLASH_DEV_POSITION)
+ *   q_out, k_out  device, as q and k; may be q and k themselves (not overlap
+ *                 them otherwise), or any layout whose heads do not overlap,
+ *                 such as rows of the packed core's keys
+ * Strides of inputs may be 0.  bf16: 16-byte boundaries, strides multiples of
+ * 8 elements.  batch or rows may be 0.  The layer's device has to be current.
+ * Errors: _ARG, _SHAPE, _CUDA. */
+int dflash_qk_norm_rope(dflash_attn* attn, int batch, int rows, const dflash_heads* q,
+                        const dflash_heads* k, const void* q_norm_w, const void* k_norm_w,
+                        const int32_t* positions, const dflash_heads* q_out,
+                        const dflash_heads* k_out, dflash_stream stream);
+
+/* Bytes of the workspace of dflash_qk_norm_rope_backward. */
+int dflash_qk_norm_rope_workspace(const dflash_attn* attn, size_t* bytes);
+
+/*   q, k            as given to dflash_qk_norm_rope (before norm and rotation)
+ *   d_q, d_k        device, as q and k: gradients of its outputs
+ *   dq_out, dk_out  device: gradients of q and k; may be d_q and d_k or q and k
+ *                   themselves
+ *   d_q_norm,       device fp32 [head_dim]: the gains' gradients, written (not
+ *   d_k_norm        added to); NULL iff q (k) is
+ *   workspace       device, 16-byte aligned, the caller's until the work is done
+ * Every sum is taken in an order that depends on the sizes alone.
+ * Errors: _ARG, _SHAPE, _CAPACITY (workspace), _CUDA. */
+int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const dflash_heads* q,
+                                 const dflash_heads* k, const void* q_norm_w,
+                                 const void* k_norm_w, const int32_t* positions,
+                                 const dflash_heads* d_q, const dflash_heads* d_k,
+                                 const dflash_heads* dq_out, const dflash_heads* dk_out,
+                                 float* d_q_norm, float* d_k_norm, void* workspace,
+                                 size_t workspace_bytes, dflash_stream stream);
+
+/* Global norm of many gradients, and clipping by it.  Needs no layer (no
+ * counterpart on the pages).
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   clipping: where norm > max_norm, out = g * (max_norm / norm); otherwise,
+ *   and where the norm is not finite (an infinity or NaN among the gradients,
+ *   which the caller finds in `norm`), out = g.
+ *   n_tensors   at most 2^20; may be 0 (norm 0)
+ *   grads, out  host arrays of device pointers, aligned to their types; out
+ *               NULL: in place.  What is written must not overlap anything
+ *               else that is read or written (_ARG): each tensor is given once.
+ *   counts      host: elements of each tensor, dense; may be 0 (the pointer
+ *               may then be NULL)
+ *   dtypes      host: DFLASH_BF16 or DFLASH_FP32 each; out has the same
+ *   max_norm    >= 0; may be infinite
+ *   norm        device fp32
+ *   workspace   device, 16-byte aligned, the caller's until the work is done
+ * Squares are added in fp64 above groups of 64, in an order that depends on
+ * the sizes and addresses' alignment alone; magnitudes over the whole fp32
+ * range count.  Gradients that need no clipping in place are only read.
+ * Work goes to the current device.
+ * Errors: _ARG, _CAPACITY (workspace), _MEMORY, _CUDA. */
+int dflash_grad_norm_workspace(int n_tensors, size_t* bytes);
+int dflash_grad_norm(int n_tensors, const void* const* grads, const int64_t* counts,
+                     const int32_t* dtypes, float* norm, void* workspace,
+                     size_t workspace_bytes, dflash_stream stream);
+int dflash_clip_grad_norm(int n_tensors, const void* const* grads, void* const* out,
+                          const int64_t* counts, const int32_t* dtypes, double max_norm,
+                          float* norm, void* workspace, size_t workspace_bytes,
+                          dflash_stream stream);
 
 /* Kernels this library has launched in this process so far, over every
  * layer, cache and device (a launch that returned an error counts too).  A

@@ -1,0 +1,204 @@
+"""Per-head norm and rotation of queries and keys and its gradient on the GPU,
+against the definition in 64 bits.
+
+Tolerance: a stored value is off by half a step of its type.  Before that, in
+fp32 (step 2^-24 of the value): the sum of squares takes at most 13 additions
+and products, halved by the root, then mean, eps, root and quotient (4), gain
+and 1/rms (2), the rotation's factor, product and addition (3): below 20 * 2^-24
+of |z_j| + |z_{j+d/2}|.  The gradient's terms pass the same steps once more and
+the sum of products: below 40 * 2^-24 of the terms' sizes.  A gain's gradient
+adds 64 sums of at most 4 such terms in sequence: 128 * 2^-24 of the terms'
+sizes together."""
+import pytest
+import torch
+
+from block_diffusion_draft_gb300 import DFlashAttention
+import train_reference as R
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+U = 2.0 ** -24
+MAXPOS, THETA, EPS = 70000, 1e6, 1e-6
+
+
+def layer(nq, nkv, d, dtype):
+    z = lambda *s: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    g = torch.Generator().manual_seed(nq + d)
+    gain = lambda: (1 + 0.2 * torch.randn(d, generator=g)).to(dtype)  # noqa: E731
+    w = dict(wq=z(nq * d, 128), wk=z(nkv * d, 128), wv=z(nkv * d, 128), wo=z(128, nq * d),
+             q_norm=gain(), k_norm=gain())
+    return DFlashAttention(w, hidden=128, n_heads=nq, n_kv_heads=nkv, head_dim=d, rms_eps=EPS,
+                           rope_theta=THETA, max_position=MAXPOS, dtype=dtype), w
+
+
+def close(got, want, size, dtype, steps, what):
+    got = got.detach().double().cpu()
+    tol = HALF[dtype] * want.abs() * (1 + 2 ** -8) + steps * U * size
+    bad = (got - want).abs() > tol
+    assert not bad.any(), f"{what}: {((got - want).abs() / tol).max()} of the tolerance"
+
+
+def case(B, rows, nq, nkv, d, dtype, layout, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, rows, nq + 2 * nkv, d, generator=g)
+    x = (x * torch.exp(torch.randn(B, rows, nq + 2 * nkv, 1, generator=g))).to(dtype).cuda()
+    q, k = x[:, :, :nq], x[:, :, nq:nq + nkv]
+    if layout == "dense":
+        q, k = q.contiguous(), k.contiguous()
+    pos = torch.randint(0, MAXPOS, (B, rows), generator=g, dtype=torch.int32)
+    dq = torch.randn(B, rows, nq, d, generator=g).to(dtype).cuda()
+    dk = torch.randn(B, nkv, rows + 3, d, generator=g).to(dtype).cuda()[:, :, 3:].transpose(1, 2)
+    return q, k, pos, dq, dk
+
+
+SHAPES = [(1, 1, 1, 1, 128, torch.bfloat16), (1, 16, 32, 8, 128, torch.bfloat16),
+          (3, 37, 7, 1, 128, torch.bfloat16), (2, 129, 9, 3, 128, torch.bfloat16),
+          (1, 1, 4, 2, 64, torch.float32), (2, 65, 6, 2, 64, torch.float32),
+          (1, 33, 5, 5, 128, torch.float32), (2, 19, 4, 2, 80, torch.float32),
+          (1, 7, 3, 1, 2, torch.float32), (1, 5, 2, 1, 256, torch.float32),
+          (2, 11, 3, 3, 34, torch.float32)]
+
+
+@pytest.mark.parametrize("layout", ["dense", "slices"])
+@pytest.mark.parametrize("B,rows,nq,nkv,d,dtype", SHAPES)
+def test_forward_and_gradient_equal_the_definition(B, rows, nq, nkv, d, dtype, layout):
+    attn, w = layer(nq, nkv, d, dtype)
+    q, k, pos, dq, dk = case(B, rows, nq, nkv, d, dtype, layout, B + rows)
+    gq, gk = w["q_norm"].cuda(), w["k_norm"].cuda()
+    keys = torch.full((B, nkv, rows + 5, d), 7.0, device="cuda", dtype=dtype)
+    q_out, k_out = attn.qk_norm_rope(q, k, pos.cuda(), gq, gk,
+                                     k_out=keys[:, :, 5:].transpose(1, 2))
+    same = attn.qk_norm_rope(q, k, pos.cuda())  # the layer's own gains
+    res = attn.qk_norm_rope_backward(q, k, pos.cuda(), gq, gk, dq, dk)
+    again = attn.qk_norm_rope_backward(q, k, pos.cuda(), None, None, dq, dk)
+    torch.cuda.synchronize()
+    assert (keys[:, :, :5] == 7.0).all()
+    assert torch.equal(same[0], q_out) and torch.equal(same[1], k_out)
+    assert all(torch.equal(a, b) for a, b in zip(res, again))
+    f = lambda t: t.double().cpu()  # noqa: E731
+    for x, gain, dy, y, dx, dg, name in ((q, gq, dq, q_out, res[0], res[2], "q"),
+                                         (k, gk, dk, k_out, res[1], res[3], "k")):
+        want, size = R.qk_rope(f(x), f(gain), pos, THETA, EPS)
+        close(y, want, size, dtype, 20, name)
+        want, wdg, size, gsize = R.qk_rope_backward(f(x), f(gain), pos, THETA, EPS, f(dy))
+        close(dx, want, size, dtype, 40, "d" + name)
+        close(dg, wdg, gsize, torch.float32, 128, "gain of " + name)
+    assert attn.device_error() == 0
+
+
+def test_unaligned_fp32_rows_and_odd_strides():
+    attn, w = layer(3, 1, 64, torch.float32)
+    g = torch.Generator().manual_seed(5)
+    wide = torch.randn(2, 9, 4 * 64 + 3, generator=g).cuda()
+    x = wide[:, :, 1:1 + 256].unflatten(-1, (4, 64))
+    q, k = x[:, :, :3], x[:, :, 3:]
+    pos = torch.randint(0, MAXPOS, (2, 9), generator=g, dtype=torch.int32)
+    q_out, k_out = attn.qk_norm_rope(q, k, pos.cuda())
+    dense = attn.qk_norm_rope(q.contiguous(), k.contiguous(), pos.cuda())
+    for x, gain, y in ((q, "q_norm", q_out), (k, "k_norm", k_out), (q, "q_norm", dense[0])):
+        want, size = R.qk_rope(x.double().cpu(), w[gain].double(), pos, THETA, EPS)
+        close(y, want, size, torch.float32, 20, gain)
+
+
+def test_only_keys_in_place_and_broadcast_gradient():
+    attn, w = layer(4, 2, 128, torch.bfloat16)
+    q, k, pos, _, _ = case(2, 21, 4, 2, 128, torch.bfloat16, "dense", 3)
+    none, k_out = attn.qk_norm_rope(None, k, pos.cuda())
+    both = attn.qk_norm_rope(q, k, pos.cuda())
+    assert none is None and torch.equal(k_out, both[1])
+    kk = k.clone()
+    attn.qk_norm_rope(None, kk, pos.cuda(), k_out=kk)
+    assert torch.equal(kk, both[1])
+    one = torch.ones(1, 1, 1, 128, device="cuda", dtype=torch.bfloat16)
+    wide, dense = one.expand(2, 21, 4, 128), one.repeat(2, 21, 4, 1)
+    a = attn.qk_norm_rope_backward(q, None, pos.cuda(), None, None, wide, None)
+    b = attn.qk_norm_rope_backward(q, None, pos.cuda(), None, None, dense, None, dq_out=dense)
+    assert a[1] is None and a[3] is None
+    assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])
+
+
+def test_nothing_to_do_and_positions_outside():
+    attn, _ = layer(4, 2, 128, torch.bfloat16)
+    z = torch.zeros(0, 5, 4, 128, device="cuda", dtype=torch.bfloat16)
+    pos = torch.zeros(0, 5, device="cuda", dtype=torch.int32)
+    q_out, _ = attn.qk_norm_rope(z, None, pos)
+    assert q_out.shape == z.shape
+    _, _, dg, _ = attn.qk_norm_rope_backward(z, None, pos, None, None, z, None)
+    assert (dg == 0).all()
+    q = torch.randn(1, 3, 4, 128, device="cuda").bfloat16()
+    far = torch.tensor([[-5, MAXPOS - 1, MAXPOS + 7]], device="cuda", dtype=torch.int32)
+    near = torch.tensor([[0, MAXPOS - 1, MAXPOS - 1]], device="cuda", dtype=torch.int32)
+    a, b = attn.qk_norm_rope(q, None, far)[0], attn.qk_norm_rope(q, None, near)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    assert attn.device_error() == 2 and attn.device_error() == 0
+
+
+def test_non_finite_heads_stay_by_themselves():
+    attn, _ = layer(4, 2, 128, torch.bfloat16)
+    q, k, pos, dq, dk = case(2, 9, 4, 2, 128, torch.bfloat16, "dense", 8)
+    clean = attn.qk_norm_rope(q, k, pos.cuda())[0].clone()
+    q[1, 3, 2, 5] = float("nan")
+    q[0, 2, 0, 0] = float("inf")
+    got = attn.qk_norm_rope(q, k, pos.cuda())[0]
+    bad = torch.zeros(2, 9, 4, dtype=torch.bool, device="cuda")
+    bad[1, 3, 2] = bad[0, 2, 0] = True
+    assert torch.equal(got[~bad], clean[~bad])
+    assert torch.isnan(got[bad]).any(-1).all()
+
+
+def test_another_stream_and_a_replayed_graph():
+    attn, _ = layer(8, 2, 128, torch.bfloat16)
+    q, k, pos, dq, dk = case(2, 50, 8, 2, 128, torch.bfloat16, "slices", 9)
+    p = pos.cuda()
+    want = attn.qk_norm_rope(q, k, p) + attn.qk_norm_rope_backward(q, k, p, None, None, dq, dk)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = attn.qk_norm_rope(q, k, p) + attn.qk_norm_rope_backward(q, k, p, None, None, dq, dk)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs = []
+    for _ in range(2):  # two graphs, replayed on two streams at a time
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = attn.qk_norm_rope(q, k, p)
+            out += attn.qk_norm_rope_backward(q, k, p, None, None, dq, dk)
+        graphs.append((graph, out))
+    other = torch.cuda.Stream()
+    for _ in range(20):
+        for t in graphs[0][1] + graphs[1][1]:
+            t.zero_()
+        torch.cuda.synchronize()
+        for (graph, _), s in zip(graphs, (side, other)):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_refusals():
+    attn, _ = layer(4, 2, 128, torch.bfloat16)
+    q, k, pos, dq, dk = case(2, 9, 4, 2, 128, torch.bfloat16, "dense", 8)
+    p = pos.cuda()
+    bad = [lambda: attn.qk_norm_rope(None, None, p), lambda: attn.qk_norm_rope(q, k, p.long()),
+           lambda: attn.qk_norm_rope(q, k, p[:1]), lambda: attn.qk_norm_rope(q.float(), k, p),
+           lambda: attn.qk_norm_rope(q[:, :, :3], k, p), lambda: attn.qk_norm_rope(q.cpu(), k, p),
+           lambda: attn.qk_norm_rope(q.transpose(2, 3).contiguous().transpose(2, 3), k, p),
+           lambda: attn.qk_norm_rope(None, k, p, q_out=q),
+           lambda: attn.qk_norm_rope(q, k, p, torch.ones(64, device="cuda").bfloat16()),
+           lambda: attn.qk_norm_rope_backward(q, k, p, None, None, dq, None)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    from block_diffusion_draft_gb300 import DFlashError
+    wide = torch.zeros(2, 9, 4 * 128 + 4, device="cuda", dtype=torch.bfloat16)
+    odd = wide[:, :, 4:].unflatten(-1, (4, 128))
+    for f in (lambda: attn.qk_norm_rope(odd, None, p),
+              lambda: attn.qk_norm_rope(q, None, p, q_out=q[:, :1].expand(2, 9, 4, 128)),
+              lambda: attn.qk_norm_rope(q, None, p, q_out=wide.view(-1).as_strided(
+                  (2, 9, 4, 128), (9 * 512, 448, 128, 1)))):
+        with pytest.raises(DFlashError, match="ARG"):
+            f()
