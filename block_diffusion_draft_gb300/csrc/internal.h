@@ -151,6 +151,10 @@ size_t gemm_scratch_bytes(int epi, int rows0, int rows1, int n, int k, int q_col
 int gemm_f32_slices(int rows, int n, int k, int num_sms);
 int make_tmap_bf16_rows(CUtensorMap* map, const void* ptr, long long rows,
                         int cols, int box_rows);
+// a [rows][cols] tensor of 2-byte (bf16) or 4-byte (fp32) elements, rows
+// `pitch` elements apart, read or written in boxes of 128 bytes by box_rows
+int make_tmap_2d(CUtensorMap* map, const void* ptr, int elem, long long rows, long long cols,
+                 long long pitch, int box_cols, int box_rows);
 
 // ----------------------------------------------------------- attention
 // Per-sequence key ranges and the work split of an inference attention call.

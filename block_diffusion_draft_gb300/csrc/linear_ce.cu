@@ -1,0 +1,1099 @@
+// linear_ce.cu -- cross entropy of a linear head over a large vocabulary,
+// and its gradients, without the logits of more than a piece of it.
+//
+//   z = x w^T,  nll = logsumexp(z) - z_t,
+//   dx = d * (sum_v p_v w_v - w_t),  dw_v = sum_rows d * (p_v - [v = t]) * x.
+//
+// Rows without a target are taken out first (compact, gather), so that they
+// cost nothing and nothing of theirs reaches a sum.  One GEMM kernel with
+// different operand layouts and epilogues does the products:
+//   LSE   x w^T of all columns; per row and 256 columns the largest logit and
+//         the sum of exponentials relative to it
+//   EXP   x w^T of one piece of columns; e = 2^(z log2 e - ref) in bf16 with a
+//         reference per row, their sums and the largest logit
+//   ACC   sum_v e_v w_v of the piece, added to an fp32 buffer
+//   GRAD  x w^T of one piece again, now with the row's lse known:
+//         d * (p - [v = t]) in bf16
+//   OUT   its transpose times x: dw's rows of the piece
+// The exponentials need no row maximum: a sum of products is linear in them,
+// so dx needs the logits once (EXP, ACC: 4 N V H operations) and is divided by
+// the row's sum at the end.  The reference is the target's logit; a row in
+// whose piece a logit lies more than 2^80 above it is done again with its
+// largest one (update and repair kernels, which end at once otherwise).
+//
+// The target's column is left out of every sum of exponentials and added
+// where the results are written: 1 - p_t is then a quotient of sums without
+// cancellation, also for a row that is sure of its target.
+#include <algorithm>
+
+#include "../../include/dflash_attn.h"
+#include "handles.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace df {
+namespace {
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int kThreads = 192;  // producer, MMA and four epilogue warps
+constexpr uint32_t A_BYTES = BM * BK * 2;
+constexpr uint32_t SLAB = 4096;  // 32 rows of 128 bytes: what a warp stores at a time
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kRefSlack = 80.f;  // binades that a logit may lie above its row's reference
+
+// CG CTAs work on one tile of CG * 128 rows and 256 columns.
+template <int CG>
+struct Geo {
+  static constexpr uint32_t B_BYTES = BN / CG * BK * 2;
+  static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + 8 * SLAB + 256;
+};
+
+enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
+
+struct CeGemm {
+  const int* n_rows;   // device: rows with a target
+  int m_tiles;         // OUT: tiles of the piece's columns
+  int n_tiles, n_kb, splits;
+  int v0;              // first column of the piece
+  int vocab, hidden;
+  int rows_pad;
+  const float* ref2;   // EXP: the rows' references; GRAD: their lse, log2 units
+  const int* target;
+  const float* d;      // GRAD: gradients of the rows' nll
+  const float* miss;   // GRAD: 1 - p_t
+  float* part_m;       // [tile][rows_pad], log2 units
+  float* part_s;
+  const int* repair;   // EXP: null, or flags of 32-row groups: only their tiles
+  int add;             // ACC: the buffer holds earlier pieces
+  int* err;
+};
+
+// ------------------------------------------------------------ PTX for pairs
+template <int CG>
+DF_DEV void tmem_alloc_cg(uint32_t* dst, uint32_t cols) {
+  if (CG == 1) {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(dst)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+
+template <int CG>
+DF_DEV void tmem_dealloc_cg(uint32_t t, uint32_t cols) {
+  if (CG == 1)
+    tmem_dealloc(t, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols)
+                 : "memory");
+}
+
+// A box into this CTA's shared memory; its bytes are counted on the barrier at
+// shared::cluster address `bar` (with pairs: the first CTA's).
+template <int CG>
+DF_DEV void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes."
+        "cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <int CG>
+DF_DEV void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (CG == 1)
+    tc_mma_bf16(d, a, b, idesc, acc);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// one arrival on `bar` (with pairs: in both CTAs) once all MMAs so far are done
+template <int CG>
+DF_DEV void commit(uint64_t* bar) {
+  if (CG == 1)
+    tc_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
+        "b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+DF_DEV void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+DF_DEV void store_box(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                   "l"(map),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+
+DF_DEV void add_box(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], "
+      "[%3];" ::"l"(map),
+      "r"(x), "r"(y), "r"(smem_u32(src))
+      : "memory");
+}
+
+DF_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+DF_DEV void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+DF_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 32 fp32 columns of this thread's TMEM lane; the wait is part of the
+// statement, so that no use of the values comes before it
+DF_DEV void tmem_read32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// D fp32, A and B bf16, K-major or MN-major each
+constexpr uint32_t idesc_ce(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ------------------------------------------------------------------- GEMM
+struct Tile {
+  int m, n, split, k0, k1;
+};
+
+// Tiles in groups of 8 row tiles, column tiles outside: the CTAs that run at
+// the same time share their operands in L2.
+DF_DEV Tile tile_at(const CeGemm& p, int m_tiles, int n_kb, int u) {
+  constexpr int GM = 8;
+  const int per_split = m_tiles * p.n_tiles;
+  Tile t;
+  t.split = u / per_split;
+  const int r = u - t.split * per_split;
+  const int g = r / (GM * p.n_tiles), gm = min(GM, m_tiles - g * GM);
+  const int rem = r - g * GM * p.n_tiles;
+  t.n = rem / gm;
+  t.m = g * GM + rem - t.n * gm;
+  t.k0 = (int)((long long)n_kb * t.split / p.splits);
+  t.k1 = (int)((long long)n_kb * (t.split + 1) / p.splits);
+  return t;
+}
+
+// Whether a repair has to compute this row tile again: one of its 32-row
+// groups is flagged.
+template <int CG>
+DF_DEV bool wanted(const CeGemm& p, const Tile& t) {
+  if (p.repair == nullptr) return true;
+  bool any = false;
+  for (int i = 0; i < CG * BM / 32; ++i) any |= __ldcg(p.repair + t.m * (CG * BM / 32) + i) != 0;
+  return any;
+}
+
+// The 32-column pieces of a warp's output go through a 4 KB slab in the layout
+// of the 128-byte swizzle: 16-byte chunk c of row r at place c ^ (r % 8).
+struct Slabs {
+  uint8_t* base;  // two slabs of this warp
+  int next;
+  // the slab to fill, once the copy that last read it has
+  DF_DEV uint8_t* begin(int lane) {
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    return base + next * SLAB;
+  }
+  DF_DEV void end() { next ^= 1; }
+};
+
+DF_DEV void slab_put(uint8_t* slab, int lane, int chunk, uint4 v) {
+  *reinterpret_cast<uint4*>(slab + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
+}
+
+template <int EPI, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
+                   const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CeGemm p) {
+  using G = Geo<CG>;
+  constexpr bool kAmn = EPI == OUT, kBmn = EPI == ACC || EPI == OUT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* slabs = smem + G::STAGES * G::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + 8 * SLAB);
+  uint64_t* empty = full + G::STAGES;
+  uint64_t* acc_full = empty + G::STAGES;  // [2]
+  uint64_t* acc_empty = acc_full + 2;      // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4 * CG);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_a);
+    prefetch_tmap(&tm_b);
+    prefetch_tmap(&tm_out);
+  }
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (CG == 2) cluster_sync();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_sync();
+  const int rows = __ldcg(p.n_rows);
+  const int m_tiles = EPI == OUT ? p.m_tiles : (rows + CG * BM - 1) / (CG * BM);
+  const int n_kb = EPI == OUT ? (rows + BK - 1) / BK : p.n_kb;
+  const int units = m_tiles * p.n_tiles * p.splits;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0;
+      bool alive = true;
+      for (int u = first; alive && u < units; u += stride) {
+        const Tile t = tile_at(p, m_tiles, n_kb, u);
+        if (!wanted<CG>(p, t)) continue;
+        const int m0 = (t.m * CG + rank) * BM, n0 = t.n * BN + rank * (BN / CG);
+        for (int kb = t.k0; kb < t.k1; ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, p.err)) {
+            alive = false;
+            break;
+          }
+          // (the first CTA's barrier counts the bytes of both)
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * G::STAGE);
+          const uint32_t bar =
+              CG == 2 ? cluster_map(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+          const uint32_t a = smem_u32(smem + s * G::STAGE), b = a + A_BYTES;
+          if (kAmn) {
+#pragma unroll
+            for (int i = 0; i < BM / 64; ++i)
+              load_box<CG>(a + i * 8192, &tm_a, bar, m0 + 64 * i, kb * BK);
+          } else {
+            load_box<CG>(a, &tm_a, bar, kb * BK, m0);
+          }
+          if (kBmn) {
+#pragma unroll
+            for (int i = 0; i < BN / CG / 64; ++i)
+              load_box<CG>(b + i * 8192, &tm_b, bar, n0 + 64 * i,
+                           (EPI == ACC ? p.v0 : 0) + kb * BK);
+          } else {
+            load_box<CG>(b, &tm_b, bar, kb * BK, p.v0 + n0);
+          }
+          if (++s == (uint32_t)G::STAGES) s = 0, ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_ce(CG * BM, BN, kAmn, kBmn);
+      uint32_t s = 0, ph = 0, tc = 0;
+      bool alive = true;
+      for (int u = first; alive && u < units; u += stride) {
+        const Tile t = tile_at(p, m_tiles, n_kb, u);
+        if (t.k0 >= t.k1 || !wanted<CG>(p, t)) continue;
+        const uint32_t buf = tc & 1, use = tc >> 1;
+        ++tc;
+        if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * BN;
+        for (int kb = t.k0; kb < t.k1; ++kb) {
+          if (!mbar_wait(&full[s], ph, abort_flag, p.err)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + s * G::STAGE), b = a + A_BYTES;
+          const uint64_t da = kAmn ? sdesc_sw128(a, 8192, 1024) : sdesc_sw128(a, 16, 1024);
+          const uint64_t db = kBmn ? sdesc_sw128(b, 8192, 1024) : sdesc_sw128(b, 16, 1024);
+          // a K step of 16: 2 groups of 8 rows, or 32 bytes of every row
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma<CG>(d, da + (uint64_t)(kk * (kAmn ? 2048 : 32) >> 4),
+                    db + (uint64_t)(kk * (kBmn ? 2048 : 32) >> 4), idesc,
+                    (kb > t.k0 || kk > 0) ? 1u : 0u);
+          commit<CG>(&empty[s]);
+          if (++s == (uint32_t)G::STAGES) s = 0, ph ^= 1;
+        }
+        commit<CG>(&acc_full[buf]);
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    Slabs out{slabs + q * 2 * SLAB, 0};
+    uint32_t tc = 0;
+    for (int u = first; u < units; u += stride) {
+      const Tile t = tile_at(p, m_tiles, n_kb, u);
+      if (!wanted<CG>(p, t)) continue;
+      const bool any = t.k0 < t.k1;  // otherwise the tile is zero
+      const int row0 = (t.m * CG + rank) * BM + q * 32, row = row0 + lane;
+      const bool live = EPI == ACC || EPI == OUT || row < rows;
+      // this row's part of an epilogue that looks at logits
+      int tgt = -1;
+      float ref = 0.f, sc = 0.f, miss = 0.f;
+      if (EPI <= GRAD && live) {
+        tgt = __ldcg(p.target + row) - p.v0 - t.n * BN;  // its column in this tile
+        if (EPI != LSE) ref = __ldcg(p.ref2 + row);
+        if (EPI == GRAD) {
+          sc = __ldcg(p.d + row);
+          miss = __ldcg(p.miss + row);
+        }
+      }
+      const uint32_t buf = tc & 1, use = tc >> 1;
+      if (any) {
+        ++tc;
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], use & 1, abort_flag, p.err)))
+          break;
+        tc_fence_after();
+      }
+      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
+      const int cols = EPI <= GRAD ? p.vocab - p.v0 - t.n * BN : BN;  // that exist
+      float mx = kNegInf, sum = 0.f;
+      uint8_t* slab = nullptr;
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        float v[32];
+        if (any) {
+          tmem_read32(trow + c * 32, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (c == BN / 32 - 1 && any) {  // read: back to the MMA warp
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) arrive_cluster(cluster_map(smem_u32(&acc_empty[buf]), 0));
+            else mbar_arrive(&acc_empty[buf]);
+          }
+        }
+        if (EPI <= GRAD) {
+          // logits of the target and of columns that do not exist: -inf
+          const bool has = tgt >= c * 32 && tgt < c * 32 + 32;
+          if (c * 32 + 32 > cols || __any_sync(0xffffffffu, has)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i >= cols || c * 32 + i == tgt) v[i] = kNegInf;
+          }
+          if (EPI != GRAD) {
+            float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], v[i]);
+            const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * kLog2e;
+            if (EPI == LSE) {
+              const float now = fmaxf(mx, top);
+              if (now > kNegInf) sum *= fast_exp2(mx - now);
+              ref = now > kNegInf ? now : 0.f;
+            }
+            mx = fmaxf(mx, top);
+          }
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = fast_exp2(fmaf(v[i], kLog2e, -ref));
+            if (EPI != GRAD) s[i & 3] += v[i];
+          }
+          sum += (s[0] + s[1]) + (s[2] + s[3]);
+          if (EPI == LSE) continue;
+          if (EPI == GRAD) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= sc;
+            if (__any_sync(0xffffffffu, has)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i == tgt) v[i] = -sc * miss;
+            }
+          }
+          if (!live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+        }
+        if (EPI == ACC) {
+          slab = out.begin(lane);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            slab_put(slab, lane, j,
+                     make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+        } else {
+          if ((c & 1) == 0) slab = out.begin(lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            slab_put(slab, lane, (c & 1) * 4 + j,
+                     make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+          if ((c & 1) == 0) continue;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (EPI == ACC) {
+            const int x = t.n * BN + c * 32;
+            if (x < p.hidden) {
+              if (p.add) add_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
+              else store_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
+            }
+          } else if (EPI == OUT) {
+            const int x = t.n * BN + (c - 1) * 32, y = p.v0 + row0;
+            if (x < p.hidden && y < p.vocab) store_box(&tm_out, slab, x, y);
+          } else {
+            store_box(&tm_out, slab, t.n * BN + (c - 1) * 32, row0);
+          }
+          bulk_commit();
+        }
+        out.end();
+      }
+      if (EPI == LSE || EPI == EXP) {
+        if (live) {
+          const size_t at = (size_t)(p.v0 / BN + t.n) * p.rows_pad + row;
+          p.part_m[at] = mx;
+          p.part_s[at] = sum;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // no CTA leaves while its pair's copies, products or arrivals may reach it
+  if (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ small kernels
+struct CeRows {
+  int rows, vocab, hidden, rows_pad;
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w;
+  long long x_stride, w_stride;
+  const int* targets;
+  const float* d_nll;  // null: forward only
+  int* n;              // rows with a target
+  int* err;
+  int* place;          // [rows]: compact row or -1
+  int* row_of;         // [rows_pad]: row of a compact one
+  int* target;         // compact
+  float* z_t;          // compact: the target's logit
+  float* ref2;         // compact: reference, log2 units
+  float* d;            // compact
+  __nv_bfloat16* xc;   // [rows_pad][hidden]
+};
+
+// Compact numbers of the rows that have a target, in their order.
+__global__ void __launch_bounds__(1024) ce_compact_kernel(const __grid_constant__ CeRows a) {
+  __shared__ int warp_n[32], base;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_sync();
+  if (threadIdx.x == 0) base = 0;
+  __syncthreads();
+  for (int r0 = 0; r0 < a.rows; r0 += 1024) {
+    const int r = r0 + threadIdx.x;
+    const int t = r < a.rows ? a.targets[r] : -1;
+    const bool has = t >= 0 && t < a.vocab;
+    const uint32_t b = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) warp_n[warp] = __popc(b);
+    __syncthreads();
+    int at = base + __popc(b & ((1u << lane) - 1u)), all = 0;
+    for (int w = 0; w < 32; ++w) {
+      at += w < warp ? warp_n[w] : 0;
+      all += warp_n[w];
+    }
+    if (r < a.rows) a.place[r] = has ? at : -1;
+    if (has) a.row_of[at] = r;
+    __syncthreads();
+    if (threadIdx.x == 0) base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    *a.n = base;
+    *a.err = 0;
+  }
+}
+
+DF_DEV float dot8(uint4 a, uint4 b) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s += __uint_as_float(u[i] << 16) * __uint_as_float(v[i] << 16);
+    s += __uint_as_float(u[i] & 0xffff0000u) * __uint_as_float(v[i] & 0xffff0000u);
+  }
+  return s;
+}
+
+// One CTA per compact row: its copy of x, its target's logit.  Rows that fill
+// the last 256 are zero.
+__global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ CeRows a) {
+  __shared__ float sm[8];
+  grid_dep_sync();
+  const int r = blockIdx.x, n = __ldcg(a.n);
+  if (r >= (n + 255) / 256 * 256) return;
+  uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)r * a.hidden);
+  const int n8 = a.hidden / 8;
+  if (r >= n) {
+    for (int i = threadIdx.x; i < n8; i += 256) dst[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int row = __ldcg(a.row_of + r), t = a.targets[row];
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.x_stride);
+  const uint4* w = reinterpret_cast<const uint4*>(a.w + t * a.w_stride);
+  float s = 0.f;
+  for (int i = threadIdx.x; i < n8; i += 256) {
+    const uint4 v = __ldg(x + i);
+    s += dot8(v, __ldg(w + i));
+    dst[i] = v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float z = 0.f;
+    for (int i = 0; i < 8; ++i) z += sm[i];
+    a.target[r] = t;
+    a.z_t[r] = z;
+    a.ref2[r] = z * kLog2e;
+    if (a.d_nll != nullptr) a.d[r] = a.d_nll[row];
+  }
+}
+
+struct CeSums {
+  const float* part_m;  // forward: [tile][rows_pad]
+  const float* part_s;
+  const float* hist;    // gradient: [piece][rows_pad] the references of the tiles, log2 units
+  int tiles, piece_tiles;
+  float* nll;           // [rows]
+  float* lse;
+  float* inv;           // compact: 1 / sum of exponentials relative to the last reference
+  float* miss;          // compact: 1 - p_t
+  float* lse2;          // compact: lse in log2 units
+};
+
+// nll and lse of 32 rows from their tiles' sums, 32 slices of the tiles each,
+// joined in a fixed order.
+__global__ void __launch_bounds__(1024)
+    ce_combine_kernel(const __grid_constant__ CeRows a, const __grid_constant__ CeSums s) {
+  __shared__ float sm[32][33], ss[32][33];
+  grid_dep_sync();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  const int c = row < a.rows ? __ldcg(a.place + row) : -1;
+  float m = kNegInf, sum = 0.f;
+  if (c >= 0) {
+    for (int t = slice; t < s.tiles; t += 32) {
+      const float ts = __ldcg(s.part_s + (size_t)t * a.rows_pad + c);
+      const float tm = s.hist != nullptr
+                           ? __ldcg(s.hist + (size_t)(t / s.piece_tiles) * a.rows_pad + c)
+                           : __ldcg(s.part_m + (size_t)t * a.rows_pad + c);
+      if (ts == 0.f) continue;
+      const float now = fmaxf(m, tm);
+      sum = sum * fast_exp2(m - now) + ts * fast_exp2(tm - now);
+      m = now;
+    }
+  }
+  sm[slice][lane] = m;
+  ss[slice][lane] = sum;
+  __syncthreads();
+  if (slice != 0 || row >= a.rows) return;
+  const bool failed = __ldcg(a.err) != 0;  // a wait ran out: no number is right
+  if (c < 0) {
+    s.nll[row] = s.lse[row] = failed ? __int_as_float(0x7fc00000) : 0.f;
+    return;
+  }
+  const float z2 = __ldcg(a.z_t + c) * kLog2e;
+  float top = z2;
+  for (int i = 0; i < 32; ++i) top = fmaxf(top, sm[i][lane]);
+  float others = 0.f;  // relative to `top`
+  for (int i = 0; i < 32; ++i)
+    if (ss[i][lane] != 0.f) others += ss[i][lane] * fast_exp2(sm[i][lane] - top);
+  const float own = fast_exp2(z2 - top), total = others + own;
+  // where the target leads, log1p keeps what is left of a small loss
+  const float nll = top == z2 ? log1pf(others) : logf(total) + (top - z2) * kLn2;
+  const float nan = __int_as_float(0x7fc00000);
+  s.nll[row] = failed ? nan : nll;
+  s.lse[row] = failed ? nan : nll + __ldcg(a.z_t + c);
+  if (s.hist != nullptr) {
+    const float last = __ldcg(a.ref2 + c);  // the accumulated products' reference
+    s.inv[c] = failed ? nan : fast_exp2(last - top) / total;
+    s.miss[c] = others / total;
+    s.lse2[c] = top + log2f(total);
+  }
+}
+
+struct CeUpdate {
+  const int* n;
+  int rows_pad, hidden, first_tile, tiles, slices;
+  const float* part_m;
+  float* ref2;
+  float* hist;   // [rows_pad] of this piece
+  int* flag;     // [rows_pad / 32]
+  float* acc;    // [slices][rows_pad][hidden], earlier pieces; null: none
+};
+
+// After a piece's exponentials: rows whose largest logit leaves the range take
+// it as their reference, what they hold of earlier pieces follows, and the
+// group is flagged for the repair.
+__global__ void __launch_bounds__(1024) ce_update_kernel(const __grid_constant__ CeUpdate a) {
+  __shared__ float sm[32][33], factor[32];
+  grid_dep_sync();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  const bool live = row < __ldcg(a.n);
+  float m = kNegInf;
+  if (live)
+    for (int t = slice; t < a.tiles; t += 32)
+      m = fmaxf(m, __ldcg(a.part_m + (size_t)(a.first_tile + t) * a.rows_pad + row));
+  sm[slice][lane] = m;
+  __syncthreads();
+  if (slice == 0) {
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, sm[i][lane]);
+    float f = 1.f;
+    if (live) {
+      const float ref = a.ref2[row];
+      const bool far = m - ref > kRefSlack;
+      f = far ? fast_exp2(ref - m) : 1.f;
+      if (far) a.ref2[row] = m;
+      a.hist[row] = far ? m : ref;
+    }
+    factor[lane] = f;
+    const bool any = __any_sync(0xffffffffu, f != 1.f);
+    if (lane == 0) a.flag[blockIdx.x] = any ? 1 : 0;
+  }
+  __syncthreads();
+  if (a.acc == nullptr) return;
+  for (int r = 0; r < 32; ++r) {
+    const float f = factor[r];
+    if (f == 1.f) continue;
+    for (int s = 0; s < a.slices; ++s) {
+      float* v = a.acc + ((size_t)s * a.rows_pad + blockIdx.x * 32 + r) * a.hidden;
+      for (int i = threadIdx.x; i < a.hidden; i += 1024) v[i] *= f;
+    }
+  }
+}
+
+// dx of one row from the accumulated products: d * (acc * inv - miss * w_t).
+__global__ void __launch_bounds__(256)
+    ce_finish_kernel(const __grid_constant__ CeRows a, const float* acc, int slices,
+                     const float* inv, const float* miss, __nv_bfloat16* dx) {
+  grid_dep_sync();
+  const int row = blockIdx.x, c = __ldcg(a.place + row), n8 = a.hidden / 8;
+  uint4* out = reinterpret_cast<uint4*>(dx + (size_t)row * a.hidden);
+  if (c < 0) {
+    for (int i = threadIdx.x; i < n8; i += 256) out[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float d = __ldcg(a.d + c), f = __ldcg(inv + c) * d, g = __ldcg(miss + c) * d;
+  const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
+  for (int i = threadIdx.x; i < n8; i += 256) {
+    float v[8] = {};
+    for (int s = 0; s < slices; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(
+                            acc + ((size_t)s * a.rows_pad + c) * a.hidden) + 2 * i;
+      const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
+      v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
+      v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
+    }
+    const uint4 t = __ldg(w + i);
+    const uint32_t u[4] = {t.x, t.y, t.z, t.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pack_bf16x2(v[2 * j] * f - g * __uint_as_float(u[j] << 16),
+                         v[2 * j + 1] * f - g * __uint_as_float(u[j] & 0xffff0000u));
+    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ----------------------------------------------------------------- the host
+constexpr size_t kPieceBytes = 512ull << 20;  // of a piece's exponentials
+constexpr int kMaxSplits = 16;
+
+struct Plan {
+  int cg, rows_pad, n_tiles;
+  int piece, pieces;   // columns of a piece (a multiple of 256)
+  int splits;          // of ACC's K
+  size_t place, row_of, target, z_t, ref2, d, inv, miss, lse2, hist, flag, xc, part_m, part_s, g,
+      acc, total;
+};
+
+// Splits of K for the products of few tiles: whole waves, and about 24
+// k-blocks' time for each wave's beginning and end.
+int acc_splits(int tiles, int n_kb, int units) {
+  double best_t = 1e30;
+  int best = 1;
+  for (int sp = 1; sp <= std::min(kMaxSplits, std::max(1, n_kb / 8)); ++sp) {
+    const int waves = (tiles * sp + units - 1) / units;
+    const double t = waves * ((double)n_kb / sp + 24.) + 4. * sp;
+    if (t < best_t - 1e-9) best_t = t, best = sp;
+  }
+  return best;
+}
+
+// The plan of a call goes by its sizes alone, so that the workspace can be
+// asked for without a GPU; 152 SMs are what it is made for.
+constexpr int kPlanSms = 152;
+
+Plan make_plan(int rows, int vocab, int hidden, int grads) {
+  Plan p{};
+  p.cg = rows <= BM ? 1 : 2;
+  p.rows_pad = (rows + 255) / 256 * 256;
+  p.n_tiles = (vocab + BN - 1) / BN;
+  const size_t most =
+      std::max<size_t>(4096, kPieceBytes / (2 * (size_t)p.rows_pad) / BN * BN);
+  p.pieces = (int)(((size_t)p.n_tiles * BN + most - 1) / most);
+  p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * BN;
+  p.pieces = (p.n_tiles * BN + p.piece - 1) / p.piece;
+  const int m_tiles = (rows + p.cg * BM - 1) / (p.cg * BM), h_tiles = (hidden + BN - 1) / BN;
+  p.splits = acc_splits(m_tiles * h_tiles, p.piece / BK, kPlanSms / p.cg);
+  size_t at = 256;  // n, err
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t pad = (size_t)p.rows_pad;
+  p.place = take((size_t)rows * 4);
+  p.row_of = take(pad * 4);
+  p.target = take(pad * 4);
+  p.z_t = take(pad * 4);
+  p.ref2 = take(pad * 4);
+  p.xc = take(pad * hidden * 2);
+  p.part_m = take(pad * p.n_tiles * 4);
+  p.part_s = take(pad * p.n_tiles * 4);
+  if (grads > 0) {
+    p.d = take(pad * 4);
+    p.inv = take(pad * 4);
+    p.miss = take(pad * 4);
+    p.lse2 = take(pad * 4);
+    p.hist = take(pad * p.pieces * 4);
+    p.flag = take(pad / 32 * 4);
+    p.g = take(pad * p.piece * 2);
+    p.acc = take(pad * p.splits * hidden * 4);
+  }
+  p.total = at;
+  return p;
+}
+
+int make_map(CUtensorMap* m, const void* p, bool f32, long long rows, long long cols,
+             long long pitch, int box_cols, int box_rows) {
+  return make_tmap_2d(m, p, f32 ? 4 : 2, rows, cols, pitch, box_cols, box_rows);
+}
+
+template <int EPI, int CG>
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
+                        const CeGemm& p, int units, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!done_on_device(attr_done)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        ce_gemm_kernel<EPI, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<CG>::SMEM);
+    if (e != cudaSuccess) return e;
+    mark_device(attr_done);
+  }
+  const int grid = std::max(1, std::min(units, sms / CG)) * CG;
+  return launch_pdl_cluster(ce_gemm_kernel<EPI, CG>, dim3(grid), dim3(kThreads), Geo<CG>::SMEM, s,
+                            (unsigned)CG, a, b, out, p);
+}
+
+template <int EPI>
+cudaError_t launch_gemm(int cg, const CUtensorMap& a, const CUtensorMap& b,
+                        const CUtensorMap& out, const CeGemm& p, int units, int sms,
+                        cudaStream_t s) {
+  return cg == 1 ? launch_gemm<EPI, 1>(a, b, out, p, units, sms, s)
+                 : launch_gemm<EPI, 2>(a, b, out, p, units, sms, s);
+}
+
+struct Call {
+  int rows, vocab, hidden;
+  const void* x;
+  int64_t x_stride;
+  const void* w;
+  int64_t w_stride;
+  const int32_t* targets;
+  const float* d_nll;
+  float* nll;
+  float* lse;
+  void* dx;
+  void* dw;
+};
+
+int device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? DFLASH_OK : api_fail(DFLASH_ERR_CUDA, "%s", cudaGetErrorString(e));
+}
+
+int check_sizes(int rows, int vocab, int hidden) {
+  if (rows < 0 || vocab <= 0 || hidden <= 0)
+    return api_fail(DFLASH_ERR_ARG, "rows must be >= 0, vocab and hidden positive");
+  if (hidden % 8 != 0) return api_fail(DFLASH_ERR_SHAPE, "hidden must be a multiple of 8");
+  if (rows > (1 << 20) || vocab > (1 << 24) || hidden > (1 << 16))
+    return api_fail(DFLASH_ERR_SHAPE, "at most 2^20 rows, 2^24 columns and hidden 2^16");
+  return DFLASH_OK;
+}
+
+bool misaligned(const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; }
+
+int check_call(const Call& c, bool grad, const void* ws, size_t ws_bytes) {
+  if (int r = check_sizes(c.rows, c.vocab, c.hidden)) return r;
+  if (c.rows > 0 && (c.x == nullptr || c.targets == nullptr || c.nll == nullptr ||
+                     c.lse == nullptr || (grad && (c.d_nll == nullptr || c.dx == nullptr))))
+    return api_fail(DFLASH_ERR_ARG, "null tensor");
+  if (c.w == nullptr) return api_fail(DFLASH_ERR_ARG, "null head");
+  if (misaligned(c.x, 15) || misaligned(c.w, 15) || misaligned(c.dx, 15) || misaligned(c.dw, 15))
+    return api_fail(DFLASH_ERR_ARG, "bf16 tensors must be 16-byte aligned");
+  if (misaligned(c.targets, 3) || misaligned(c.d_nll, 3) || misaligned(c.nll, 3) ||
+      misaligned(c.lse, 3))
+    return api_fail(DFLASH_ERR_ARG, "32-bit tensors must be aligned to their type");
+  if ((c.rows > 1 && (c.x_stride < c.hidden || c.x_stride % 8 != 0)) ||
+      (c.vocab > 1 && (c.w_stride < c.hidden || c.w_stride % 8 != 0)))
+    return api_fail(DFLASH_ERR_ARG, "row strides must be multiples of 8, at least hidden");
+  if (c.x_stride > (1LL << 32) || c.w_stride > (1LL << 32))
+    return api_fail(DFLASH_ERR_SHAPE, "row strides must be at most 2^32");
+  if (ws == nullptr || misaligned(ws, 255))
+    return api_fail(DFLASH_ERR_ARG, "workspace null or not on a 256-byte boundary");
+  size_t need = 0;
+  if (int r = dflash_linear_ce_workspace(c.rows, c.vocab, c.hidden, grad ? (c.dw ? 2 : 1) : 0,
+                                         &need))
+    return r;
+  if (ws_bytes < need)
+    return api_fail(DFLASH_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  return DFLASH_OK;
+}
+
+int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
+  if (int r = check_call(c, grad, ws, ws_bytes)) return r;
+  int sms = 0;
+  if (int r = device_sms(&sms)) return r;
+  cudaError_t e = cudaSuccess;
+  auto done = [&](const char* what) {
+    return e == cudaSuccess ? DFLASH_OK
+                            : api_fail(DFLASH_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  };
+  if (c.rows == 0) {
+    if (c.dw != nullptr)
+      e = cudaMemsetAsync(c.dw, 0, (size_t)c.vocab * c.hidden * 2, s);
+    return done("memset");
+  }
+  const Plan p = make_plan(c.rows, c.vocab, c.hidden, grad ? 1 : 0);
+  char* base = static_cast<char*>(ws);
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+  auto i32 = [&](size_t at) { return reinterpret_cast<int*>(base + at); };
+  const int pad = p.rows_pad, H = c.hidden, V = c.vocab;
+
+  CeRows a{};
+  a.rows = c.rows;
+  a.vocab = V;
+  a.hidden = H;
+  a.rows_pad = pad;
+  a.x = static_cast<const __nv_bfloat16*>(c.x);
+  a.w = static_cast<const __nv_bfloat16*>(c.w);
+  a.x_stride = c.x_stride;
+  a.w_stride = c.w_stride;
+  a.targets = c.targets;
+  a.d_nll = c.d_nll;
+  a.n = i32(0);
+  a.err = i32(4);
+  a.place = i32(p.place);
+  a.row_of = i32(p.row_of);
+  a.target = i32(p.target);
+  a.z_t = f32(p.z_t);
+  a.ref2 = f32(p.ref2);
+  a.d = f32(p.d);
+  a.xc = reinterpret_cast<__nv_bfloat16*>(base + p.xc);
+
+  // maps: x by rows and by channels, w the same, a piece's exponentials, the
+  // fp32 products, dw
+  const long long w_pitch = V > 1 ? c.w_stride : H;
+  CUtensorMap x_k, w_k, x_mn, w_mn, g_k, g_mn, g_out, acc_out, dw_out;
+  int bad = make_map(&x_k, a.xc, false, pad, H, H, 64, BM) |
+            make_map(&w_k, c.w, false, V, H, w_pitch, 64, BN / p.cg);
+  if (grad) {
+    const void* g = base + p.g;
+    bad |= make_map(&w_mn, c.w, false, V, H, w_pitch, 64, 64) |
+           make_map(&g_k, g, false, pad, p.piece, p.piece, 64, BM) |
+           make_map(&g_out, g, false, pad, p.piece, p.piece, 64, 32) |
+           make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, H, 32, 32);
+    if (c.dw != nullptr)
+      bad |= make_map(&x_mn, a.xc, false, pad, H, H, 64, 64) |
+             make_map(&g_mn, g, false, pad, p.piece, p.piece, 64, 64) |
+             make_map(&dw_out, c.dw, false, V, H, H, 64, 32);
+  }
+  if (bad != 0) return api_fail(DFLASH_ERR_CUDA, "tensor map encoding failed");
+
+  CeGemm gm{};
+  gm.n_rows = a.n;
+  gm.n_kb = (H + BK - 1) / BK;
+  gm.splits = 1;
+  gm.vocab = V;
+  gm.hidden = H;
+  gm.rows_pad = pad;
+  gm.ref2 = a.ref2;
+  gm.target = a.target;
+  gm.part_m = f32(p.part_m);
+  gm.part_s = f32(p.part_s);
+  gm.err = a.err;
+  CeSums sums{};
+  sums.part_m = gm.part_m;
+  sums.part_s = gm.part_s;
+  sums.tiles = p.n_tiles;
+  sums.piece_tiles = p.piece / BN;
+  sums.nll = c.nll;
+  sums.lse = c.lse;
+  const int m_tiles = (c.rows + p.cg * BM - 1) / (p.cg * BM);
+  const int h_tiles = (H + BN - 1) / BN;
+  const dim3 b1024(1024), b256(256), groups((c.rows + 31) / 32);
+
+  e = launch_pdl(ce_compact_kernel, dim3(1), b1024, 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(ce_gather_kernel, dim3(pad), b256, 0, s, a);
+  if (!grad) {
+    gm.n_tiles = p.n_tiles;
+    if (e == cudaSuccess)
+      e = launch_gemm<LSE>(p.cg, x_k, w_k, x_k, gm, m_tiles * p.n_tiles, sms, s);
+    if (e == cudaSuccess) e = launch_pdl(ce_combine_kernel, groups, b1024, 0, s, a, sums);
+    return done("cross entropy launch");
+  }
+
+  sums.hist = f32(p.hist);
+  sums.inv = f32(p.inv);
+  sums.miss = f32(p.miss);
+  sums.lse2 = f32(p.lse2);
+  CeUpdate up{};
+  up.n = a.n;
+  up.rows_pad = pad;
+  up.hidden = H;
+  up.slices = p.splits;
+  up.part_m = gm.part_m;
+  up.ref2 = a.ref2;
+  up.flag = i32(p.flag);
+  for (int i = 0; i < p.pieces && e == cudaSuccess; ++i) {
+    const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
+    CeGemm ex = gm;
+    ex.v0 = v0;
+    ex.n_tiles = tiles;
+    e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
+    up.first_tile = v0 / BN;
+    up.tiles = tiles;
+    up.hist = f32(p.hist) + (size_t)i * pad;
+    up.acc = i > 0 ? f32(p.acc) : nullptr;
+    if (e == cudaSuccess) e = launch_pdl(ce_update_kernel, dim3(pad / 32), b1024, 0, s, up);
+    ex.repair = up.flag;
+    if (e == cudaSuccess)
+      e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
+    CeGemm ac = gm;
+    ac.v0 = v0;
+    ac.n_tiles = h_tiles;
+    ac.n_kb = tiles * BN / BK;
+    ac.splits = p.splits;
+    ac.add = i > 0;
+    if (e == cudaSuccess)
+      e = launch_gemm<ACC>(p.cg, g_k, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
+  }
+  if (e == cudaSuccess) e = launch_pdl(ce_combine_kernel, groups, b1024, 0, s, a, sums);
+  if (e == cudaSuccess)
+    e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, f32(p.acc), p.splits,
+                   f32(p.inv), f32(p.miss), static_cast<__nv_bfloat16*>(c.dx));
+  for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
+    const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
+    CeGemm gr = gm;
+    gr.v0 = v0;
+    gr.n_tiles = tiles;
+    gr.ref2 = f32(p.lse2);
+    gr.d = a.d;
+    gr.miss = f32(p.miss);
+    e = launch_gemm<GRAD>(p.cg, x_k, w_k, g_out, gr, m_tiles * tiles, sms, s);
+    CeGemm ow = gm;
+    ow.v0 = v0;
+    ow.m_tiles = (tiles * BN + p.cg * BM - 1) / (p.cg * BM);
+    ow.n_tiles = h_tiles;
+    if (e == cudaSuccess)
+      e = launch_gemm<OUT>(p.cg, g_mn, x_mn, dw_out, ow, ow.m_tiles * h_tiles, sms, s);
+  }
+  return done("cross entropy launch");
+}
+
+}  // namespace
+}  // namespace df
+
+using namespace df;
+
+extern "C" {
+
+int dflash_linear_ce_workspace(int rows, int vocab, int hidden, int grads, size_t* bytes) {
+  if (bytes == nullptr) return api_fail(DFLASH_ERR_ARG, "bytes is null");
+  if (grads < 0 || grads > 2) return api_fail(DFLASH_ERR_ARG, "grads must be 0, 1 or 2");
+  if (int r = check_sizes(rows, vocab, hidden)) return r;
+  *bytes = make_plan(std::max(rows, 1), vocab, hidden, grads).total;
+  return DFLASH_OK;
+}
+
+int dflash_linear_ce(int rows, int vocab, int hidden, const void* x, int64_t x_stride,
+                     const void* w, int64_t w_stride, const int32_t* targets, float* nll,
+                     float* lse, void* workspace, size_t workspace_bytes, dflash_stream stream) {
+  return run({rows, vocab, hidden, x, x_stride, w, w_stride, targets, nullptr, nll, lse, nullptr,
+              nullptr},
+             false, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int dflash_linear_ce_grad(int rows, int vocab, int hidden, const void* x, int64_t x_stride,
+                          const void* w, int64_t w_stride, const int32_t* targets,
+                          const float* d_nll, float* nll, float* lse, void* dx, void* dw,
+                          void* workspace, size_t workspace_bytes, dflash_stream stream) {
+  return run({rows, vocab, hidden, x, x_stride, w, w_stride, targets, d_nll, nll, lse, dx, dw},
+             true, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -106,6 +106,11 @@ _SIGNATURES = {
     "dflash_qk_norm_rope_backward": ([c_void_p, c_int, c_int, POINTER(Heads), POINTER(Heads)] +
                                      [c_void_p] * 3 + [POINTER(Heads)] * 4 + [c_void_p] * 3 +
                                      [c_size_t, c_void_p], c_int),
+    "dflash_linear_ce_workspace": ([c_int] * 4 + [POINTER(c_size_t)], c_int),
+    "dflash_linear_ce": ([c_int] * 3 + [c_void_p, c_int64, c_void_p, c_int64] + [c_void_p] * 4 +
+                         [c_size_t, c_void_p], c_int),
+    "dflash_linear_ce_grad": ([c_int] * 3 + [c_void_p, c_int64, c_void_p, c_int64] +
+                              [c_void_p] * 7 + [c_size_t, c_void_p], c_int),
     "dflash_grad_norm_workspace": ([c_int, POINTER(c_size_t)], c_int),
     "dflash_grad_norm": ([c_int] + [c_void_p] * 5 + [c_size_t, c_void_p], c_int),
     "dflash_clip_grad_norm": ([c_int] + [c_void_p] * 4 + [ctypes.c_double] + [c_void_p] * 2 +
@@ -750,6 +755,56 @@ def _probabilities(name: str, t: torch.Tensor, dtype: torch.dtype, device: torch
     if strides[2] != 1 and shape[2] > 1 and t.numel():
         raise ValueError(f"{name}: a row's values must be dense")
     return strides
+
+
+def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
+    """Cross entropy of a linear head: x [N, H] and w [V, H] bf16 (rows dense,
+    H a multiple of 8), targets [N] int32, one outside [0, V) for a row that does
+    not count.  Returns (nll, lse) [N] fp32: logsumexp(x w^T) - (x w^T)[target]
+    and logsumexp(x w^T), 0 for rows that do not count.  The logits are never
+    held.  See dflash_linear_ce in include/dflash_attn.h."""
+    nll, lse, _, _ = _linear_ce(x, w, targets, None, 0)
+    return nll, lse
+
+
+def linear_cross_entropy_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                              d_nll: torch.Tensor, need_dw: bool = True):
+    """linear_cross_entropy and the gradients of sum(d_nll * nll) (d_nll [N]
+    fp32, the rows' weights in the loss) in one call.  Returns (nll, lse, dx [N,
+    H] bf16, dw [V, H] bf16 or None: a head that is not trained needs none)."""
+    return _linear_ce(x, w, targets, d_nll, 2 if need_dw else 1)
+
+
+def _linear_ce(x, w, targets, d_nll, grads: int):
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"x must be [N, H] and w [V, H], got {list(x.shape)} and "
+                         f"{list(w.shape)}")
+    (N, H), V, dev = x.shape, w.shape[0], w.device
+    if not w.is_cuda:
+        raise ValueError("the library runs on CUDA devices only")
+    for name, t in (("x", x), ("w", w)):
+        if t.dtype is not torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be bfloat16 on {dev}, got {t.dtype} on {t.device}")
+        if t.stride(1) != 1 and H > 1 and t.numel():
+            raise ValueError(f"{name}: a row's values must be dense")
+    _require("targets", targets, torch.int32, dev, (N,))
+    if grads:
+        _require("d_nll", d_nll, torch.float32, dev, (N,))
+    size = c_size_t(0)
+    check(lib().dflash_linear_ce_workspace(N, V, H, grads, byref(size)))
+    ws = torch.empty(size.value, device=dev, dtype=torch.uint8)
+    nll = torch.empty(2, N, device=dev, dtype=torch.float32)
+    nll, lse = nll[0], nll[1]
+    args = (N, V, H, x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0), targets.data_ptr())
+    if not grads:
+        _call(dev, lib().dflash_linear_ce, *args, nll.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+              size.value)
+        return nll, lse, None, None
+    dx = torch.empty(N, H, device=dev, dtype=torch.bfloat16)
+    dw = torch.empty(V, H, device=dev, dtype=torch.bfloat16) if grads == 2 else None
+    _call(dev, lib().dflash_linear_ce_grad, *args, d_nll.data_ptr(), nll.data_ptr(),
+          lse.data_ptr(), dx.data_ptr(), _p(dw), ws.data_ptr(), size.value)
+    return nll, lse, dx, dw
 
 
 def grad_norm(grads: Sequence[torch.Tensor]) -> torch.Tensor:

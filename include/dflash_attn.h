@@ -660,6 +660,44 @@ int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const d
                                  float* d_q_norm, float* d_k_norm, void* workspace,
                                  size_t workspace_bytes, dflash_stream stream);
 
+/* Cross entropy of a linear head over a vocabulary, and its gradients, for
+ * training a draft against the target's tokens, without holding the logits
+ * (no counterpart on the pages).  Needs no layer.  With z = x w^T:
+ *   nll = logsumexp(z) - z[target],   lse = logsumexp(z)   (natural logs)
+ *   dx = d_nll * (sum_v p_v w_v - w[target]),
+ *   dw[v] = sum over rows of d_nll * (p_v - [v = target]) * x,   p = exp(z - lse):
+ * the gradients of sum(d_nll * nll), so that d_nll holds the loss' weights.
+ *   x        device bf16: row r at x + r * x_stride elements, channels dense
+ *   w        device bf16 [vocab][hidden], rows w_stride elements apart
+ *   targets  device int32 [rows]; one outside [0, vocab) marks a row without a
+ *            target: nll, lse and dx are 0, and nothing of the row is looked at
+ *   d_nll    device fp32 [rows]
+ *   nll, lse device fp32 [rows]
+ *   dx       device bf16 [rows][hidden]; dw device bf16 [vocab][hidden] or NULL
+ *            (a head that is not trained).  Written, not added to; must not
+ *            overlap the inputs.
+ * hidden is a multiple of 8 (at most 2^16), row strides too; rows may be 0 (dw
+ * is then zero).  Products are of bf16 with fp32 sums; exponentials relative to
+ * a reference, and d_nll * p for dw, are rounded to bf16 once before the second
+ * product.  Sums are taken in an order that depends on the sizes and on which
+ * rows have a target alone.
+ *   workspace  device, 256-byte aligned, the caller's until the work is done;
+ *              dflash_linear_ce_workspace gives its size for grads = 0 (nll and
+ *              lse), 1 (dx) or 2 (dx and dw): at most about 512 MiB (and 4096
+ *              columns' worth) for a piece's exponentials, and small multiples
+ *              of rows * hidden and rows * vocab / 256.
+ * After a bounded wait that ran out nll and lse are NaN.  Work goes to the
+ * current device.
+ * Errors: _ARG, _SHAPE, _CAPACITY (workspace), _CUDA. */
+int dflash_linear_ce_workspace(int rows, int vocab, int hidden, int grads, size_t* bytes);
+int dflash_linear_ce(int rows, int vocab, int hidden, const void* x, int64_t x_stride,
+                     const void* w, int64_t w_stride, const int32_t* targets, float* nll,
+                     float* lse, void* workspace, size_t workspace_bytes, dflash_stream stream);
+int dflash_linear_ce_grad(int rows, int vocab, int hidden, const void* x, int64_t x_stride,
+                          const void* w, int64_t w_stride, const int32_t* targets,
+                          const float* d_nll, float* nll, float* lse, void* dx, void* dw,
+                          void* workspace, size_t workspace_bytes, dflash_stream stream);
+
 /* Global norm of many gradients, and clipping by it.  Needs no layer (no
  * counterpart on the pages).
  *   norm = sqrt(sum over all tensors of g^2)

@@ -47,20 +47,33 @@ def qk_rope_backward(x, gain, positions, theta, eps, d_y):
 def linear_cross_entropy(x, w, target, d_nll):
     """nll, lse of every row and the gradients of sum(d_nll * nll) in x and w;
     a target outside the vocabulary: no loss, no gradient."""
+    return linear_cross_entropy_sizes(x, w, target, d_nll)[:4]
+
+
+def linear_cross_entropy_sizes(x, w, target, d_nll):
+    """The same, and what its errors follow: the largest sum |x||w| and |z| of
+    a row, and the sums of the gradients' terms without their signs."""
     N, V = x.shape[0], w.shape[0]
     held = (target >= 0) & (target < V)
-    nll, lse = torch.zeros(N).double(), torch.zeros(N).double()
-    dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+    zero = lambda *s: torch.zeros(*s, dtype=x.dtype, device=x.device)  # noqa: E731
+    nll, lse, z_size, z_top = zero(N), zero(N), zero(N), zero(N)
+    dx, dw, dx_size, dw_size = (torch.zeros_like(t) for t in (x, w, x, w))
     at = torch.nonzero(held).flatten()
     if len(at):
         t = target[at].long()
-        z = x[at] @ w.t()
+        xa, d = x[at], d_nll[at][:, None]
+        z = xa @ w.t()
         lse[at] = torch.logsumexp(z, 1)
-        one = torch.arange(len(at))
+        one = torch.arange(len(at), device=x.device)
         nll[at] = lse[at] - z[one, t]
+        z_size[at] = (xa.abs() @ w.abs().t()).amax(1)
+        z_top[at] = z.abs().amax(1)
         g = torch.exp(z - lse[at][:, None])
-        g[one, t] -= 1.0
-        g = g * d_nll[at][:, None]
+        g[one, t] = 0.0
+        g[one, t] = -g.sum(1)  # p_t - 1, without cancelling
+        g = g * d
         dx[at] = g @ w
-        dw = g.t() @ x[at]
-    return nll, lse, dx, dw
+        dw = g.t() @ xa
+        dx_size[at] = g.abs() @ w.abs()
+        dw_size = g.abs().t() @ xa.abs()
+    return nll, lse, dx, dw, z_size, z_top, dx_size, dw_size
