@@ -65,9 +65,11 @@ struct CeGemm {
   const int* target;
   const float* d;      // GRAD: gradients of the rows' nll
   const float* miss;   // GRAD: 1 - p_t
-  float* part_m;       // [tile][rows_pad], log2 units
+  float* part_m;       // [rows_pad][all_tiles], log2 units
   float* part_s;
-  const int* repair;   // EXP: null, or flags of 32-row groups: only their tiles
+  int all_tiles;
+  const int* any;      // EXP: null, or whether a repair has anything to do
+  const int* repair;   // and the flags of 32-row groups: only their tiles
   int add;             // ACC: the buffer holds earlier pieces
   int* err;
 };
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CG == 2) cluster_sync();
   const uint32_t tmem = *tmem_slot;
   grid_dep_sync();
-  const int rows = __ldcg(p.n_rows);
+  const int rows = p.any != nullptr && __ldcg(p.any) == 0 ? 0 : __ldcg(p.n_rows);
   const int m_tiles = EPI == OUT ? p.m_tiles : (rows + CG * BM - 1) / (CG * BM);
   const int n_kb = EPI == OUT ? (rows + BK - 1) / BK : p.n_kb;
   const int units = m_tiles * p.n_tiles * p.splits;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (EPI == LSE || EPI == EXP) {
         if (live) {
-          const size_t at = (size_t)(p.v0 / BN + t.n) * p.rows_pad + row;
+          const size_t at = (size_t)row * p.all_tiles + p.v0 / BN + t.n;
           p.part_m[at] = mx;
           p.part_s[at] = sum;
         }
@@ -521,10 +523,12 @@ struct CeRows {
   long long x_stride, w_stride;
   const int* targets;
   const float* d_nll;  // null: forward only
+  int scan;            // the gather numbers the rows itself
   int* n;              // rows with a target
   int* err;
+  int* any;            // [pieces]: whether a repair has anything to do
+  int pieces;
   int* place;          // [rows]: compact row or -1
-  int* row_of;         // [rows_pad]: row of a compact one
   int* target;         // compact
   float* z_t;          // compact: the target's logit
   float* ref2;         // compact: reference, log2 units
@@ -532,35 +536,38 @@ struct CeRows {
   __nv_bfloat16* xc;   // [rows_pad][hidden]
 };
 
+DF_DEV bool has_target(const CeRows& a, int r) {
+  const int t = __ldg(a.targets + r);
+  return t >= 0 && t < a.vocab;
+}
+
+DF_DEV void store_counts(const CeRows& a, int n) {
+  *a.n = n;
+  *a.err = 0;
+  for (int i = 0; i < a.pieces; ++i) a.any[i] = 0;
+}
+
 // Compact numbers of the rows that have a target, in their order.
 __global__ void __launch_bounds__(1024) ce_compact_kernel(const __grid_constant__ CeRows a) {
-  __shared__ int warp_n[32], base;
+  __shared__ int warp_n[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_sync();
-  if (threadIdx.x == 0) base = 0;
-  __syncthreads();
+  int base = 0;
   for (int r0 = 0; r0 < a.rows; r0 += 1024) {
     const int r = r0 + threadIdx.x;
-    const int t = r < a.rows ? a.targets[r] : -1;
-    const bool has = t >= 0 && t < a.vocab;
+    const bool has = r < a.rows && has_target(a, r);
     const uint32_t b = __ballot_sync(0xffffffffu, has);
     if (lane == 0) warp_n[warp] = __popc(b);
     __syncthreads();
-    int at = base + __popc(b & ((1u << lane) - 1u)), all = 0;
+    int at = base + __popc(b & ((1u << lane) - 1u));
     for (int w = 0; w < 32; ++w) {
       at += w < warp ? warp_n[w] : 0;
-      all += warp_n[w];
+      base += warp_n[w];
     }
     if (r < a.rows) a.place[r] = has ? at : -1;
-    if (has) a.row_of[at] = r;
-    __syncthreads();
-    if (threadIdx.x == 0) base += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    *a.n = base;
-    *a.err = 0;
-  }
+  if (threadIdx.x == 0) store_counts(a, base);
 }
 
 DF_DEV float dot8(uint4 a, uint4 b) {
@@ -574,174 +581,201 @@ DF_DEV float dot8(uint4 a, uint4 b) {
   return s;
 }
 
-// One CTA per compact row: its copy of x, its target's logit.  Rows that fill
-// the last 256 are zero.
-__global__ void __launch_bounds__(256) ce_gather_kernel(const __grid_constant__ CeRows a) {
+// One CTA per row: its place, its copy of x, its target's logit.  The compact
+// rows that fill the last 256 are zero.
+constexpr int kRowThreads = 256;
+
+__global__ void __launch_bounds__(kRowThreads) ce_gather_kernel(const __grid_constant__ CeRows a) {
   __shared__ float sm[8];
+  __shared__ int before[8], all[8];
   grid_dep_sync();
-  const int r = blockIdx.x, n = __ldcg(a.n);
-  if (r >= (n + 255) / 256 * 256) return;
-  uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)r * a.hidden);
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n8 = a.hidden / 8;
-  if (r >= n) {
-    for (int i = threadIdx.x; i < n8; i += 256) dst[i] = make_uint4(0, 0, 0, 0);
-    return;
+  int n, c = -1;
+  if (a.scan) {  // the rows with a target in front of this one, and all of them
+    int mine = 0, sum = 0;
+    for (int r = threadIdx.x; r < a.rows; r += kRowThreads) {
+      const int has = has_target(a, r) ? 1 : 0;
+      sum += has;
+      mine += r < row ? has : 0;
+    }
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) before[warp] = mine, all[warp] = sum;
+    __syncthreads();
+    n = mine = 0;
+    for (int w = 0; w < 8; ++w) n += all[w], mine += before[w];
+    if (row < a.rows) {
+      c = has_target(a, row) ? mine : -1;
+      if (threadIdx.x == 0) a.place[row] = c;
+    }
+    if (row == 0 && threadIdx.x == 0) store_counts(a, n);
+  } else {
+    n = __ldcg(a.n);
+    if (row < a.rows) c = __ldcg(a.place + row);
   }
-  const int row = __ldcg(a.row_of + r), t = a.targets[row];
+  if (row < 256 && n + row < (n + 255) / 256 * 256) {
+    uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)(n + row) * a.hidden);
+    for (int i = threadIdx.x; i < n8; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
+  }
+  if (c < 0) return;
+  const int t = __ldg(a.targets + row);
   const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.x_stride);
   const uint4* w = reinterpret_cast<const uint4*>(a.w + t * a.w_stride);
+  uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)c * a.hidden);
   float s = 0.f;
-  for (int i = threadIdx.x; i < n8; i += 256) {
+  for (int i = threadIdx.x; i < n8; i += kRowThreads) {
     const uint4 v = __ldg(x + i);
     s += dot8(v, __ldg(w + i));
     dst[i] = v;
   }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  if (lane == 0) sm[warp] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     float z = 0.f;
     for (int i = 0; i < 8; ++i) z += sm[i];
-    a.target[r] = t;
-    a.z_t[r] = z;
-    a.ref2[r] = z * kLog2e;
-    if (a.d_nll != nullptr) a.d[r] = a.d_nll[row];
-  }
-}
-
-struct CeSums {
-  const float* part_m;  // forward: [tile][rows_pad]
-  const float* part_s;
-  const float* hist;    // gradient: [piece][rows_pad] the references of the tiles, log2 units
-  int tiles, piece_tiles;
-  float* nll;           // [rows]
-  float* lse;
-  float* inv;           // compact: 1 / sum of exponentials relative to the last reference
-  float* miss;          // compact: 1 - p_t
-  float* lse2;          // compact: lse in log2 units
-};
-
-// nll and lse of 32 rows from their tiles' sums, 32 slices of the tiles each,
-// joined in a fixed order.
-__global__ void __launch_bounds__(1024)
-    ce_combine_kernel(const __grid_constant__ CeRows a, const __grid_constant__ CeSums s) {
-  __shared__ float sm[32][33], ss[32][33];
-  grid_dep_sync();
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
-  const int c = row < a.rows ? __ldcg(a.place + row) : -1;
-  float m = kNegInf, sum = 0.f;
-  if (c >= 0) {
-    for (int t = slice; t < s.tiles; t += 32) {
-      const float ts = __ldcg(s.part_s + (size_t)t * a.rows_pad + c);
-      const float tm = s.hist != nullptr
-                           ? __ldcg(s.hist + (size_t)(t / s.piece_tiles) * a.rows_pad + c)
-                           : __ldcg(s.part_m + (size_t)t * a.rows_pad + c);
-      if (ts == 0.f) continue;
-      const float now = fmaxf(m, tm);
-      sum = sum * fast_exp2(m - now) + ts * fast_exp2(tm - now);
-      m = now;
-    }
-  }
-  sm[slice][lane] = m;
-  ss[slice][lane] = sum;
-  __syncthreads();
-  if (slice != 0 || row >= a.rows) return;
-  const bool failed = __ldcg(a.err) != 0;  // a wait ran out: no number is right
-  if (c < 0) {
-    s.nll[row] = s.lse[row] = failed ? __int_as_float(0x7fc00000) : 0.f;
-    return;
-  }
-  const float z2 = __ldcg(a.z_t + c) * kLog2e;
-  float top = z2;
-  for (int i = 0; i < 32; ++i) top = fmaxf(top, sm[i][lane]);
-  float others = 0.f;  // relative to `top`
-  for (int i = 0; i < 32; ++i)
-    if (ss[i][lane] != 0.f) others += ss[i][lane] * fast_exp2(sm[i][lane] - top);
-  const float own = fast_exp2(z2 - top), total = others + own;
-  // where the target leads, log1p keeps what is left of a small loss
-  const float nll = top == z2 ? log1pf(others) : logf(total) + (top - z2) * kLn2;
-  const float nan = __int_as_float(0x7fc00000);
-  s.nll[row] = failed ? nan : nll;
-  s.lse[row] = failed ? nan : nll + __ldcg(a.z_t + c);
-  if (s.hist != nullptr) {
-    const float last = __ldcg(a.ref2 + c);  // the accumulated products' reference
-    s.inv[c] = failed ? nan : fast_exp2(last - top) / total;
-    s.miss[c] = others / total;
-    s.lse2[c] = top + log2f(total);
+    a.target[c] = t;
+    a.z_t[c] = z;
+    a.ref2[c] = z * kLog2e;
+    if (a.d_nll != nullptr) a.d[c] = __ldg(a.d_nll + row);
   }
 }
 
 struct CeUpdate {
   const int* n;
-  int rows_pad, hidden, first_tile, tiles, slices;
+  int rows_pad, hidden, first_tile, tiles, all_tiles, slices;
   const float* part_m;
   float* ref2;
   float* hist;   // [rows_pad] of this piece
   int* flag;     // [rows_pad / 32]
+  int* any;      // of this piece
   float* acc;    // [slices][rows_pad][hidden], earlier pieces; null: none
 };
 
-// After a piece's exponentials: rows whose largest logit leaves the range take
-// it as their reference, what they hold of earlier pieces follows, and the
-// group is flagged for the repair.
+// After a piece's exponentials, a warp per row: rows whose largest logit
+// leaves the range take it as their reference, what they hold of earlier
+// pieces follows, and their group of 32 is flagged for the repair.
 __global__ void __launch_bounds__(1024) ce_update_kernel(const __grid_constant__ CeUpdate a) {
-  __shared__ float sm[32][33], factor[32];
+  __shared__ float factor[32];
   grid_dep_sync();
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + warp;
   const bool live = row < __ldcg(a.n);
-  float m = kNegInf;
-  if (live)
-    for (int t = slice; t < a.tiles; t += 32)
-      m = fmaxf(m, __ldcg(a.part_m + (size_t)(a.first_tile + t) * a.rows_pad + row));
-  sm[slice][lane] = m;
-  __syncthreads();
-  if (slice == 0) {
-    for (int i = 0; i < 32; ++i) m = fmaxf(m, sm[i][lane]);
-    float f = 1.f;
-    if (live) {
-      const float ref = a.ref2[row];
-      const bool far = m - ref > kRefSlack;
-      f = far ? fast_exp2(ref - m) : 1.f;
+  float f = 1.f;
+  if (live) {
+    const float* part = a.part_m + (size_t)row * a.all_tiles + a.first_tile;
+    float m = kNegInf;
+    for (int t = lane; t < a.tiles; t += 32) m = fmaxf(m, __ldcg(part + t));
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = __ldcg(a.ref2 + row);
+    const bool far = m - ref > kRefSlack;
+    if (far) f = fast_exp2(ref - m);
+    if (lane == 0) {
       if (far) a.ref2[row] = m;
       a.hist[row] = far ? m : ref;
     }
-    factor[lane] = f;
-    const bool any = __any_sync(0xffffffffu, f != 1.f);
-    if (lane == 0) a.flag[blockIdx.x] = any ? 1 : 0;
   }
-  __syncthreads();
-  if (a.acc == nullptr) return;
+  if (lane == 0) factor[warp] = f;
+  const int any = __syncthreads_or(f != 1.f);
+  if (threadIdx.x == 0) {
+    a.flag[blockIdx.x] = any;
+    if (any) *a.any = 1;  // (every writer stores the same)
+  }
+  if (!any || a.acc == nullptr) return;
   for (int r = 0; r < 32; ++r) {
-    const float f = factor[r];
-    if (f == 1.f) continue;
+    const float k = factor[r];
+    if (k == 1.f) continue;
     for (int s = 0; s < a.slices; ++s) {
       float* v = a.acc + ((size_t)s * a.rows_pad + blockIdx.x * 32 + r) * a.hidden;
-      for (int i = threadIdx.x; i < a.hidden; i += 1024) v[i] *= f;
+      for (int i = threadIdx.x; i < a.hidden; i += 1024) v[i] *= k;
     }
   }
 }
 
-// dx of one row from the accumulated products: d * (acc * inv - miss * w_t).
-__global__ void __launch_bounds__(256)
-    ce_finish_kernel(const __grid_constant__ CeRows a, const float* acc, int slices,
-                     const float* inv, const float* miss, __nv_bfloat16* dx) {
+struct CeSums {
+  const float* part_m;  // [rows_pad][tiles]
+  const float* part_s;
+  const float* hist;    // gradient: [piece][rows_pad] the references of the tiles, log2 units
+  int tiles, piece_tiles;
+  float* nll;           // [rows]
+  float* lse;
+  const float* acc;     // gradient: [slices][rows_pad][hidden]
+  int slices;
+  __nv_bfloat16* dx;
+  float* miss;          // compact: 1 - p_t
+  float* lse2;          // compact: lse in log2 units
+};
+
+// (m, s) and (m2, s2), sums relative to a reference each, as one
+DF_DEV void join(float& m, float& s, float m2, float s2) {
+  if (s2 == 0.f) return;
+  const float top = fmaxf(m, m2);
+  s = s * fast_exp2(m - top) + s2 * fast_exp2(m2 - top);
+  m = top;
+}
+
+// One CTA per row: nll and lse from the tiles' sums, joined in a fixed order,
+// and with a gradient dx = d * (acc / sum - (1 - p_t) * w_t).
+__global__ void __launch_bounds__(kRowThreads)
+    ce_finish_kernel(const __grid_constant__ CeRows a, const __grid_constant__ CeSums s) {
+  __shared__ float sm[8], ss[8];
   grid_dep_sync();
   const int row = blockIdx.x, c = __ldcg(a.place + row), n8 = a.hidden / 8;
-  uint4* out = reinterpret_cast<uint4*>(dx + (size_t)row * a.hidden);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float nan = __int_as_float(0x7fc00000);
+  const bool failed = __ldcg(a.err) != 0;  // a wait ran out: no number is right
+  uint4* out = reinterpret_cast<uint4*>(s.dx + (size_t)row * a.hidden);
   if (c < 0) {
-    for (int i = threadIdx.x; i < n8; i += 256) out[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) s.nll[row] = s.lse[row] = failed ? nan : 0.f;
+    if (s.dx != nullptr)
+      for (int i = threadIdx.x; i < n8; i += kRowThreads) out[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const float d = __ldcg(a.d + c), f = __ldcg(inv + c) * d, g = __ldcg(miss + c) * d;
+  float m = kNegInf, sum = 0.f;
+  const float* pm = s.part_m + (size_t)c * s.tiles;
+  const float* ps = s.part_s + (size_t)c * s.tiles;
+  for (int t = threadIdx.x; t < s.tiles; t += kRowThreads)
+    join(m, sum,
+         s.hist != nullptr ? __ldcg(s.hist + (size_t)(t / s.piece_tiles) * a.rows_pad + c)
+                           : __ldcg(pm + t),
+         __ldcg(ps + t));
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+    join(m, sum, m2, s2);
+  }
+  if (lane == 0) sm[warp] = m, ss[warp] = sum;
+  __syncthreads();
+  m = sm[0], sum = ss[0];
+  for (int i = 1; i < 8; ++i) join(m, sum, sm[i], ss[i]);
+  const float z = __ldcg(a.z_t + c), z2 = z * kLog2e;
+  const float top = sum == 0.f ? z2 : fmaxf(m, z2);
+  const float others = sum == 0.f ? 0.f : sum * fast_exp2(m - top);  // relative to `top`
+  const float total = others + fast_exp2(z2 - top);
+  if (threadIdx.x == 0) {
+    // where the target leads, log1p keeps what is left of a small loss
+    const float nll = top == z2 ? log1pf(others) : logf(total) + (top - z2) * kLn2;
+    s.nll[row] = failed ? nan : nll;
+    s.lse[row] = failed ? nan : nll + z;
+    if (s.dx != nullptr) {
+      s.miss[c] = others / total;
+      s.lse2[c] = top + log2f(total);
+    }
+  }
+  if (s.dx == nullptr) return;
+  // the products are relative to the row's last reference
+  const float d = __ldcg(a.d + c);
+  const float f = failed ? nan : d * fast_exp2(__ldcg(a.ref2 + c) - top) / total;
+  const float g = d * (others / total);
   const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
-  for (int i = threadIdx.x; i < n8; i += 256) {
+  for (int i = threadIdx.x; i < n8; i += kRowThreads) {
     float v[8] = {};
-    for (int s = 0; s < slices; ++s) {
+    for (int k = 0; k < s.slices; ++k) {
       const float4* p = reinterpret_cast<const float4*>(
-                            acc + ((size_t)s * a.rows_pad + c) * a.hidden) + 2 * i;
+                            s.acc + ((size_t)k * a.rows_pad + c) * a.hidden) + 2 * i;
       const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
       v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
       v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
@@ -760,13 +794,16 @@ __global__ void __launch_bounds__(256)
 // ----------------------------------------------------------------- the host
 constexpr size_t kPieceBytes = 512ull << 20;  // of a piece's exponentials
 constexpr int kMaxSplits = 16;
+// Up to here every CTA of the gather counts the targets in front of its row
+// itself (16 KB from L2 each): a launch less.
+constexpr int kScanRows = 4096;
 
 struct Plan {
   int cg, rows_pad, n_tiles;
   int piece, pieces;   // columns of a piece (a multiple of 256)
   int splits;          // of ACC's K
-  size_t place, row_of, target, z_t, ref2, d, inv, miss, lse2, hist, flag, xc, part_m, part_s, g,
-      acc, total;
+  size_t any, place, target, z_t, ref2, d, miss, lse2, hist, flag, xc, part_m, part_s, g, acc,
+      total;
 };
 
 // Splits of K for the products of few tiles: whole waves, and about 24
@@ -805,8 +842,8 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
     return here;
   };
   const size_t pad = (size_t)p.rows_pad;
+  p.any = take((size_t)p.pieces * 4);
   p.place = take((size_t)rows * 4);
-  p.row_of = take(pad * 4);
   p.target = take(pad * 4);
   p.z_t = take(pad * 4);
   p.ref2 = take(pad * 4);
@@ -815,7 +852,6 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
   p.part_s = take(pad * p.n_tiles * 4);
   if (grads > 0) {
     p.d = take(pad * 4);
-    p.inv = take(pad * 4);
     p.miss = take(pad * 4);
     p.lse2 = take(pad * 4);
     p.hist = take(pad * p.pieces * 4);
@@ -947,8 +983,10 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   a.d_nll = c.d_nll;
   a.n = i32(0);
   a.err = i32(4);
+  a.scan = c.rows <= kScanRows;
+  a.any = i32(p.any);
+  a.pieces = p.pieces;
   a.place = i32(p.place);
-  a.row_of = i32(p.row_of);
   a.target = i32(p.target);
   a.z_t = f32(p.z_t);
   a.ref2 = f32(p.ref2);
@@ -985,6 +1023,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   gm.target = a.target;
   gm.part_m = f32(p.part_m);
   gm.part_s = f32(p.part_s);
+  gm.all_tiles = p.n_tiles;
   gm.err = a.err;
   CeSums sums{};
   sums.part_m = gm.part_m;
@@ -995,26 +1034,29 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   sums.lse = c.lse;
   const int m_tiles = (c.rows + p.cg * BM - 1) / (p.cg * BM);
   const int h_tiles = (H + BN - 1) / BN;
-  const dim3 b1024(1024), b256(256), groups((c.rows + 31) / 32);
+  const dim3 b1024(1024), b256(kRowThreads);
 
-  e = launch_pdl(ce_compact_kernel, dim3(1), b1024, 0, s, a);
+  if (!a.scan) e = launch_pdl(ce_compact_kernel, dim3(1), b1024, 0, s, a);
   if (e == cudaSuccess) e = launch_pdl(ce_gather_kernel, dim3(pad), b256, 0, s, a);
   if (!grad) {
     gm.n_tiles = p.n_tiles;
     if (e == cudaSuccess)
       e = launch_gemm<LSE>(p.cg, x_k, w_k, x_k, gm, m_tiles * p.n_tiles, sms, s);
-    if (e == cudaSuccess) e = launch_pdl(ce_combine_kernel, groups, b1024, 0, s, a, sums);
+    if (e == cudaSuccess) e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, sums);
     return done("cross entropy launch");
   }
 
   sums.hist = f32(p.hist);
-  sums.inv = f32(p.inv);
+  sums.acc = f32(p.acc);
+  sums.slices = p.splits;
+  sums.dx = static_cast<__nv_bfloat16*>(c.dx);
   sums.miss = f32(p.miss);
   sums.lse2 = f32(p.lse2);
   CeUpdate up{};
   up.n = a.n;
   up.rows_pad = pad;
   up.hidden = H;
+  up.all_tiles = p.n_tiles;
   up.slices = p.splits;
   up.part_m = gm.part_m;
   up.ref2 = a.ref2;
@@ -1028,8 +1070,10 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     up.first_tile = v0 / BN;
     up.tiles = tiles;
     up.hist = f32(p.hist) + (size_t)i * pad;
+    up.any = a.any + i;
     up.acc = i > 0 ? f32(p.acc) : nullptr;
     if (e == cudaSuccess) e = launch_pdl(ce_update_kernel, dim3(pad / 32), b1024, 0, s, up);
+    ex.any = up.any;
     ex.repair = up.flag;
     if (e == cudaSuccess)
       e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
@@ -1042,10 +1086,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     if (e == cudaSuccess)
       e = launch_gemm<ACC>(p.cg, g_k, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
   }
-  if (e == cudaSuccess) e = launch_pdl(ce_combine_kernel, groups, b1024, 0, s, a, sums);
-  if (e == cudaSuccess)
-    e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, f32(p.acc), p.splits,
-                   f32(p.inv), f32(p.miss), static_cast<__nv_bfloat16*>(c.dx));
+  if (e == cudaSuccess) e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, sums);
   for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
     const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
     CeGemm gr = gm;
