@@ -1747,7 +1747,7 @@ int dflash_qk_norm_rope(dflash_attn* a, int batch, int rows, const dflash_heads*
 int dflash_qk_norm_rope_workspace(const dflash_attn* a, size_t* bytes) {
   if (int r = check_attn(a)) return r;
   if (bytes == nullptr) return fail(DFLASH_ERR_ARG, "bytes is null");
-  *bytes = (size_t)qk_rope_max_ctas(a->num_sms) * 2 * a->d * sizeof(float);
+  *bytes = (size_t)qk_rope_max_ctas(a->num_sms) * a->d * sizeof(float);
   return DFLASH_OK;
 }
 

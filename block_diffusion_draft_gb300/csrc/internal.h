@@ -401,14 +401,14 @@ struct HeadView {
 struct QkRopeArgs {
   int batch, rows, d, max_pos;
   int heads[2];
-  long long items;             // set by the launch: units of work of a warp
+  int items[2], split;         // set by the launch: warps' units of work, CTAs of the queries
   float eps;
   const float2* rope;          // [max_pos][d / 2] (cos, sin)
   const int* positions;        // [batch][rows]
   const void* gain[2];         // [d] in the layer's type; null: gain32
   const float* gain32[2];
   HeadView x[2], dy[2], out[2];
-  float* partial;              // backward: [qk_rope_max_ctas][2][d]
+  float* partial;              // backward: [qk_rope_max_ctas][d]
   int* err;
 };
 int qk_rope_max_ctas(int num_sms);

@@ -21,16 +21,24 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
-DF_DEV void load4(const float* p, float (&v)[4]) {
-  const float4 t = *reinterpret_cast<const float4*>(p);
-  v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-}
-
-DF_DEV void load4(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 t = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(t.x << 16), v[1] = __uint_as_float(t.x & 0xffff0000u);
-  v[2] = __uint_as_float(t.y << 16), v[3] = __uint_as_float(t.y & 0xffff0000u);
-}
+// Four channels as they lie in memory, and as numbers.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<float> {
+  float4 r;
+  DF_DEV void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  DF_DEV float operator[](int i) const { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
+};
+template <>
+struct Quad<__nv_bfloat16> {
+  uint2 r;
+  DF_DEV void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint2*>(p); }
+  DF_DEV float operator[](int i) const {
+    const uint32_t w = i < 2 ? r.x : r.y;
+    return __uint_as_float((i & 1) ? w & 0xffff0000u : w << 16);
+  }
+};
 
 DF_DEV void store4(float* p, const float (&v)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -45,18 +53,16 @@ DF_DEV T* head_ptr(const HeadView& h, int b, int r) {
   return reinterpret_cast<T*>(h.p) + b * h.batch + r * h.row;
 }
 
-// (row of the call, which of q and k, first head) of a warp's item: `per`
-// heads of one row
+// A warp's unit of work: `per` heads from `head` on of row r of sequence b.
 struct Item {
-  int b, r, kind, head;
+  int b, r, head;
 };
 
-DF_DEV Item item_at(const QkRopeArgs& a, long long i, int per) {
-  const int cq = (a.heads[0] + per - 1) / per, ck = (a.heads[1] + per - 1) / per;
-  const int row = (int)(i / (cq + ck)), c = (int)(i - (long long)row * (cq + ck));
+DF_DEV Item item_at(const QkRopeArgs& a, int kind, int i, int per) {
+  const int chunks = (a.heads[kind] + per - 1) / per;
+  const int row = i / chunks;
   Item t;
-  t.kind = c >= cq;
-  t.head = (t.kind ? c - cq : c) * per;
+  t.head = (i - row * chunks) * per;
   t.b = row / a.rows;
   t.r = row - t.b * a.rows;
   return t;
@@ -73,49 +79,62 @@ DF_DEV const float2* rope_row(const QkRopeArgs& a, const Item& t) {
 
 template <typename T>
 DF_DEV void load_gain(const QkRopeArgs& a, int kind, int j, float (&v)[4]) {
-  if (a.gain[kind] != nullptr)
-    load4(static_cast<const T*>(a.gain[kind]) + j, v);
-  else
-    load4(a.gain32[kind] + j, v);
+  Quad<T> q;
+  Quad<float> f;
+  if (a.gain[kind] != nullptr) q.load(static_cast<const T*>(a.gain[kind]) + j);
+  else f.load(a.gain32[kind] + j);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = a.gain[kind] != nullptr ? q[i] : f[i];
 }
 
-// Heads of D channels whose tensors allow 4-channel accesses.
+// (cos, sin) of four neighbouring pairs
+DF_DEV void load_turn(const float2* p, float (&cs)[4], float (&sn)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  cs[0] = a.x, sn[0] = a.y, cs[1] = a.z, sn[1] = a.w;
+  cs[2] = b.x, sn[2] = b.y, cs[3] = b.z, sn[3] = b.w;
+}
+
+#ifndef FU
+#define FU 4
+#define FB 4
+#define BU 2
+#define BB 3
+#endif
+// Heads of D channels whose tensors allow 4-channel accesses.  The CTAs below
+// `a.split` take the queries, the others the keys.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
-  constexpr int L = D / 8, G = 32 / L, U = 4;
+__global__ void __launch_bounds__(kThreads, FB)
+    qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
+  constexpr int L = D / 8, G = 32 / L, U = FU;
   const int lane = threadIdx.x & 31, l = lane % L, g = lane / L;
+  const int kind = (int)blockIdx.x >= a.split;
+  const int i = ((int)blockIdx.x - (kind ? a.split : 0)) * kWarps + (threadIdx.x >> 5);
   grid_dep_sync();
-  const long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= a.items) return;
-  const Item t = item_at(a, i, G * U);
-  const int n = a.heads[t.kind];
-  const T* src = head_ptr<const T>(a.x[t.kind], t.b, t.r) + 4 * l;
-  float lo[U][4], hi[U][4];
+  if (i >= a.items[kind]) return;
+  const Item t = item_at(a, kind, i, G * U);
+  const int n = a.heads[kind];
+  const T* src = head_ptr<const T>(a.x[kind], t.b, t.r) + 4 * l;
+  Quad<T> lo[U], hi[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = t.head + u * G + g;
-    if (h < n) {
-      load4(src + h * a.x[t.kind].head, lo[u]);
-      load4(src + h * a.x[t.kind].head + D / 2, hi[u]);
-    }
+    const int h = min(t.head + u * G + g, n - 1);
+    lo[u].load(src + h * a.x[kind].head);
+    hi[u].load(src + h * a.x[kind].head + D / 2);
   }
-  const float2* rp = rope_row(a, t) + 4 * l;
-  const float4 c01 = __ldg(reinterpret_cast<const float4*>(rp));
-  const float4 c23 = __ldg(reinterpret_cast<const float4*>(rp) + 1);
-  const float cs[4] = {c01.x, c01.z, c23.x, c23.z}, sn[4] = {c01.y, c01.w, c23.y, c23.w};
-  float ga[4], gb[4];
-  load_gain<T>(a, t.kind, 4 * l, ga);
-  load_gain<T>(a, t.kind, 4 * l + D / 2, gb);
-  T* dst = head_ptr<T>(a.out[t.kind], t.b, t.r) + 4 * l;
+  float cs[4], sn[4], ga[4], gb[4];
+  load_turn(rope_row(a, t) + 4 * l, cs, sn);
+  load_gain<T>(a, kind, 4 * l, ga);
+  load_gain<T>(a, kind, 4 * l + D / 2, gb);
+  T* dst = head_ptr<T>(a.out[kind], t.b, t.r) + 4 * l;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = t.head + u * G + g;
     float ss = 0.f;
-    if (h < n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ss += lo[u][j] * lo[u][j] + hi[u][j] * hi[u][j];
+    for (int j = 0; j < 4; ++j) ss += lo[u][j] * lo[u][j] + hi[u][j] * hi[u][j];
 #pragma unroll
     for (int o = L / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const int h = t.head + u * G + g;
     if (h >= n) continue;
     const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
     float ya[4], yb[4];
@@ -125,105 +144,95 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const __grid_constant
       ya[j] = za * cs[j] - zb * sn[j];
       yb[j] = zb * cs[j] + za * sn[j];
     }
-    store4(dst + h * a.out[t.kind].head, ya);
-    store4(dst + h * a.out[t.kind].head + D / 2, yb);
+    store4(dst + h * a.out[kind].head, ya);
+    store4(dst + h * a.out[kind].head + D / 2, yb);
   }
 }
 
-// The CTA's sums for the gains' gradients: lanes of a warp that hold the same
-// channels (L apart), then the warps in order, to partial[CTA][kind][d].
-template <int D>
-DF_DEV void store_gain_sums(const QkRopeArgs& a, float (&acc)[2][8]) {
-  constexpr int L = D / 8;
-  __shared__ float red[kWarps][2][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v = acc[k][j];
-#pragma unroll
-      for (int o = 16; o >= L; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < L) red[warp][k][4 * lane + (j & 3) + (j >> 2) * (D / 2)] = v;
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-    float v = 0.f;
-    for (int w = 0; w < kWarps; ++w) v += (&red[w][0][0])[i];
-    a.partial[(size_t)blockIdx.x * 2 * D + i] = v;
-  }
-}
+// One item's rows as they come from memory.
+template <typename T, int U>
+struct RawItem {
+  Quad<T> xa[U], xb[U], wa[U], wb[U];
+};
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, BB)
     qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a) {
-  constexpr int L = D / 8, G = 32 / L, U = 2;
-  const int lane = threadIdx.x & 31, l = lane % L, g = lane / L;
+  constexpr int L = D / 8, G = 32 / L, U = BU;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, g = lane / L;
+  const int kind = (int)blockIdx.x >= a.split;
+  const int ctas = kind ? (int)gridDim.x - a.split : a.split;
+  const int n = a.heads[kind];
   grid_dep_sync();
-  float acc[2][8] = {};
-  for (long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < a.items;
-       i += (long long)gridDim.x * kWarps) {
-    const Item t = item_at(a, i, G * U);
-    const int n = a.heads[t.kind];
-    const T* src = head_ptr<const T>(a.x[t.kind], t.b, t.r) + 4 * l;
-    const T* dsrc = head_ptr<const T>(a.dy[t.kind], t.b, t.r) + 4 * l;
-    float xa[U][4], xb[U][4], wa[U][4], wb[U][4];
+  float ga[4], gb[4], acc[8] = {};
+  load_gain<T>(a, kind, 4 * l, ga);
+  load_gain<T>(a, kind, 4 * l + D / 2, gb);
+  for (int i = ((int)blockIdx.x - (kind ? a.split : 0)) * kWarps + warp; i < a.items[kind];
+       i += ctas * kWarps) {
+    const Item t = item_at(a, kind, i, G * U);
+    const T* src = head_ptr<const T>(a.x[kind], t.b, t.r) + 4 * l;
+    const T* dsrc = head_ptr<const T>(a.dy[kind], t.b, t.r) + 4 * l;
+    RawItem<T, U> v;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = t.head + u * G + g;
-      if (h < n) {
-        load4(src + h * a.x[t.kind].head, xa[u]);
-        load4(src + h * a.x[t.kind].head + D / 2, xb[u]);
-        load4(dsrc + h * a.dy[t.kind].head, wa[u]);
-        load4(dsrc + h * a.dy[t.kind].head + D / 2, wb[u]);
-      }
+      const int h = min(t.head + u * G + g, n - 1);
+      v.xa[u].load(src + h * a.x[kind].head);
+      v.xb[u].load(src + h * a.x[kind].head + D / 2);
+      v.wa[u].load(dsrc + h * a.dy[kind].head);
+      v.wb[u].load(dsrc + h * a.dy[kind].head + D / 2);
     }
-    const float2* rp = rope_row(a, t) + 4 * l;
-    const float4 c01 = __ldg(reinterpret_cast<const float4*>(rp));
-    const float4 c23 = __ldg(reinterpret_cast<const float4*>(rp) + 1);
-    const float cs[4] = {c01.x, c01.z, c23.x, c23.z}, sn[4] = {c01.y, c01.w, c23.y, c23.w};
-    float ga[4], gb[4];
-    load_gain<T>(a, t.kind, 4 * l, ga);
-    load_gain<T>(a, t.kind, 4 * l + D / 2, gb);
-    T* dst = head_ptr<T>(a.out[t.kind], t.b, t.r) + 4 * l;
+    float cs[4], sn[4];
+    load_turn(rope_row(a, t) + 4 * l, cs, sn);
+    T* dst = head_ptr<T>(a.out[kind], t.b, t.r) + 4 * l;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = t.head + u * G + g;
-      float ss = 0.f, ux = 0.f;
-      if (h < n)
+      float wa[4], wb[4], ss = 0.f, ux = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float da = wa[u][j], db = wb[u][j];
-          wa[u][j] = da * cs[j] + db * sn[j];
-          wb[u][j] = db * cs[j] - da * sn[j];
-          ss += xa[u][j] * xa[u][j] + xb[u][j] * xb[u][j];
-          ux += wa[u][j] * ga[j] * xa[u][j] + wb[u][j] * gb[j] * xb[u][j];
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float xa = v.xa[u][j], xb = v.xb[u][j];
+        wa[j] = v.wa[u][j] * cs[j] + v.wb[u][j] * sn[j];
+        wb[j] = v.wb[u][j] * cs[j] - v.wa[u][j] * sn[j];
+        ss += xa * xa + xb * xb;
+        ux += wa[j] * ga[j] * xa + wb[j] * gb[j] * xb;
+      }
 #pragma unroll
       for (int o = L / 2; o > 0; o /= 2) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
         ux += __shfl_xor_sync(0xffffffffu, ux, o);
       }
+      const int h = t.head + u * G + g;
       if (h >= n) continue;
       const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
       const float m = r * r * ux * (1.f / D);
       float da[4], db[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        da[j] = r * (wa[u][j] * ga[j] - xa[u][j] * m);
-        db[j] = r * (wb[u][j] * gb[j] - xb[u][j] * m);
-        const float pa = wa[u][j] * xa[u][j] * r, pb = wb[u][j] * xb[u][j] * r;
-        // (selects, so that the sums stay in registers)
-        acc[0][j] += t.kind ? 0.f : pa;
-        acc[0][4 + j] += t.kind ? 0.f : pb;
-        acc[1][j] += t.kind ? pa : 0.f;
-        acc[1][4 + j] += t.kind ? pb : 0.f;
+        const float xa = v.xa[u][j], xb = v.xb[u][j];
+        da[j] = r * (wa[j] * ga[j] - xa * m);
+        db[j] = r * (wb[j] * gb[j] - xb * m);
+        acc[j] += wa[j] * xa * r;
+        acc[4 + j] += wb[j] * xb * r;
       }
-      store4(dst + h * a.out[t.kind].head, da);
-      store4(dst + h * a.out[t.kind].head + D / 2, db);
+      store4(dst + h * a.out[kind].head, da);
+      store4(dst + h * a.out[kind].head + D / 2, db);
     }
   }
-  store_gain_sums<D>(a, acc);
+  // the CTA's sums: lanes that hold the same channels (L apart), then the
+  // warps in order
+  __shared__ float red[kWarps][D];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float v = acc[j];
+#pragma unroll
+    for (int o = 16; o >= L; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane < L) red[warp][4 * lane + (j & 3) + (j >> 2) * (D / 2)] = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    float v = 0.f;
+    for (int w = 0; w < kWarps; ++w) v += red[w][i];
+    a.partial[(size_t)blockIdx.x * D + i] = v;
+  }
 }
 
 // Any even head size up to 256 and any alignment, fp32: a warp takes a head,
@@ -233,19 +242,20 @@ constexpr int kPairs = 4;
 template <bool BWD>
 __global__ void __launch_bounds__(kThreads)
     qk_rope_any_kernel(const __grid_constant__ QkRopeArgs a) {
-  __shared__ float red[BWD ? kWarps : 1][2][256];
+  __shared__ float red[BWD ? kWarps : 1][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.d / 2;
+  const int kind = (int)blockIdx.x >= a.split;
+  const int ctas = kind ? (int)gridDim.x - a.split : a.split;
   grid_dep_sync();
-  float acc[2][2 * kPairs] = {};
-  for (long long i = (long long)blockIdx.x * kWarps + warp; i < a.items;
-       i += (long long)gridDim.x * kWarps) {
-    const Item t = item_at(a, i, 1);
-    const float* x = head_ptr<const float>(a.x[t.kind], t.b, t.r) + t.head * a.x[t.kind].head;
-    const float* dy = BWD ? head_ptr<const float>(a.dy[t.kind], t.b, t.r) +
-                                t.head * a.dy[t.kind].head
-                          : nullptr;
-    const float* gain = a.gain[t.kind] != nullptr ? static_cast<const float*>(a.gain[t.kind])
-                                                  : a.gain32[t.kind];
+  const float* gain = a.gain[kind] != nullptr ? static_cast<const float*>(a.gain[kind])
+                                              : a.gain32[kind];
+  float acc[2 * kPairs] = {};
+  for (int i = ((int)blockIdx.x - (kind ? a.split : 0)) * kWarps + warp; i < a.items[kind];
+       i += ctas * kWarps) {
+    const Item t = item_at(a, kind, i, 1);
+    const float* x = head_ptr<const float>(a.x[kind], t.b, t.r) + t.head * a.x[kind].head;
+    const float* dy =
+        BWD ? head_ptr<const float>(a.dy[kind], t.b, t.r) + t.head * a.dy[kind].head : nullptr;
     const float2* rp = rope_row(a, t);
     float xa[kPairs], xb[kPairs], wa[kPairs], wb[kPairs], ga[kPairs], gb[kPairs];
     float2 cs[kPairs];
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(kThreads)
       if (BWD) ux += __shfl_xor_sync(0xffffffffu, ux, o);
     }
     const float r = 1.f / sqrtf(ss / a.d + a.eps), m = r * r * ux / a.d;
-    float* out = head_ptr<float>(a.out[t.kind], t.b, t.r) + t.head * a.out[t.kind].head;
+    float* out = head_ptr<float>(a.out[kind], t.b, t.r) + t.head * a.out[kind].head;
 #pragma unroll
     for (int q = 0; q < kPairs; ++q) {
       const int j = lane + 32 * q;
@@ -281,11 +291,8 @@ __global__ void __launch_bounds__(kThreads)
       if (BWD) {
         out[j] = r * (wa[q] * ga[q] - xa[q] * m);
         out[j + half] = r * (wb[q] * gb[q] - xb[q] * m);
-        const float pa = wa[q] * xa[q] * r, pb = wb[q] * xb[q] * r;
-        acc[0][q] += t.kind ? 0.f : pa;
-        acc[0][kPairs + q] += t.kind ? 0.f : pb;
-        acc[1][q] += t.kind ? pa : 0.f;
-        acc[1][kPairs + q] += t.kind ? pb : 0.f;
+        acc[q] += wa[q] * xa[q] * r;
+        acc[kPairs + q] += wb[q] * xb[q] * r;
       } else {
         const float za = xa[q] * r * ga[q], zb = xb[q] * r * gb[q];
         out[j] = za * cs[q].x - zb * cs[q].y;
@@ -295,43 +302,44 @@ __global__ void __launch_bounds__(kThreads)
   }
   if constexpr (BWD) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        const int j = lane + 32 * q;
-        if (j >= half) continue;
-        red[warp][k][j] = acc[k][q];
-        red[warp][k][j + half] = acc[k][kPairs + q];
-      }
+    for (int q = 0; q < kPairs; ++q) {
+      const int j = lane + 32 * q;
+      if (j >= half) continue;
+      red[warp][j] = acc[q];
+      red[warp][j + half] = acc[kPairs + q];
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
-      const int k = i / a.d, j = i - k * a.d;
+    for (int i = threadIdx.x; i < a.d; i += kThreads) {
       float v = 0.f;
-      for (int w = 0; w < kWarps; ++w) v += red[w][k][j];
-      a.partial[(size_t)blockIdx.x * 2 * a.d + i] = v;
+      for (int w = 0; w < kWarps; ++w) v += red[w][i];
+      a.partial[(size_t)blockIdx.x * a.d + i] = v;
     }
   }
 }
 
-// The gains' gradients from the CTAs' sums, always in the same order: 32
-// channels per CTA, 32 slices of the CTAs each.
+// The gains' gradients from the CTAs' sums (the first `split` CTAs: the
+// queries'), always in the same order: 32 channels per CTA, 32 slices of the
+// CTAs each.
 __global__ void __launch_bounds__(1024)
-    qk_rope_gain_kernel(const float* partial, int n, int d, float* dq_gain, float* dk_gain) {
+    qk_rope_gain_kernel(const float* partial, int split, int n, int d, float* dq_gain,
+                        float* dk_gain) {
   __shared__ float red[32][33];
   grid_dep_sync();
   const int c = threadIdx.x & 31, s = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  const int kind = blockIdx.y;
   float v = 0.f;
-  if (col < 2 * d)
+  if (col < d)
 #pragma unroll 8
-    for (int i = s; i < n; i += 32) v += __ldcg(partial + (size_t)i * 2 * d + col);
+    for (int i = (kind ? split : 0) + s; i < (kind ? n : split); i += 32)
+      v += __ldcg(partial + (size_t)i * d + col);
   red[s][c] = v;
   __syncthreads();
-  if (s == 0 && col < 2 * d) {
+  if (s == 0 && col < d) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum += red[i][c];
-    float* out = col < d ? dq_gain : dk_gain;
-    if (out != nullptr) out[col < d ? col : col - d] = sum;
+    float* out = kind ? dk_gain : dq_gain;
+    if (out != nullptr) out[col] = sum;
   }
 }
 
@@ -340,24 +348,35 @@ bool vector_view(const HeadView& v, size_t elem) {
   return ((reinterpret_cast<uintptr_t>(v.p) & 15) | ((v.batch | v.row | v.head) & m)) == 0;
 }
 
-long long n_items(const QkRopeArgs& a, int per) {
-  const int chunks = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
-  return (long long)a.batch * a.rows * chunks;
+// Items of `per` heads, and the CTAs of either kind: as many as there is work
+// for, in proportion to it where `most` are less.
+int share(QkRopeArgs& a, int per, long long most) {
+  long long need[2];
+  for (int k = 0; k < 2; ++k) {
+    a.items[k] = a.batch * a.rows * ((a.heads[k] + per - 1) / per);
+    need[k] = (a.items[k] + kWarps - 1) / kWarps;
+  }
+  const long long all = need[0] + need[1];
+  if (all > most)
+    for (int k = 0; k < 2; ++k)
+      if (need[k] > 0) need[k] = std::max(1LL, need[k] * (most - 1) / all);
+  a.split = (int)need[0];
+  return (int)(need[0] + need[1]);
 }
 
 template <typename T, int D>
-cudaError_t launch_heads(QkRopeArgs a, bool bwd, int max_ctas, int* ctas, cudaStream_t s) {
-  a.items = n_items(a, 32 / (D / 8) * (bwd ? 2 : 4));
-  const long long need = (a.items + kWarps - 1) / kWarps;
-  *ctas = (int)(bwd ? std::min<long long>(need, max_ctas) : need);
+cudaError_t launch_heads(QkRopeArgs& a, bool bwd, int max_ctas, int* ctas, cudaStream_t s) {
+  *ctas = share(a, 32 / (D / 8) * (bwd ? BU : FU), bwd ? max_ctas : 1LL << 30);
   return bwd ? launch_pdl(qk_rope_bwd_kernel<T, D>, dim3(*ctas), dim3(kThreads), 0, s, a)
              : launch_pdl(qk_rope_kernel<T, D>, dim3(*ctas), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
 
-// Four CTAs of 256 threads per SM keep enough loads in flight.
-int qk_rope_max_ctas(int num_sms) { return 4 * num_sms; }
+#ifndef BC
+#define BC BB
+#endif
+int qk_rope_max_ctas(int num_sms) { return BC * num_sms; }
 
 int launch_qk_rope(const QkRopeArgs& args, int bf16, bool bwd, int num_sms, float* dq_gain,
                    float* dk_gain, cudaStream_t s) {
@@ -380,14 +399,13 @@ int launch_qk_rope(const QkRopeArgs& args, int bf16, bool bwd, int num_sms, floa
   } else if (wide && a.d == 128) {
     e = launch_heads<float, 128>(a, bwd, max_ctas, &ctas, s);
   } else {
-    a.items = n_items(a, 1);
-    ctas = (int)std::min<long long>((a.items + kWarps - 1) / kWarps, max_ctas);
+    ctas = share(a, 1, max_ctas);
     e = bwd ? launch_pdl(qk_rope_any_kernel<true>, dim3(ctas), dim3(kThreads), 0, s, a)
             : launch_pdl(qk_rope_any_kernel<false>, dim3(ctas), dim3(kThreads), 0, s, a);
   }
   if (e != cudaSuccess || !bwd) return (int)e;
-  return (int)launch_pdl(qk_rope_gain_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, s,
-                         a.partial, ctas, a.d, dq_gain, dk_gain);
+  return (int)launch_pdl(qk_rope_gain_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s,
+                         a.partial, a.split, ctas, a.d, dq_gain, dk_gain);
 }
 
 }  // namespace df
