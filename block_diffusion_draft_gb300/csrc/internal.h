@@ -396,11 +396,29 @@ struct HeadView {
   long long batch, row, head;
 };
 
+// Quotients of numbers below 2^31 by a number known on the host: a product's
+// upper half, a sum and a shift.
+struct Divisor {
+  int d = 1, shift = 0;
+  unsigned mul = 1;
+  Divisor() = default;
+  explicit Divisor(int by) : d(by > 0 ? by : 1) {
+    while ((1LL << shift) < d) ++shift;
+    mul = (unsigned)(((1ULL << 32) * ((1ULL << shift) - (unsigned)d)) / (unsigned)d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int n) const {
+    return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+  }
+#endif
+};
+
 // One call of dflash_qk_norm_rope or its backward (qk_rope.cu); index 0: the
 // queries, 1: the keys (0 heads where a call has none).
 struct QkRopeArgs {
   int batch, rows, d, max_pos;
   int heads[2];
+  Divisor chunks[2], by_rows;  // set by the launch: units of a row, rows of a sequence
   int items[2], split;         // set by the launch: warps' units of work, CTAs of the queries
   float eps;
   const float2* rope;          // [max_pos][d / 2] (cos, sin)
