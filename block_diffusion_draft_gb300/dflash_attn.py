@@ -7,6 +7,7 @@ library's CUDA kernels; if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from array import array
@@ -32,11 +33,6 @@ class Config(ctypes.Structure):
                 ("n_target_layers", c_int32), ("rms_eps", c_float),
                 ("rope_theta", c_float), ("sliding_window", c_int32),
                 ("max_position", c_int32), ("dtype", c_int32), ("causal", c_int32)]
-
-
-class Heads(ctypes.Structure):
-    _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("row_stride", c_int64),
-                ("head_stride", c_int64)]
 
 
 class DFlashError(RuntimeError):
@@ -100,11 +96,9 @@ _SIGNATURES = {
                                 POINTER(c_int32), c_void_p, c_void_p, c_void_p], c_int),
     "dflash_verify": ([c_int] * 4 + [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64,
                                      c_int64] + [c_void_p] * 6, c_int),
-    "dflash_qk_norm_rope": ([c_void_p, c_int, c_int, POINTER(Heads), POINTER(Heads)] +
-                            [c_void_p] * 3 + [POINTER(Heads), POINTER(Heads), c_void_p], c_int),
+    "dflash_qk_norm_rope": ([c_void_p, c_int, c_int] + [c_void_p] * 8, c_int),
     "dflash_qk_norm_rope_workspace": ([c_void_p, POINTER(c_size_t)], c_int),
-    "dflash_qk_norm_rope_backward": ([c_void_p, c_int, c_int, POINTER(Heads), POINTER(Heads)] +
-                                     [c_void_p] * 3 + [POINTER(Heads)] * 4 + [c_void_p] * 3 +
+    "dflash_qk_norm_rope_backward": ([c_void_p, c_int, c_int] + [c_void_p] * 12 +
                                      [c_size_t, c_void_p], c_int),
     "dflash_linear_ce_workspace": ([c_int] * 4 + [POINTER(c_size_t)], c_int),
     "dflash_linear_ce": ([c_int] * 3 + [c_void_p, c_int64, c_void_p, c_int64] + [c_void_p] * 4 +
@@ -433,13 +427,11 @@ class DFlashAttention:
         by default dense tensors.  Returns (q_out, k_out)."""
         B, R = _rows_of(q, k)
         _require("positions", positions, torch.int32, self.device, (B, R))
-        qs, ks = self._heads("q", q, (B, R), self.n_heads), self._heads("k", k, (B, R),
-                                                                       self.n_kv_heads)
         q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-        _call(self.device, lib().dflash_qk_norm_rope, self.handle, B, R, qs, ks,
+        v, at = self._views((B, R), q, k, q_out, k_out)
+        _call(self.device, lib().dflash_qk_norm_rope, self.handle, B, R, at[0], at[1],
               self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
-              self._heads("q_out", q_out, (B, R), self.n_heads),
-              self._heads("k_out", k_out, (B, R), self.n_kv_heads))
+              at[2], at[3])
         return q_out, k_out
 
     def qk_norm_rope_backward(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -453,40 +445,50 @@ class DFlashAttention:
         d_q_norm, d_k_norm), the gains' in fp32, None for q or k None."""
         B, R = _rows_of(q, k)
         _require("positions", positions, torch.int32, self.device, (B, R))
-        nq, nkv = self.n_heads, self.n_kv_heads
-        qs, ks = self._heads("q", q, (B, R), nq), self._heads("k", k, (B, R), nkv)
         if (q is None) != (d_q is None) or (k is None) != (d_k is None):
             raise ValueError("d_q and d_k must be given exactly where q and k are")
         dq_out, dk_out = _like(q, dq_out, "dq_out"), _like(k, dk_out, "dk_out")
-        f32 = lambda t: None if t is None else torch.empty(  # noqa: E731
-            self.head_dim, device=self.device, dtype=torch.float32)
-        dgq, dgk = f32(q), f32(k)
+        v, at = self._views((B, R), q, k, d_q, d_k, dq_out, dk_out)
         if self._rope_ws is None:
             n = c_size_t(0)
             check(lib().dflash_qk_norm_rope_workspace(self.handle, byref(n)))
             self._rope_ws = n.value
-        ws = torch.empty(self._rope_ws, device=self.device, dtype=torch.uint8)
-        _call(self.device, lib().dflash_qk_norm_rope_backward, self.handle, B, R, qs, ks,
+        # one allocation: the gains' gradients, then the workspace
+        d = self.head_dim
+        pad = (2 * d + 63) // 64 * 64
+        buf = torch.empty(pad + self._rope_ws // 4, device=self.device, dtype=torch.float32)
+        p = buf.data_ptr()
+        _call(self.device, lib().dflash_qk_norm_rope_backward, self.handle, B, R, at[0], at[1],
               self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
-              self._heads("d_q", d_q, (B, R), nq), self._heads("d_k", d_k, (B, R), nkv),
-              self._heads("dq_out", dq_out, (B, R), nq), self._heads("dk_out", dk_out, (B, R), nkv),
-              _p(dgq), _p(dgk), ws.data_ptr(), self._rope_ws)
-        return dq_out, dk_out, dgq, dgk
+              at[2], at[3], at[4], at[5], None if q is None else p,
+              None if k is None else p + 4 * d, p + 4 * pad, self._rope_ws)
+        return (dq_out, dk_out, None if q is None else buf[:d],
+                None if k is None else buf[d:2 * d])
 
-    def _heads(self, name: str, t: Optional[torch.Tensor], rows: Tuple[int, int],
-               heads: int) -> Optional[Heads]:
-        if t is None:
-            return None
-        if t.shape != (*rows, heads, self.head_dim):
-            raise ValueError(f"{name} must be {[*rows, heads, self.head_dim]}, "
-                             f"got {list(t.shape)}")
-        if t.dtype is not self.dtype or not _on(t, self.device):
-            raise ValueError(f"{name} must be {self.dtype} on {self.device}, "
-                             f"got {t.dtype} on {t.device}")
-        s = t.stride()
-        if s[3] != 1 and t.numel():
-            raise ValueError(f"{name}: a head's channels must be dense")
-        return Heads(t.data_ptr() or 16, s[0], s[1], s[2])  # (no data: no rows)
+    def _views(self, rows: Tuple[int, int], *tensors: Optional[torch.Tensor]):
+        """dflash_heads of tensors of queries and keys in turn: an array of
+        (address, batch, row and head stride) that has to outlive the call, and
+        the addresses of its parts (None for None)."""
+        flat, dt, d, index = [], self.dtype, self.head_dim, self.device.index
+        shapes = ((*rows, self.n_heads, d), (*rows, self.n_kv_heads, d))
+        for i, t in enumerate(tensors):
+            if t is None:
+                flat += (0, 0, 0, 0)
+                continue
+            on = t.get_device()  # -1: not on a CUDA device
+            if t.shape != shapes[i & 1] or t.dtype is not dt or (
+                    on != index and (index is not None or on < 0)):
+                name = "qk"[i & 1]
+                raise ValueError(f"{name} and what belongs to it must be {list(shapes[i & 1])}, "
+                                 f"{dt} on {self.device}, got {list(t.shape)}, {t.dtype} on "
+                                 f"{t.device}")
+            s = t.stride()
+            if s[3] != 1 and t.numel():
+                raise ValueError("a head's channels must be dense")
+            flat += (t.data_ptr() or 16, s[0], s[1], s[2])  # (no data: no rows)
+        v = array("q", flat)
+        base = v.buffer_info()[0]
+        return v, [None if t is None else base + 32 * i for i, t in enumerate(tensors)]
 
     def _gain(self, name: str, t: Optional[torch.Tensor]) -> Optional[int]:
         if t is None:
@@ -775,35 +777,41 @@ def linear_cross_entropy_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.T
     return _linear_ce(x, w, targets, d_nll, 2 if need_dw else 1)
 
 
+@functools.lru_cache(maxsize=64)
+def _linear_ce_workspace(rows: int, vocab: int, hidden: int, grads: int) -> int:
+    size = c_size_t(0)
+    check(lib().dflash_linear_ce_workspace(rows, vocab, hidden, grads, byref(size)))
+    return size.value
+
+
 def _linear_ce(x, w, targets, d_nll, grads: int):
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError(f"x must be [N, H] and w [V, H], got {list(x.shape)} and "
                          f"{list(w.shape)}")
     (N, H), V, dev = x.shape, w.shape[0], w.device
-    if not w.is_cuda:
+    if dev.type != "cuda":
         raise ValueError("the library runs on CUDA devices only")
-    for name, t in (("x", x), ("w", w)):
-        if t.dtype is not torch.bfloat16 or t.device != dev:
-            raise ValueError(f"{name} must be bfloat16 on {dev}, got {t.dtype} on {t.device}")
-        if t.stride(1) != 1 and H > 1 and t.numel():
-            raise ValueError(f"{name}: a row's values must be dense")
+    if x.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16 or x.device != dev:
+        raise ValueError(f"x and w must be bfloat16 on {dev}, got {x.dtype} on {x.device} and "
+                         f"{w.dtype}")
+    xs, ws = x.stride(), w.stride()
+    if (xs[1] != 1 and H > 1 and x.numel()) or (ws[1] != 1 and H > 1 and w.numel()):
+        raise ValueError("x, w: a row's values must be dense")
     _require("targets", targets, torch.int32, dev, (N,))
     if grads:
         _require("d_nll", d_nll, torch.float32, dev, (N,))
-    size = c_size_t(0)
-    check(lib().dflash_linear_ce_workspace(N, V, H, grads, byref(size)))
-    ws = torch.empty(size.value, device=dev, dtype=torch.uint8)
-    nll = torch.empty(2, N, device=dev, dtype=torch.float32)
-    nll, lse = nll[0], nll[1]
-    args = (N, V, H, x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0), targets.data_ptr())
+    size = _linear_ce_workspace(N, V, H, grads)
+    space = torch.empty(size, device=dev, dtype=torch.uint8)
+    nll, lse = torch.empty((2, N), device=dev, dtype=torch.float32).unbind(0)
     if not grads:
-        _call(dev, lib().dflash_linear_ce, *args, nll.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-              size.value)
+        _call(dev, lib().dflash_linear_ce, N, V, H, x.data_ptr(), xs[0], w.data_ptr(), ws[0],
+              targets.data_ptr(), nll.data_ptr(), lse.data_ptr(), space.data_ptr(), size)
         return nll, lse, None, None
-    dx = torch.empty(N, H, device=dev, dtype=torch.bfloat16)
-    dw = torch.empty(V, H, device=dev, dtype=torch.bfloat16) if grads == 2 else None
-    _call(dev, lib().dflash_linear_ce_grad, *args, d_nll.data_ptr(), nll.data_ptr(),
-          lse.data_ptr(), dx.data_ptr(), _p(dw), ws.data_ptr(), size.value)
+    dx = torch.empty((N, H), device=dev, dtype=torch.bfloat16)
+    dw = torch.empty((V, H), device=dev, dtype=torch.bfloat16) if grads == 2 else None
+    _call(dev, lib().dflash_linear_ce_grad, N, V, H, x.data_ptr(), xs[0], w.data_ptr(), ws[0],
+          targets.data_ptr(), d_nll.data_ptr(), nll.data_ptr(), lse.data_ptr(), dx.data_ptr(),
+          None if dw is None else dw.data_ptr(), space.data_ptr(), size)
     return nll, lse, dx, dw
 
 
@@ -825,6 +833,13 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
 _GRAD_TYPES = {torch.bfloat16: DFLASH_BF16, torch.float32: DFLASH_FP32}
 
 
+@functools.lru_cache(maxsize=64)
+def _grad_norm_workspace(n: int) -> int:
+    size = c_size_t(0)
+    check(lib().dflash_grad_norm_workspace(n, byref(size)))
+    return size.value
+
+
 def _grad_norm(grads, max_norm, out) -> torch.Tensor:
     grads = list(grads)
     if not grads:
@@ -832,37 +847,35 @@ def _grad_norm(grads, max_norm, out) -> torch.Tensor:
     dev, n = grads[0].device, len(grads)
     if dev.type != "cuda":
         raise ValueError("the library runs on CUDA devices only")
-    for i, g in enumerate(grads):
-        if g.dtype not in _GRAD_TYPES or g.device != dev:
-            raise ValueError(f"gradient {i} must be float32 or bfloat16 on {dev}, "
-                             f"got {g.dtype} on {g.device}")
-        if not _dense(g):
-            raise ValueError(f"gradient {i} must be dense")
+    # (whole lists at a time: a training step has hundreds of tensors)
+    types = [_GRAD_TYPES.get(g.dtype) for g in grads]
+    if None in types or any([g.get_device() != dev.index for g in grads]):
+        raise ValueError(f"gradients must be float32 or bfloat16 on {dev}")
+    dense = [g.is_contiguous() for g in grads]
+    if not all(dense) and not all([c or _dense(g) for c, g in zip(dense, grads)]):
+        raise ValueError("gradients must be dense")
+    ptrs = array("Q", [g.data_ptr() for g in grads])
     outs = None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out must hold {n} tensors, got {len(out)}")
-        for i, (g, o) in enumerate(zip(grads, out)):
-            if o.dtype is not g.dtype or o.device != dev or o.shape != g.shape or (
-                    o.stride() != g.stride() and g.numel() > 1):
-                raise ValueError(f"out {i} must have the shape, strides, type and device of "
-                                 f"gradient {i}")
-        outs = (c_void_p * n)(*[o.data_ptr() for o in out])
-    ptrs = (c_void_p * n)(*[g.data_ptr() for g in grads])
-    counts = (c_int64 * n)(*[g.numel() for g in grads])
-    types = (c_int32 * n)(*[_GRAD_TYPES[g.dtype] for g in grads])
-    size = c_size_t(0)
-    check(lib().dflash_grad_norm_workspace(n, byref(size)))
-    ws = torch.empty(size.value, device=dev, dtype=torch.uint8)
-    norm = torch.empty((), device=dev, dtype=torch.float32)
+        for g, o, c in zip(grads, out, dense):
+            if o.dtype is not g.dtype or o.get_device() != dev.index or o.shape != g.shape or not (
+                    c and o.is_contiguous() or o.stride() == g.stride() or g.numel() <= 1):
+                raise ValueError("out must have the gradients' shapes, strides, types and device")
+        outs = array("Q", [o.data_ptr() for o in out])
+    counts, types = array("q", [g.numel() for g in grads]), array("i", types)
+    size = _grad_norm_workspace(n)
+    # one allocation: the norm, then the workspace
+    buf = torch.empty(64 + size // 4, device=dev, dtype=torch.float32)
+    p = buf.data_ptr()
+    lists = [a if a is None else a.buffer_info()[0] for a in (ptrs, outs, counts, types)]
     if max_norm is None:
-        _call(dev, lib().dflash_grad_norm, n, ptrs, counts, types, norm.data_ptr(), ws.data_ptr(),
-              size.value)
+        _call(dev, lib().dflash_grad_norm, n, lists[0], lists[2], lists[3], p, p + 256, size)
     else:
-        _call(dev, lib().dflash_clip_grad_norm, n, ptrs, outs, counts, types, max_norm,
-              norm.data_ptr(), ws.data_ptr(), size.value)
-    return norm
+        _call(dev, lib().dflash_clip_grad_norm, n, *lists, max_norm, p, p + 256, size)
+    return buf[0]
 
 
 def _dense(t: torch.Tensor) -> bool:

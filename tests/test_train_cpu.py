@@ -21,7 +21,8 @@ FAKE = 0x1000
 
 
 def test_norm_and_rotation_reject_null_handles(L):
-    h = D.Heads(FAKE, 0, 0, 0)
+    h = (ctypes.c_int64 * 4)(FAKE, 0, 0, 0)
+    h = ctypes.cast(h, ctypes.c_void_p)
     n = ctypes.c_size_t(0)
     assert L.dflash_qk_norm_rope(None, 1, 1, h, h, None, None, FAKE, h, h, None) == -1
     assert b"null" in L.dflash_last_error()
