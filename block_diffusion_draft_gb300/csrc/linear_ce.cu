@@ -15,6 +15,9 @@
 //   GRAD  x w^T of one piece again, now with the row's lse known:
 //         d * (p - [v = t]) in bf16
 //   OUT   its transpose times x: dw's rows of the piece
+// Where the whole vocabulary is one piece, GRAD's product is saved: EXP keeps 8
+// more bits of every exponential, which scaled by the row's sum and rounded to
+// bf16 once are what GRAD computes.
 // The exponentials need no row maximum: a sum of products is linear in them,
 // so dx needs the logits once (EXP, ACC: 4 N V H operations) and is divided by
 // the row's sum at the end.  The reference is the target's logit; a row in
@@ -35,7 +38,9 @@ namespace df {
 namespace {
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int kThreads = 192;  // producer, MMA and four epilogue warps
+constexpr int kEpiWarps = 8;   // two for each quarter of TMEM's lanes, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // and the producer's and the MMA's warp
+constexpr int HN = BN / 2;     // columns of an epilogue warp, and of the sums that it writes
 constexpr uint32_t A_BYTES = BM * BK * 2;
 constexpr uint32_t SLAB = 4096;  // 32 rows of 128 bytes: what a warp stores at a time
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,7 +54,7 @@ struct Geo {
   static constexpr uint32_t B_BYTES = BN / CG * BK * 2;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = CG == 2 ? 6 : 4;
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE + 8 * SLAB + 256;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + kEpiWarps * SLAB + 256;
 };
 
 enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
@@ -61,13 +66,15 @@ struct CeGemm {
   int v0;              // first column of the piece
   int vocab, hidden;
   int rows_pad;
+  uint8_t* low;        // EXP: null, or [rows_pad][low_pitch] the exponentials' next 8 bits
+  int low_pitch;
   const float* ref2;   // EXP: the rows' references; GRAD: their lse, log2 units
   const int* target;
   const float* d;      // GRAD: gradients of the rows' nll
   const float* miss;   // GRAD: 1 - p_t
-  float* part_m;       // [rows_pad][all_tiles], log2 units
+  float* part_m;       // [rows_pad][parts], log2 units: of 128 columns each
   float* part_s;
-  int all_tiles;
+  int parts;
   const int* any;      // EXP: null, or whether a repair has anything to do
   const int* repair;   // and the flags of 32-row groups: only their tiles
   int add;             // ACC: the buffer holds earlier pieces
@@ -228,19 +235,12 @@ DF_DEV bool wanted(const CeGemm& p, const Tile& t) {
   return any;
 }
 
-// The 32-column pieces of a warp's output go through a 4 KB slab in the layout
-// of the 128-byte swizzle: 16-byte chunk c of row r at place c ^ (r % 8).
-struct Slabs {
-  uint8_t* base;  // two slabs of this warp
-  int next;
-  // the slab to fill, once the copy that last read it has
-  DF_DEV uint8_t* begin(int lane) {
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    return base + next * SLAB;
-  }
-  DF_DEV void end() { next ^= 1; }
-};
+// What a warp stores goes through a 4 KB slab of its own in the layout of the
+// 128-byte swizzle: 16-byte chunk c of row r at place c ^ (r % 8).
+DF_DEV void slab_begin(int lane) {  // once the copy that last read it has
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+}
 
 DF_DEV void slab_put(uint8_t* slab, int lane, int chunk, uint4 v) {
   *reinterpret_cast<uint4*>(slab + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* slabs = smem + G::STAGES * G::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + 8 * SLAB);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + kEpiWarps * SLAB);
   uint64_t* empty = full + G::STAGES;
   uint64_t* acc_full = empty + G::STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4 * CG);
+      mbar_init(&acc_empty[b], kEpiWarps * CG);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3;
-    Slabs out{slabs + q * 2 * SLAB, 0};
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* slab = slabs + (warp - 2) * SLAB;
     uint32_t tc = 0;
     for (int u = first; u < units; u += stride) {
       const Tile t = tile_at(p, m_tiles, n_kb, u);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tgt = -1;
       float ref = 0.f, sc = 0.f, miss = 0.f;
       if (EPI <= GRAD && live) {
-        tgt = __ldcg(p.target + row) - p.v0 - t.n * BN;  // its column in this tile
+        tgt = __ldcg(p.target + row) - p.v0 - t.n * BN - half * HN;  // its column of this warp's
         if (EPI != LSE) ref = __ldcg(p.ref2 + row);
         if (EPI == GRAD) {
           sc = __ldcg(p.d + row);
@@ -394,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         tc_fence_after();
       }
-      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * BN;
-      const int cols = EPI <= GRAD ? p.vocab - p.v0 - t.n * BN : BN;  // that exist
+      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * HN;
+      const int x0 = t.n * BN + half * HN;  // first column of this warp
+      const int cols = p.vocab - p.v0 - x0;  // logits: columns that exist
       float mx = kNegInf, sum = 0.f;
-      uint8_t* slab = nullptr;
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < HN / 32; ++c) {
         float v[32];
         if (any) {
           tmem_read32(trow + c * 32, v);
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if (c == BN / 32 - 1 && any) {  // read: back to the MMA warp
+        if (c == HN / 32 - 1 && any) {  // read: back to the MMA warp
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -458,45 +458,73 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (EPI == ACC) {
-          slab = out.begin(lane);
+          slab_begin(lane);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             slab_put(slab, lane, j,
                      make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                 __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
         } else {
-          if ((c & 1) == 0) slab = out.begin(lane);
+          if ((c & 1) == 0) slab_begin(lane);
+          if (EPI == EXP && p.low != nullptr) {
+            // 24 bits of every number: rounded there, the upper 16 rounded from
+            // those to a bf16 number, and the byte below as what is left (a
+            // signed number: carries are in the upper ones)
+            uint32_t lo[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            slab_put(slab, lane, (c & 1) * 4 + j,
-                     make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
-                                pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+            for (int j = 0; j < 8; ++j) {
+              uint32_t b[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[4 * j + i]) + 0x80u;
+              lo[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0051), __byte_perm(b[2], b[3], 0x0051),
+                                  0x5410);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[4 * j + i] = __uint_as_float(b[i] + 0x8000u);
+            }
+            uint4* at = reinterpret_cast<uint4*>(p.low + (size_t)row * p.low_pitch + x0 + c * 32);
+            at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                h[i] = __byte_perm(__float_as_uint(v[8 * j + 2 * i]),
+                                   __float_as_uint(v[8 * j + 2 * i + 1]), 0x7632);
+              slab_put(slab, lane, (c & 1) * 4 + j, make_uint4(h[0], h[1], h[2], h[3]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              slab_put(slab, lane, (c & 1) * 4 + j,
+                       make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                  pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                  pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+          }
           if ((c & 1) == 0) continue;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           if (EPI == ACC) {
-            const int x = t.n * BN + c * 32;
+            const int x = x0 + c * 32;
             if (x < p.hidden) {
               if (p.add) add_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
               else store_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
             }
           } else if (EPI == OUT) {
-            const int x = t.n * BN + (c - 1) * 32, y = p.v0 + row0;
+            const int x = x0 + (c - 1) * 32, y = p.v0 + row0;
             if (x < p.hidden && y < p.vocab) store_box(&tm_out, slab, x, y);
           } else {
-            store_box(&tm_out, slab, t.n * BN + (c - 1) * 32, row0);
+            store_box(&tm_out, slab, x0 + (c - 1) * 32, row0);
           }
           bulk_commit();
         }
-        out.end();
       }
       if (EPI == LSE || EPI == EXP) {
         if (live) {
-          const size_t at = (size_t)row * p.all_tiles + p.v0 / BN + t.n;
+          const size_t at = (size_t)row * p.parts + (p.v0 + x0) / HN;
           p.part_m[at] = mx;
           p.part_s[at] = sum;
         }
@@ -533,7 +561,8 @@ struct CeRows {
   float* z_t;          // compact: the target's logit
   float* ref2;         // compact: reference, log2 units
   float* d;            // compact
-  __nv_bfloat16* xc;   // [rows_pad][hidden]
+  __nv_bfloat16* xc;   // [rows_pad][pitch]
+  int pitch;           // hidden rounded up: rows on 128-byte boundaries
 };
 
 DF_DEV bool has_target(const CeRows& a, int r) {
@@ -615,14 +644,14 @@ __global__ void __launch_bounds__(kRowThreads) ce_gather_kernel(const __grid_con
     if (row < a.rows) c = __ldcg(a.place + row);
   }
   if (row < 256 && n + row < (n + 255) / 256 * 256) {
-    uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)(n + row) * a.hidden);
+    uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)(n + row) * a.pitch);
     for (int i = threadIdx.x; i < n8; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
   }
   if (c < 0) return;
   const int t = __ldg(a.targets + row);
   const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.x_stride);
   const uint4* w = reinterpret_cast<const uint4*>(a.w + t * a.w_stride);
-  uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)c * a.hidden);
+  uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)c * a.pitch);
   float s = 0.f;
   for (int i = threadIdx.x; i < n8; i += kRowThreads) {
     const uint4 v = __ldg(x + i);
@@ -645,13 +674,13 @@ __global__ void __launch_bounds__(kRowThreads) ce_gather_kernel(const __grid_con
 
 struct CeUpdate {
   const int* n;
-  int rows_pad, hidden, first_tile, tiles, all_tiles, slices;
+  int rows_pad, pitch, first, n_parts, parts, slices;  // `n_parts` from `first` on
   const float* part_m;
   float* ref2;
   float* hist;   // [rows_pad] of this piece
   int* flag;     // [rows_pad / 32]
   int* any;      // of this piece
-  float* acc;    // [slices][rows_pad][hidden], earlier pieces; null: none
+  float* acc;    // [slices][rows_pad][pitch], earlier pieces; null: none
 };
 
 // After a piece's exponentials, a warp per row: rows whose largest logit
@@ -665,9 +694,9 @@ __global__ void __launch_bounds__(1024) ce_update_kernel(const __grid_constant__
   const bool live = row < __ldcg(a.n);
   float f = 1.f;
   if (live) {
-    const float* part = a.part_m + (size_t)row * a.all_tiles + a.first_tile;
+    const float* part = a.part_m + (size_t)row * a.parts + a.first;
     float m = kNegInf;
-    for (int t = lane; t < a.tiles; t += 32) m = fmaxf(m, __ldcg(part + t));
+    for (int t = lane; t < a.n_parts; t += 32) m = fmaxf(m, __ldcg(part + t));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = __ldcg(a.ref2 + row);
@@ -689,24 +718,25 @@ __global__ void __launch_bounds__(1024) ce_update_kernel(const __grid_constant__
     const float k = factor[r];
     if (k == 1.f) continue;
     for (int s = 0; s < a.slices; ++s) {
-      float* v = a.acc + ((size_t)s * a.rows_pad + blockIdx.x * 32 + r) * a.hidden;
-      for (int i = threadIdx.x; i < a.hidden; i += 1024) v[i] *= k;
+      float* v = a.acc + ((size_t)s * a.rows_pad + blockIdx.x * 32 + r) * a.pitch;
+      for (int i = threadIdx.x; i < a.pitch; i += 1024) v[i] *= k;
     }
   }
 }
 
 struct CeSums {
-  const float* part_m;  // [rows_pad][tiles]
+  const float* part_m;  // [rows_pad][parts]
   const float* part_s;
-  const float* hist;    // gradient: [piece][rows_pad] the references of the tiles, log2 units
-  int tiles, piece_tiles;
+  const float* hist;    // gradient: [piece][rows_pad] the references of the sums, log2 units
+  int parts, piece_parts;
   float* nll;           // [rows]
   float* lse;
-  const float* acc;     // gradient: [slices][rows_pad][hidden]
+  const float* acc;     // gradient: [slices][rows_pad][pitch]
   int slices;
   __nv_bfloat16* dx;
   float* miss;          // compact: 1 - p_t
   float* lse2;          // compact: lse in log2 units
+  float* scale;         // compact: d / sum of the exponentials, with the last reference
 };
 
 // (m, s) and (m2, s2), sums relative to a reference each, as one
@@ -735,13 +765,19 @@ __global__ void __launch_bounds__(kRowThreads)
     return;
   }
   float m = kNegInf, sum = 0.f;
-  const float* pm = s.part_m + (size_t)c * s.tiles;
-  const float* ps = s.part_s + (size_t)c * s.tiles;
-  for (int t = threadIdx.x; t < s.tiles; t += kRowThreads)
-    join(m, sum,
-         s.hist != nullptr ? __ldcg(s.hist + (size_t)(t / s.piece_tiles) * a.rows_pad + c)
-                           : __ldcg(pm + t),
-         __ldcg(ps + t));
+  const float* pm = s.part_m + (size_t)c * s.parts;
+  const float* ps = s.part_s + (size_t)c * s.parts;
+  if (s.hist == nullptr) {
+    for (int t = threadIdx.x; t < s.parts; t += kRowThreads) join(m, sum, __ldcg(pm + t),
+                                                                  __ldcg(ps + t));
+  } else {
+    for (int i = 0, t0 = 0; t0 < s.parts; ++i, t0 += s.piece_parts) {
+      float one = 0.f;
+      for (int t = t0 + threadIdx.x; t < min(t0 + s.piece_parts, s.parts); t += kRowThreads)
+        one += __ldcg(ps + t);
+      join(m, sum, __ldcg(s.hist + (size_t)i * a.rows_pad + c), one);
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
@@ -770,12 +806,14 @@ __global__ void __launch_bounds__(kRowThreads)
   const float d = __ldcg(a.d + c);
   const float f = failed ? nan : d * fast_exp2(__ldcg(a.ref2 + c) - top) / total;
   const float g = d * (others / total);
+  if (threadIdx.x == 0) s.scale[c] = f;
   const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
   for (int i = threadIdx.x; i < n8; i += kRowThreads) {
     float v[8] = {};
+#pragma unroll 4
     for (int k = 0; k < s.slices; ++k) {
       const float4* p = reinterpret_cast<const float4*>(
-                            s.acc + ((size_t)k * a.rows_pad + c) * a.hidden) + 2 * i;
+                            s.acc + ((size_t)k * a.rows_pad + c) * a.pitch) + 2 * i;
       const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
       v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
       v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
@@ -791,19 +829,47 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// The kept exponentials of a piece that is the whole vocabulary, with their
+// sums known: 24-bit numbers times the row's scale, rounded to bf16 once, the
+// target's in its place.  A row and 2048 columns per CTA.
+__global__ void __launch_bounds__(kRowThreads)
+    ce_scale_kernel(const __grid_constant__ CeRows a, __nv_bfloat16* g, const uint8_t* low,
+                    int pitch, const float* scale, const float* miss) {
+  grid_dep_sync();
+  const int row = blockIdx.x, col = (blockIdx.y * kRowThreads + threadIdx.x) * 8;
+  if (row >= __ldcg(a.n) || col >= pitch) return;
+  uint4* at = reinterpret_cast<uint4*>(g + (size_t)row * pitch + col);
+  const uint4 hi = *at;
+  const uint2 lo = __ldcg(reinterpret_cast<const uint2*>(low + (size_t)row * pitch + col));
+  const float s = __ldcg(scale + row);
+  const int t = __ldcg(a.target + row) - col;
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t up = (i & 1) ? h[i >> 1] & 0xffff0000u : h[i >> 1] << 16;
+    const int down = (int)(int8_t)((i < 4 ? lo.x : lo.y) >> (8 * (i & 3)));
+    v[i] = __uint_as_float(up + (uint32_t)(down * 256)) * s;
+    if (i == t) v[i] = -__ldcg(a.d + row) * __ldcg(miss + row);
+  }
+  *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+}
+
 // ----------------------------------------------------------------- the host
-constexpr size_t kPieceBytes = 512ull << 20;  // of a piece's exponentials
+constexpr size_t kPieceBytes = 1ull << 30;  // of a piece's exponentials
 constexpr int kMaxSplits = 16;
 // Up to here every CTA of the gather counts the targets in front of its row
 // itself (16 KB from L2 each): a launch less.
 constexpr int kScanRows = 4096;
 
 struct Plan {
-  int cg, rows_pad, n_tiles;
+  int cg, rows_pad, pitch, n_tiles;
   int piece, pieces;   // columns of a piece (a multiple of 256)
   int splits;          // of ACC's K
-  size_t any, place, target, z_t, ref2, d, miss, lse2, hist, flag, xc, part_m, part_s, g, acc,
-      total;
+  bool keep;           // dw from the exponentials that dx was made from
+  size_t any, place, target, z_t, ref2, d, miss, lse2, scale, hist, flag, xc, part_m, part_s, g,
+      low, acc, total;
 };
 
 // Splits of K for the products of few tiles: whole waves, and about 24
@@ -827,12 +893,14 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
   Plan p{};
   p.cg = rows <= BM ? 1 : 2;
   p.rows_pad = (rows + 255) / 256 * 256;
+  p.pitch = (hidden + 63) / 64 * 64;
   p.n_tiles = (vocab + BN - 1) / BN;
   const size_t most =
       std::max<size_t>(4096, kPieceBytes / (2 * (size_t)p.rows_pad) / BN * BN);
   p.pieces = (int)(((size_t)p.n_tiles * BN + most - 1) / most);
   p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * BN;
   p.pieces = (p.n_tiles * BN + p.piece - 1) / p.piece;
+  p.keep = grads == 2 && p.pieces == 1;
   const int m_tiles = (rows + p.cg * BM - 1) / (p.cg * BM), h_tiles = (hidden + BN - 1) / BN;
   p.splits = acc_splits(m_tiles * h_tiles, p.piece / BK, kPlanSms / p.cg);
   size_t at = 256;  // n, err
@@ -847,17 +915,19 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
   p.target = take(pad * 4);
   p.z_t = take(pad * 4);
   p.ref2 = take(pad * 4);
-  p.xc = take(pad * hidden * 2);
-  p.part_m = take(pad * p.n_tiles * 4);
-  p.part_s = take(pad * p.n_tiles * 4);
+  p.xc = take(pad * p.pitch * 2);
+  p.part_m = take(pad * p.n_tiles * 2 * 4);
+  p.part_s = take(pad * p.n_tiles * 2 * 4);
   if (grads > 0) {
     p.d = take(pad * 4);
     p.miss = take(pad * 4);
     p.lse2 = take(pad * 4);
+    p.scale = take(pad * 4);
     p.hist = take(pad * p.pieces * 4);
     p.flag = take(pad / 32 * 4);
     p.g = take(pad * p.piece * 2);
-    p.acc = take(pad * p.splits * hidden * 4);
+    if (p.keep) p.low = take(pad * p.piece);
+    p.acc = take(pad * p.splits * p.pitch * 4);
   }
   p.total = at;
   return p;
@@ -964,7 +1034,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
       e = cudaMemsetAsync(c.dw, 0, (size_t)c.vocab * c.hidden * 2, s);
     return done("memset");
   }
-  const Plan p = make_plan(c.rows, c.vocab, c.hidden, grad ? 1 : 0);
+  const Plan p = make_plan(c.rows, c.vocab, c.hidden, !grad ? 0 : c.dw == nullptr ? 1 : 2);
   char* base = static_cast<char*>(ws);
   auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
   auto i32 = [&](size_t at) { return reinterpret_cast<int*>(base + at); };
@@ -992,21 +1062,22 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   a.ref2 = f32(p.ref2);
   a.d = f32(p.d);
   a.xc = reinterpret_cast<__nv_bfloat16*>(base + p.xc);
+  a.pitch = p.pitch;
 
   // maps: x by rows and by channels, w the same, a piece's exponentials, the
   // fp32 products, dw
   const long long w_pitch = V > 1 ? c.w_stride : H;
   CUtensorMap x_k, w_k, x_mn, w_mn, g_k, g_mn, g_out, acc_out, dw_out;
-  int bad = make_map(&x_k, a.xc, false, pad, H, H, 64, BM) |
+  int bad = make_map(&x_k, a.xc, false, pad, H, p.pitch, 64, BM) |
             make_map(&w_k, c.w, false, V, H, w_pitch, 64, BN / p.cg);
   if (grad) {
     const void* g = base + p.g;
     bad |= make_map(&w_mn, c.w, false, V, H, w_pitch, 64, 64) |
            make_map(&g_k, g, false, pad, p.piece, p.piece, 64, BM) |
            make_map(&g_out, g, false, pad, p.piece, p.piece, 64, 32) |
-           make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, H, 32, 32);
+           make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, p.pitch, 32, 32);
     if (c.dw != nullptr)
-      bad |= make_map(&x_mn, a.xc, false, pad, H, H, 64, 64) |
+      bad |= make_map(&x_mn, a.xc, false, pad, H, p.pitch, 64, 64) |
              make_map(&g_mn, g, false, pad, p.piece, p.piece, 64, 64) |
              make_map(&dw_out, c.dw, false, V, H, H, 64, 32);
   }
@@ -1023,13 +1094,13 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   gm.target = a.target;
   gm.part_m = f32(p.part_m);
   gm.part_s = f32(p.part_s);
-  gm.all_tiles = p.n_tiles;
+  gm.parts = p.n_tiles * 2;
   gm.err = a.err;
   CeSums sums{};
   sums.part_m = gm.part_m;
   sums.part_s = gm.part_s;
-  sums.tiles = p.n_tiles;
-  sums.piece_tiles = p.piece / BN;
+  sums.parts = p.n_tiles * 2;
+  sums.piece_parts = p.piece / HN;
   sums.nll = c.nll;
   sums.lse = c.lse;
   const int m_tiles = (c.rows + p.cg * BM - 1) / (p.cg * BM);
@@ -1052,11 +1123,12 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   sums.dx = static_cast<__nv_bfloat16*>(c.dx);
   sums.miss = f32(p.miss);
   sums.lse2 = f32(p.lse2);
+  sums.scale = f32(p.scale);
   CeUpdate up{};
   up.n = a.n;
   up.rows_pad = pad;
-  up.hidden = H;
-  up.all_tiles = p.n_tiles;
+  up.pitch = p.pitch;
+  up.parts = p.n_tiles * 2;
   up.slices = p.splits;
   up.part_m = gm.part_m;
   up.ref2 = a.ref2;
@@ -1066,9 +1138,13 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     CeGemm ex = gm;
     ex.v0 = v0;
     ex.n_tiles = tiles;
+    if (p.keep) {
+      ex.low = reinterpret_cast<uint8_t*>(base + p.low);
+      ex.low_pitch = p.piece;
+    }
     e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
-    up.first_tile = v0 / BN;
-    up.tiles = tiles;
+    up.first = v0 / HN;
+    up.n_parts = tiles * 2;
     up.hist = f32(p.hist) + (size_t)i * pad;
     up.any = a.any + i;
     up.acc = i > 0 ? f32(p.acc) : nullptr;
@@ -1089,13 +1165,20 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   if (e == cudaSuccess) e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, sums);
   for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
     const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
-    CeGemm gr = gm;
-    gr.v0 = v0;
-    gr.n_tiles = tiles;
-    gr.ref2 = f32(p.lse2);
-    gr.d = a.d;
-    gr.miss = f32(p.miss);
-    e = launch_gemm<GRAD>(p.cg, x_k, w_k, g_out, gr, m_tiles * tiles, sms, s);
+    if (p.keep) {
+      e = launch_pdl(ce_scale_kernel, dim3(pad, (p.piece / 8 + kRowThreads - 1) / kRowThreads),
+                     b256, 0, s, a, reinterpret_cast<__nv_bfloat16*>(base + p.g),
+                     reinterpret_cast<const uint8_t*>(base + p.low), p.piece, f32(p.scale),
+                     f32(p.miss));
+    } else {
+      CeGemm gr = gm;
+      gr.v0 = v0;
+      gr.n_tiles = tiles;
+      gr.ref2 = f32(p.lse2);
+      gr.d = a.d;
+      gr.miss = f32(p.miss);
+      e = launch_gemm<GRAD>(p.cg, x_k, w_k, g_out, gr, m_tiles * tiles, sms, s);
+    }
     CeGemm ow = gm;
     ow.v0 = v0;
     ow.m_tiles = (tiles * BN + p.cg * BM - 1) / (p.cg * BM);

@@ -683,9 +683,10 @@ int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const d
  * rows have a target alone.
  *   workspace  device, 256-byte aligned, the caller's until the work is done;
  *              dflash_linear_ce_workspace gives its size for grads = 0 (nll and
- *              lse), 1 (dx) or 2 (dx and dw): at most about 512 MiB (and 4096
- *              columns' worth) for a piece's exponentials, and small multiples
- *              of rows * hidden and rows * vocab / 256.
+ *              lse), 1 (dx) or 2 (dx and dw): for a piece's exponentials at
+ *              most about 1 GiB (or 4096 columns' worth, if that is more; half as
+ *              much again with dw and all columns in one piece), and small
+ *              multiples of rows * hidden and rows * vocab / 128.
  * After a bounded wait that ran out nll and lse are NaN.  Work goes to the
  * current device.
  * Errors: _ARG, _SHAPE, _CAPACITY (workspace), _CUDA. */

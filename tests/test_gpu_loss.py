@@ -126,8 +126,8 @@ def test_every_row_far_apart():
 
 
 def test_several_pieces():
-    """The exponentials of 20000 rows and 30000 columns (1.2 GB) come in three
-    pieces; rows with a far logit in any of them."""
+    """The exponentials of 20000 rows and 30000 columns (1.2 GB) come in
+    two pieces; rows with a far logit in either."""
     x, w, t, d = inputs(20000, 30000, 64, 11, 0.01)
     for i, column in enumerate((5, 12000, 20000, 29999)):
         far_rows(x, w, t, range(100 + i, 20000, 4999), column, 90.0 + 30.0 * i)
