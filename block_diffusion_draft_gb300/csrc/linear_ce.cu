@@ -48,26 +48,32 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRefSlack = 80.f;  // binades that a logit may lie above its row's reference
 
-// CG CTAs work on one tile of CG * 128 rows and 256 columns.
-template <int CG>
+enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
+
+// CG CTAs work on one tile of CG * 128 rows and 256 columns.  Shared memory
+// holds the ring and the slabs of the epilogues that store through them: two a
+// warp where tiles are short (OUT's are as long as there are rows).
+template <int EPI, int CG>
 struct Geo {
   static constexpr uint32_t B_BYTES = BN / CG * BK * 2;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = CG == 2 ? 6 : 4;
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE + kEpiWarps * SLAB + 256;
+  static constexpr int SLABS = EPI == ACC ? 1 : EPI == OUT ? 2 : 0;
+  static constexpr size_t FIXED = 1024 + SLABS * kEpiWarps * SLAB + 256;
+  static constexpr int STAGES = (int)((232448 - FIXED) / STAGE);
+  static constexpr size_t SMEM = FIXED + STAGES * STAGE;
 };
-
-enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
 
 struct CeGemm {
   const int* n_rows;   // device: rows with a target
   int m_tiles;         // OUT: tiles of the piece's columns
   int n_tiles, n_kb, splits;
+  Divisor by_group;    // kGroup * n_tiles
   int v0;              // first column of the piece
   int vocab, hidden;
   int rows_pad;
-  uint8_t* low;        // EXP: null, or [rows_pad][low_pitch] the exponentials' next 8 bits
-  int low_pitch;
+  uint8_t* g;          // EXP, GRAD: [rows_pad][g_pitch] bf16
+  uint8_t* low;        // EXP: null, or [rows_pad][g_pitch] the exponentials' next 8 bits
+  int g_pitch;
   const float* ref2;   // EXP: the rows' references; GRAD: their lse, log2 units
   const int* target;
   const float* d;      // GRAD: gradients of the rows' nll
@@ -176,25 +182,16 @@ DF_DEV void bulk_wait_read() {
 }
 DF_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// 32 fp32 columns of this thread's TMEM lane; the wait is part of the
-// statement, so that no use of the values comes before it
-DF_DEV void tmem_read32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+// 32 fp32 columns of this thread's TMEM lane: the load, and the wait, through
+// which the values go so that no use of them comes before it
+DF_DEV void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // D fp32, A and B bf16, K-major or MN-major each
@@ -210,18 +207,22 @@ struct Tile {
 
 // Tiles in groups of 8 row tiles, column tiles outside: the CTAs that run at
 // the same time share their operands in L2.
+constexpr int kGroup = 8;
+
 DF_DEV Tile tile_at(const CeGemm& p, int m_tiles, int n_kb, int u) {
-  constexpr int GM = 8;
-  const int per_split = m_tiles * p.n_tiles;
   Tile t;
-  t.split = u / per_split;
-  const int r = u - t.split * per_split;
-  const int g = r / (GM * p.n_tiles), gm = min(GM, m_tiles - g * GM);
-  const int rem = r - g * GM * p.n_tiles;
-  t.n = rem / gm;
-  t.m = g * GM + rem - t.n * gm;
-  t.k0 = (int)((long long)n_kb * t.split / p.splits);
-  t.k1 = (int)((long long)n_kb * (t.split + 1) / p.splits);
+  t.split = 0, t.k0 = 0, t.k1 = n_kb;
+  if (p.splits > 1) {
+    const int per_split = m_tiles * p.n_tiles;
+    t.split = u / per_split;
+    u -= t.split * per_split;
+    t.k0 = n_kb * t.split / p.splits;
+    t.k1 = n_kb * (t.split + 1) / p.splits;
+  }
+  const int g = p.by_group.quotient(u), left = m_tiles - g * kGroup;
+  const int rem = u - g * p.by_group.d;
+  t.n = left >= kGroup ? rem / kGroup : rem / left;
+  t.m = g * kGroup + rem - t.n * min(left, kGroup);
   return t;
 }
 
@@ -235,11 +236,20 @@ DF_DEV bool wanted(const CeGemm& p, const Tile& t) {
   return any;
 }
 
-// What a warp stores goes through a 4 KB slab of its own in the layout of the
-// 128-byte swizzle: 16-byte chunk c of row r at place c ^ (r % 8).
-DF_DEV void slab_begin(int lane) {  // once the copy that last read it has
-  if (lane == 0) bulk_wait_read<0>();
+// What a warp stores by bulk copies goes through slabs of 4 KB of its own, in
+// the layout of the 128-byte swizzle: 16-byte chunk c of row r at place
+// c ^ (r % 8).  A slab is filled once the copy that last read it has.
+template <int SLABS>
+DF_DEV void slab_begin(int lane) {
+  if (lane == 0) bulk_wait_read<SLABS - 1>();
   __syncwarp();
+}
+
+// 32 bytes: a whole sector
+DF_DEV void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 DF_DEV void slab_put(uint8_t* slab, int lane, int chunk, uint4 v) {
@@ -251,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CeGemm p) {
-  using G = Geo<CG>;
+  using G = Geo<EPI, CG>;
   constexpr bool kAmn = EPI == OUT, kBmn = EPI == ACC || EPI == OUT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* slabs = smem + G::STAGES * G::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + kEpiWarps * SLAB);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + G::SLABS * kEpiWarps * SLAB);
   uint64_t* empty = full + G::STAGES;
   uint64_t* acc_full = empty + G::STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
@@ -368,25 +378,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* slab = slabs + (warp - 2) * SLAB;
+    uint8_t* slab = slabs + (warp - 2) * G::SLABS * SLAB;
+    int other = (int)SLAB;  // from one slab to the other
+    // a row's part of an epilogue that looks at logits; the next tile's is
+    // read before this one's logits are waited for
+    struct Row {
+      int tgt = -1;
+      float ref = 0.f, sc = 0.f, miss = 0.f;
+    };
+    auto row_of = [&](const Tile& t) {
+      Row r;
+      const int row = (t.m * CG + rank) * BM + q * 32 + lane;
+      if (EPI <= GRAD && row < rows) {
+        r.tgt = __ldcg(p.target + row);
+        if (EPI != LSE) r.ref = __ldcg(p.ref2 + row);
+        if (EPI == GRAD) {
+          r.sc = __ldcg(p.d + row);
+          r.miss = __ldcg(p.miss + row);
+        }
+      }
+      return r;
+    };
     uint32_t tc = 0;
+    Tile next{};
+    Row next_row;
+    if (first < units) {
+      next = tile_at(p, m_tiles, n_kb, first);
+      next_row = row_of(next);
+    }
     for (int u = first; u < units; u += stride) {
-      const Tile t = tile_at(p, m_tiles, n_kb, u);
+      const Tile t = next;
+      const Row mine = next_row;
+      if (u + stride < units) {
+        next = tile_at(p, m_tiles, n_kb, u + stride);
+        next_row = row_of(next);
+      }
       if (!wanted<CG>(p, t)) continue;
       const bool any = t.k0 < t.k1;  // otherwise the tile is zero
       const int row0 = (t.m * CG + rank) * BM + q * 32, row = row0 + lane;
       const bool live = EPI == ACC || EPI == OUT || row < rows;
-      // this row's part of an epilogue that looks at logits
-      int tgt = -1;
-      float ref = 0.f, sc = 0.f, miss = 0.f;
-      if (EPI <= GRAD && live) {
-        tgt = __ldcg(p.target + row) - p.v0 - t.n * BN - half * HN;  // its column of this warp's
-        if (EPI != LSE) ref = __ldcg(p.ref2 + row);
-        if (EPI == GRAD) {
-          sc = __ldcg(p.d + row);
-          miss = __ldcg(p.miss + row);
-        }
-      }
+      const int x0 = t.n * BN + half * HN;   // first column of this warp
+      const int cols = p.vocab - p.v0 - x0;  // logits: columns that exist
+      const int tgt = mine.tgt - p.v0 - x0;  // the target's among them
+      const float sc = mine.sc, miss = mine.miss;
+      float ref = mine.ref;
       const uint32_t buf = tc & 1, use = tc >> 1;
       if (any) {
         ++tc;
@@ -395,25 +430,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * HN;
-      const int x0 = t.n * BN + half * HN;  // first column of this warp
-      const int cols = p.vocab - p.v0 - x0;  // logits: columns that exist
       float mx = kNegInf, sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < HN / 32; ++c) {
         float v[32];
         if (any) {
-          tmem_read32(trow + c * 32, v);
+          uint32_t raw[32];
+          tmem_ld32_nowait(trow + c * 32, raw);
+          tmem_wait32(raw);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+          if (c == HN / 32 - 1) {  // read: back to the MMA warp
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2) arrive_cluster(cluster_map(smem_u32(&acc_empty[buf]), 0));
+              else mbar_arrive(&acc_empty[buf]);
+            }
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        if (c == HN / 32 - 1 && any) {  // read: back to the MMA warp
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2) arrive_cluster(cluster_map(smem_u32(&acc_empty[buf]), 0));
-            else mbar_arrive(&acc_empty[buf]);
-          }
         }
         if (EPI <= GRAD) {
           // logits of the target and of columns that do not exist: -inf
@@ -457,15 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
           }
         }
-        if (EPI == ACC) {
-          slab_begin(lane);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            slab_put(slab, lane, j,
-                     make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
-        } else {
-          if ((c & 1) == 0) slab_begin(lane);
+        if (EPI == EXP || EPI == GRAD) {
+          const size_t at = (size_t)row * p.g_pitch + x0 + c * 32;
           if (EPI == EXP && p.low != nullptr) {
             // 24 bits of every number: rounded there, the upper 16 rounded from
             // those to a bf16 number, and the byte below as what is left (a
@@ -481,27 +511,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) v[4 * j + i] = __uint_as_float(b[i] + 0x8000u);
             }
-            uint4* at = reinterpret_cast<uint4*>(p.low + (size_t)row * p.low_pitch + x0 + c * 32);
-            at[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            at[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+            store32(p.low + at, lo);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t h[4];
+            for (int k = 0; k < 2; ++k) {
+              uint32_t h[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                h[i] = __byte_perm(__float_as_uint(v[8 * j + 2 * i]),
-                                   __float_as_uint(v[8 * j + 2 * i + 1]), 0x7632);
-              slab_put(slab, lane, (c & 1) * 4 + j, make_uint4(h[0], h[1], h[2], h[3]));
+              for (int i = 0; i < 8; ++i)
+                h[i] = __byte_perm(__float_as_uint(v[16 * k + 2 * i]),
+                                   __float_as_uint(v[16 * k + 2 * i + 1]), 0x7632);
+              store32(p.g + 2 * at + 32 * k, h);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              slab_put(slab, lane, (c & 1) * 4 + j,
-                       make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
-                                  pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                  pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+            for (int k = 0; k < 2; ++k) {
+              uint32_t h[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                h[i] = pack_bf16x2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]);
+              store32(p.g + 2 * at + 32 * k, h);
+            }
           }
+          continue;
+        }
+        if (EPI == ACC) {
+          slab_begin<(G::SLABS > 0 ? G::SLABS : 1)>(lane);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            slab_put(slab, lane, j,
+                     make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+        } else {
+          if ((c & 1) == 0) slab_begin<(G::SLABS > 0 ? G::SLABS : 1)>(lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            slab_put(slab, lane, (c & 1) * 4 + j,
+                     make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
           if ((c & 1) == 0) continue;
         }
         fence_proxy_async_smem();
@@ -513,13 +560,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (p.add) add_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
               else store_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
             }
-          } else if (EPI == OUT) {
+          } else {
             const int x = x0 + (c - 1) * 32, y = p.v0 + row0;
             if (x < p.hidden && y < p.vocab) store_box(&tm_out, slab, x, y);
-          } else {
-            store_box(&tm_out, slab, x0 + (c - 1) * 32, row0);
           }
           bulk_commit();
+        }
+        if (G::SLABS == 2) {
+          slab += other;
+          other = -other;
         }
       }
       if (EPI == LSE || EPI == EXP) {
@@ -831,29 +880,46 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // The kept exponentials of a piece that is the whole vocabulary, with their
 // sums known: 24-bit numbers times the row's scale, rounded to bf16 once, the
-// target's in its place.  A row and 2048 columns per CTA.
+// target's in its place.  A row and 4 * 2048 columns per CTA.
+constexpr int kScaleCols = 8, kScaleSteps = 4;
+
 __global__ void __launch_bounds__(kRowThreads)
     ce_scale_kernel(const __grid_constant__ CeRows a, __nv_bfloat16* g, const uint8_t* low,
                     int pitch, const float* scale, const float* miss) {
   grid_dep_sync();
-  const int row = blockIdx.x, col = (blockIdx.y * kRowThreads + threadIdx.x) * 8;
-  if (row >= __ldcg(a.n) || col >= pitch) return;
-  uint4* at = reinterpret_cast<uint4*>(g + (size_t)row * pitch + col);
-  const uint4 hi = *at;
-  const uint2 lo = __ldcg(reinterpret_cast<const uint2*>(low + (size_t)row * pitch + col));
-  const float s = __ldcg(scale + row);
-  const int t = __ldcg(a.target + row) - col;
-  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
-  float v[8];
+  const int row = blockIdx.x;
+  const int col0 = (blockIdx.y * kScaleSteps * kRowThreads + threadIdx.x) * kScaleCols;
+  if (row >= __ldcg(a.n)) return;
+  uint4* at = reinterpret_cast<uint4*>(g + (size_t)row * pitch);
+  const uint2* lat = reinterpret_cast<const uint2*>(low + (size_t)row * pitch);
+  uint4 hi[kScaleSteps];
+  uint2 lo[kScaleSteps];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t up = (i & 1) ? h[i >> 1] & 0xffff0000u : h[i >> 1] << 16;
-    const int down = (int)(int8_t)((i < 4 ? lo.x : lo.y) >> (8 * (i & 3)));
-    v[i] = __uint_as_float(up + (uint32_t)(down * 256)) * s;
-    if (i == t) v[i] = -__ldcg(a.d + row) * __ldcg(miss + row);
+  for (int k = 0; k < kScaleSteps; ++k) {
+    const int col = col0 + k * kRowThreads * kScaleCols;
+    if (col < pitch) {
+      hi[k] = at[col / kScaleCols];
+      lo[k] = __ldcg(lat + col / kScaleCols);
+    }
   }
-  *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
+  const float s = __ldcg(scale + row), own = -__ldcg(a.d + row) * __ldcg(miss + row);
+  const int target = __ldcg(a.target + row);
+#pragma unroll
+  for (int k = 0; k < kScaleSteps; ++k) {
+    const int col = col0 + k * kRowThreads * kScaleCols;
+    if (col >= pitch) break;
+    const uint32_t h[4] = {hi[k].x, hi[k].y, hi[k].z, hi[k].w};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t up = (i & 1) ? h[i >> 1] & 0xffff0000u : h[i >> 1] << 16;
+      const int down = (int)(int8_t)((i < 4 ? lo[k].x : lo[k].y) >> (8 * (i & 3)));
+      v[i] = __uint_as_float(up + (uint32_t)(down * 256)) * s;
+      if (col + i == target) v[i] = own;
+    }
+    at[col / kScaleCols] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
 }
 
 // ----------------------------------------------------------------- the host
@@ -944,13 +1010,16 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
   static std::atomic<unsigned long long> attr_done{0};
   if (!done_on_device(attr_done)) {
     const cudaError_t e = cudaFuncSetAttribute(
-        ce_gemm_kernel<EPI, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<CG>::SMEM);
+        ce_gemm_kernel<EPI, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)Geo<EPI, CG>::SMEM);
     if (e != cudaSuccess) return e;
     mark_device(attr_done);
   }
   const int grid = std::max(1, std::min(units, sms / CG)) * CG;
-  return launch_pdl_cluster(ce_gemm_kernel<EPI, CG>, dim3(grid), dim3(kThreads), Geo<CG>::SMEM, s,
-                            (unsigned)CG, a, b, out, p);
+  CeGemm q = p;
+  q.by_group = Divisor(kGroup * p.n_tiles);
+  return launch_pdl_cluster(ce_gemm_kernel<EPI, CG>, dim3(grid), dim3(kThreads),
+                            Geo<EPI, CG>::SMEM, s, (unsigned)CG, a, b, out, q);
 }
 
 template <int EPI>
@@ -1067,14 +1136,13 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   // maps: x by rows and by channels, w the same, a piece's exponentials, the
   // fp32 products, dw
   const long long w_pitch = V > 1 ? c.w_stride : H;
-  CUtensorMap x_k, w_k, x_mn, w_mn, g_k, g_mn, g_out, acc_out, dw_out;
+  CUtensorMap x_k, w_k, x_mn, w_mn, g_k, g_mn, acc_out, dw_out;
   int bad = make_map(&x_k, a.xc, false, pad, H, p.pitch, 64, BM) |
             make_map(&w_k, c.w, false, V, H, w_pitch, 64, BN / p.cg);
   if (grad) {
     const void* g = base + p.g;
     bad |= make_map(&w_mn, c.w, false, V, H, w_pitch, 64, 64) |
            make_map(&g_k, g, false, pad, p.piece, p.piece, 64, BM) |
-           make_map(&g_out, g, false, pad, p.piece, p.piece, 64, 32) |
            make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, p.pitch, 32, 32);
     if (c.dw != nullptr)
       bad |= make_map(&x_mn, a.xc, false, pad, H, p.pitch, 64, 64) |
@@ -1094,6 +1162,8 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   gm.target = a.target;
   gm.part_m = f32(p.part_m);
   gm.part_s = f32(p.part_s);
+  gm.g = reinterpret_cast<uint8_t*>(base + p.g);
+  gm.g_pitch = p.piece;
   gm.parts = p.n_tiles * 2;
   gm.err = a.err;
   CeSums sums{};
@@ -1138,11 +1208,8 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     CeGemm ex = gm;
     ex.v0 = v0;
     ex.n_tiles = tiles;
-    if (p.keep) {
-      ex.low = reinterpret_cast<uint8_t*>(base + p.low);
-      ex.low_pitch = p.piece;
-    }
-    e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
+    if (p.keep) ex.low = reinterpret_cast<uint8_t*>(base + p.low);
+    e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
     up.first = v0 / HN;
     up.n_parts = tiles * 2;
     up.hist = f32(p.hist) + (size_t)i * pad;
@@ -1152,7 +1219,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ex.any = up.any;
     ex.repair = up.flag;
     if (e == cudaSuccess)
-      e = launch_gemm<EXP>(p.cg, x_k, w_k, g_out, ex, m_tiles * tiles, sms, s);
+      e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
     CeGemm ac = gm;
     ac.v0 = v0;
     ac.n_tiles = h_tiles;
@@ -1166,7 +1233,8 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
     const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
     if (p.keep) {
-      e = launch_pdl(ce_scale_kernel, dim3(pad, (p.piece / 8 + kRowThreads - 1) / kRowThreads),
+      e = launch_pdl(ce_scale_kernel, dim3(pad, (p.piece + kScaleSteps * kScaleCols * kRowThreads - 1) /
+                                     (kScaleSteps * kScaleCols * kRowThreads)),
                      b256, 0, s, a, reinterpret_cast<__nv_bfloat16*>(base + p.g),
                      reinterpret_cast<const uint8_t*>(base + p.low), p.piece, f32(p.scale),
                      f32(p.miss));
@@ -1177,7 +1245,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
       gr.ref2 = f32(p.lse2);
       gr.d = a.d;
       gr.miss = f32(p.miss);
-      e = launch_gemm<GRAD>(p.cg, x_k, w_k, g_out, gr, m_tiles * tiles, sms, s);
+      e = launch_gemm<GRAD>(p.cg, x_k, w_k, x_k, gr, m_tiles * tiles, sms, s);
     }
     CeGemm ow = gm;
     ow.v0 = v0;
