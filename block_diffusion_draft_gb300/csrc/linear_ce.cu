@@ -48,6 +48,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRefSlack = 80.f;  // binades that a logit may lie above its row's reference
 
+// The factor of a row's own target, -d (1 - p_t), is by far the largest of its
+// column, so what its rounding to bf16 changes is most of dw's error beyond the
+// last rounding.  A column that is one row's target (own = kOwnOne + row) is
+// multiplied by what that rounding took away, which puts it back exactly; the
+// other factors of the column move by no more than their own rounding.
+constexpr unsigned long long kOwnOne = 1ull << 40;
+
 enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
 
 // CG CTAs work on one tile of CG * 128 rows and 256 columns.  Shared memory
@@ -76,8 +83,9 @@ struct CeGemm {
   int g_pitch;
   const float* ref2;   // EXP: the rows' references; GRAD: their lse, log2 units
   const int* target;
-  const float* d;      // GRAD: gradients of the rows' nll
-  const float* miss;   // GRAD: 1 - p_t
+  const float* d;      // GRAD, OUT: gradients of the rows' nll
+  const float* miss;   // GRAD, OUT: 1 - p_t
+  const unsigned long long* own;  // OUT: [vocab] rows with this target (see kOwnOne)
   float* part_m;       // [rows_pad][parts], log2 units: of 128 columns each
   float* part_s;
   int parts;
@@ -389,6 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](const Tile& t) {
       Row r;
       const int row = (t.m * CG + rank) * BM + q * 32 + lane;
+      if (EPI == OUT) {  // (here a row is a column of the vocabulary)
+        r.sc = 1.f;
+        if (p.v0 + row < p.vocab) {
+          const unsigned long long own = __ldcg(p.own + p.v0 + row);
+          if (own >= kOwnOne && own < 2 * kOwnOne) {
+            const int c = (int)(own - kOwnOne);
+            const float g = __ldcg(p.d + c) * __ldcg(p.miss + c);
+            const float rounded = __bfloat162float(__float2bfloat16(g));
+            if (rounded != 0.f) r.sc = g / rounded;
+          }
+        }
+      }
       if (EPI <= GRAD && row < rows) {
         r.tgt = __ldcg(p.target + row);
         if (EPI != LSE) r.ref = __ldcg(p.ref2 + row);
@@ -533,6 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        if (EPI == OUT) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= sc;
+        }
         if (EPI == ACC) {
           slab_begin<(G::SLABS > 0 ? G::SLABS : 1)>(lane);
 #pragma unroll
@@ -610,6 +634,7 @@ struct CeRows {
   float* z_t;          // compact: the target's logit
   float* ref2;         // compact: reference, log2 units
   float* d;            // compact
+  unsigned long long* own;  // [vocab] or null: rows with this target, kOwnOne + row each
   __nv_bfloat16* xc;   // [rows_pad][pitch]
   int pitch;           // hidden rounded up: rows on 128-byte boundaries
 };
@@ -692,6 +717,10 @@ __global__ void __launch_bounds__(kRowThreads) ce_gather_kernel(const __grid_con
     n = __ldcg(a.n);
     if (row < a.rows) c = __ldcg(a.place + row);
   }
+  if (a.own != nullptr)
+    for (long long v = (long long)row * kRowThreads + threadIdx.x; v < a.vocab;
+         v += (long long)gridDim.x * kRowThreads)
+      a.own[v] = 0;
   if (row < 256 && n + row < (n + 255) / 256 * 256) {
     uint4* dst = reinterpret_cast<uint4*>(a.xc + (size_t)(n + row) * a.pitch);
     for (int i = threadIdx.x; i < n8; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
@@ -855,7 +884,11 @@ __global__ void __launch_bounds__(kRowThreads)
   const float d = __ldcg(a.d + c);
   const float f = failed ? nan : d * fast_exp2(__ldcg(a.ref2 + c) - top) / total;
   const float g = d * (others / total);
-  if (threadIdx.x == 0) s.scale[c] = f;
+  if (threadIdx.x == 0) {
+    s.scale[c] = f;
+    // (whole numbers: the sum does not depend on the rows' order)
+    if (a.own != nullptr) atomicAdd(a.own + __ldcg(a.target + c), kOwnOne + (unsigned)c);
+  }
   const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
   for (int i = threadIdx.x; i < n8; i += kRowThreads) {
     float v[8] = {};
@@ -934,7 +967,7 @@ struct Plan {
   int piece, pieces;   // columns of a piece (a multiple of 256)
   int splits;          // of ACC's K
   bool keep;           // dw from the exponentials that dx was made from
-  size_t any, place, target, z_t, ref2, d, miss, lse2, scale, hist, flag, xc, part_m, part_s, g,
+  size_t any, place, target, z_t, ref2, d, miss, lse2, scale, own, hist, flag, xc, part_m, part_s, g,
       low, acc, total;
 };
 
@@ -993,6 +1026,7 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
     p.flag = take(pad / 32 * 4);
     p.g = take(pad * p.piece * 2);
     if (p.keep) p.low = take(pad * p.piece);
+    if (grads == 2) p.own = take((size_t)vocab * 8);
     p.acc = take(pad * p.splits * p.pitch * 4);
   }
   p.total = at;
@@ -1132,6 +1166,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   a.d = f32(p.d);
   a.xc = reinterpret_cast<__nv_bfloat16*>(base + p.xc);
   a.pitch = p.pitch;
+  if (c.dw != nullptr) a.own = reinterpret_cast<unsigned long long*>(base + p.own);
 
   // maps: x by rows and by channels, w the same, a piece's exponentials, the
   // fp32 products, dw
@@ -1251,6 +1286,9 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ow.v0 = v0;
     ow.m_tiles = (tiles * BN + p.cg * BM - 1) / (p.cg * BM);
     ow.n_tiles = h_tiles;
+    ow.d = a.d;
+    ow.miss = f32(p.miss);
+    ow.own = a.own;
     if (e == cudaSuccess)
       e = launch_gemm<OUT>(p.cg, g_mn, x_mn, dw_out, ow, ow.m_tiles * h_tiles, sms, s);
   }

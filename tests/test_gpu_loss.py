@@ -10,7 +10,9 @@ p / (sum of p) are off by
     e = 2 e_z + 4u |z| + 264u  (relative to p, absolute for nll, of which and of
 lse 4u each are rounded off).  A gradient rounds the factor p once to bf16
 (half a step: 2^-8), sums its terms in steps of 16 again, and rounds the result
-to bf16.  Below 2^-126, the smallest normal number of fp32 and bf16, numbers may
+to bf16.  For dw the factor of a column's own row is rounded without loss, at
+the price of a factor of 1 +- 2^-8 for the column's others: 2^-8 once more.
+Below 2^-126, the smallest normal number of fp32 and bf16, numbers may
 be lost: each of a sum's terms (factors p, relative to a reference of at least
 the target's p, times |d w| or |x|) and the result, 2^-126 * (1 + sum of the
 other factors) in all."""
@@ -72,7 +74,7 @@ def check(x, w, t, d, grads=("none", "x", "xw")):
             within(got[2], dx, HALF * 1.01 * dx.abs() + rel * dx_size + lost, f"dx ({grad})")
         assert (got[3] is not None) == (grad == "xw")
         if got[3] is not None:
-            rel = HALF + float(e.max() if N else 0) + (N / 16 + 32) * 2 * U
+            rel = 2 * HALF + float(e.max() if N else 0) + (N / 16 + 32) * 2 * U
             at = x[held > 0].double()
             lost = 2.0 ** -126 * (1 + at.abs().sum(0))
             within(got[3], dw, HALF * 1.01 * dw.abs() + rel * dw_size + lost, "dw")
@@ -222,6 +224,24 @@ def test_gradient_equals_differences():
             # third derivative: below size * (sum of |step| over a row)^2
             spread = float((hi.double() - lo.double()).abs().sum(1).max())
             assert abs(loss(*b) - loss(*a) - slope) <= size * (0.02 + spread ** 2) + 1e-5
+
+
+@pytest.mark.parametrize("N,V", [(96, 4000), (500, 20000)])
+def test_own_factors_of_dw_lose_nothing(N, V):
+    """Rows with targets of their own: what is left of dw's error is its last
+    rounding (relative to the 2-norm 2^-8 / sqrt(3) at most for numbers of one
+    binade's lower end) and the other factors', which are below 2^-4 of the
+    targets' here: together below 2^-8 * (0.58 + 2^-4 * 2)."""
+    x, w, t, d = inputs(N, V, 128, 12, pull=1.0)
+    t = torch.randperm(V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)
+                       )[:N].int()
+    d = d.abs() + 1e-3
+    _, _, _, dw = linear_cross_entropy_grad(x, w, t, d)
+    want = R.linear_cross_entropy(x.double(), w.double(), t, d.double())[3]
+    own = torch.zeros(V, dtype=torch.bool, device="cuda")
+    own[t.long()] = True
+    assert float(want[~own].norm()) < 2 ** -4 * float(want[own].norm())
+    assert float((dw.double() - want).norm() / want.norm()) <= HALF * (0.58 + 2 ** -3)
 
 
 def test_refusals():
