@@ -7,9 +7,9 @@
 //   dx = r * (u - x * r^2 * s / d),   dg = sum over rows and heads of w * x * r.
 // Both sums (x^2 and u * x) go through one reduction.
 //
-// HBM bounds it: every value is read and written once.  A lane holds four
-// channels of either half of a head, so a pair's two channels meet in one
-// lane without an exchange and every access is a contiguous half head.
+// HBM bounds it: every value is read and written once.  A lane holds channels of
+// either half of a head, so a pair's two channels meet in one lane without an
+// exchange and every access is a contiguous half head.
 #include <algorithm>
 
 #include "internal.h"
@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;  // of the backward
 
 // Four channels as they lie in memory, and as two pairs of numbers (the fp32
 // units take two at a time, and instructions are what this kernel has to save
@@ -73,13 +72,16 @@ DF_DEV Item item_at(const QkRopeArgs& a, int kind, int i, int per) {
   return t;
 }
 
+// the position of an item's row, moved into the table
+DF_DEV int position(const QkRopeArgs& a, const Item& t) {
+  const int pos = __ldg(a.positions + (long long)t.b * a.rows + t.r);
+  if (pos >= 0 && pos < a.max_pos) return pos;
+  record_error(a.err, 2 /* DFLASH_DEV_POSITION */);
+  return pos < 0 ? 0 : a.max_pos - 1;
+}
+
 DF_DEV const float2* rope_row(const QkRopeArgs& a, const Item& t) {
-  int pos = __ldg(a.positions + (long long)t.b * a.rows + t.r);
-  if (pos < 0 || pos >= a.max_pos) {
-    record_error(a.err, 2 /* DFLASH_DEV_POSITION */);
-    pos = min(max(pos, 0), a.max_pos - 1);
-  }
-  return a.rope + (long long)pos * (a.d / 2);
+  return a.rope + (long long)position(a, t) * (a.d / 2);
 }
 
 template <typename T>
@@ -100,11 +102,10 @@ DF_DEV void load_turn(const float2* p, float2 (&cs)[2], float2 (&sn)[2]) {
   cs[1] = make_float2(b.x, b.z), sn[1] = make_float2(b.y, b.w);
 }
 
-// Groups of heads that a warp holds at a time: their loads are in flight
-// together.  Training shape (8192 rows of 32 + 8 heads, bf16): forward 34.5,
-// 32.9, 34.5 us with 2, 4, 8 groups; backward 68, 57 us with 2, 4 (one CTA less
-// per SM, but twice the bytes in flight of a warp).
-constexpr int kForward = 4, kBackward = 4;
+// Groups of heads that a warp of the forward holds at a time: their loads are in
+// flight together.  8192 rows of 32 + 8 heads, bf16: 34.5, 32.9, 34.5 us with 2,
+// 4, 8 groups (cold; 28 us, 6.0 TB/s, among other calls).
+constexpr int kForward = 4;
 // Heads of D channels whose tensors allow 4-channel accesses.  The CTAs below
 // `a.split` take the queries, the others the keys.
 template <typename T, int D>
@@ -168,56 +169,169 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   }
 }
 
-// One item's rows as they come from memory.
-template <typename T, int U>
-struct RawItem {
-  Quad<T> xa[U], xb[U], wa[U], wb[U];
+// 16 bytes of a head, as numbers in pairs
+template <typename T>
+struct Wide;
+template <>
+struct Wide<float> {
+  static constexpr int N = 4;
+  uint4 r;
+  DF_DEV float2 pair(int i) const {
+    return i == 0 ? make_float2(__uint_as_float(r.x), __uint_as_float(r.y))
+                  : make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+  }
+  DF_DEV void set(const float2 (&v)[2]) {
+    r = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                   __float_as_uint(v[1].y));
+  }
+};
+template <>
+struct Wide<__nv_bfloat16> {
+  static constexpr int N = 8;
+  uint4 r;
+  DF_DEV float2 pair(int i) const {
+    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  DF_DEV void set(const float2 (&v)[4]) {
+    r = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+  }
 };
 
+DF_DEV void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+
+DF_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DF_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Stages, groups of heads of an item, CTAs per SM: 8192 rows of 32 + 8 heads
+// took 51.0 us with (2, 4, 3), 51.9 with (2, 2, 4), 52.3 with (3, 2, 3), 56 with
+// (3, 1, 5), 80 and more where the CTAs' registers or rings leave too few warps.
+constexpr int kStages = 2, kSteps = 4, kCtasPerSm = 3;
+constexpr int kBackWarps = 4, kBackThreads = kBackWarps * 32;
+
+// One stage of a warp's ring: its lanes' pieces of x and of the gradient of y
+// for kSteps groups of heads, and the row's cosines and sines.
+template <int D>
+struct Stage {
+  uint4 piece[kSteps][4][32];
+  float4 turn[D / 4];
+};
+
+// where the turns of a lane's pairs lie, so that eight lanes' reads at a time
+// fall into different banks (P reads of 16 bytes each)
+template <int P>
+DF_DEV int turn_at(int q) {
+  return q / P * P + (q % P + q / P / (8 / P)) % P;
+}
+
+// The gradient.  A lane holds 16 bytes of either half of a head (8 lanes share
+// a head of 128 bf16 channels: half the exchanges of the forward's split), a
+// warp takes kSteps groups of such heads of one row at a time.  Every lane
+// copies what it will need kStages - 1 items ahead into a ring of its warp's,
+// which needs no barrier: held in registers, those bytes left too few warps.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kBackThreads, kCtasPerSm)
     qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a) {
-  constexpr int L = D / 8, G = 32 / L, U = sizeof(T) == 2 ? kBackward : kBackward / 2;
+  constexpr int N = Wide<T>::N, P = N / 2;  // channels and pairs of numbers of a piece
+  constexpr int L = D / 2 / N, G = 32 / L;  // lanes of a head, heads of a group
+  extern __shared__ uint4 smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, g = lane / L;
+  Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem) + warp * kStages;
   const int kind = (int)blockIdx.x >= a.split;
-  const int ctas = kind ? (int)gridDim.x - a.split : a.split;
-  const int n = a.heads[kind];
+  const int step = (kind ? (int)gridDim.x - a.split : a.split) * kBackWarps;
+  const int n = a.heads[kind], items = a.items[kind];
+  const int first = ((int)blockIdx.x - (kind ? a.split : 0)) * kBackWarps + warp;
+  const long long x_group = G * a.x[kind].head, dy_group = G * a.dy[kind].head;
   grid_dep_sync();
-  float2 ga[2], gb[2], acc[4] = {};
-  load_gain<T>(a, kind, 4 * l, ga);
-  load_gain<T>(a, kind, 4 * l + D / 2, gb);
-  for (int i = ((int)blockIdx.x - (kind ? a.split : 0)) * kWarps + warp; i < a.items[kind];
-       i += ctas * kWarps) {
-    const Item t = item_at(a, kind, i, G * U);
-    const T* src = head_ptr<const T>(a.x[kind], t.b, t.r) + 4 * l;
-    const T* dsrc = head_ptr<const T>(a.dy[kind], t.b, t.r) + 4 * l;
-    RawItem<T, U> v;
+  // copies of an item into a stage; one group each, also for none
+  auto issue = [&](int i, int pos, int stage) {
+    if (i < items) {
+      const Item t = item_at(a, kind, i, G * kSteps);
+      Stage<D>& s = ring[stage];
+      const int h = t.head + g;
+      const T* x = head_ptr<const T>(a.x[kind], t.b, t.r) + h * a.x[kind].head + N * l;
+      const T* dy = head_ptr<const T>(a.dy[kind], t.b, t.r) + h * a.dy[kind].head + N * l;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = min(t.head + u * G + g, n - 1);
-      v.xa[u].load(src + h * a.x[kind].head);
-      v.xb[u].load(src + h * a.x[kind].head + D / 2);
-      v.wa[u].load(dsrc + h * a.dy[kind].head);
-      v.wb[u].load(dsrc + h * a.dy[kind].head + D / 2);
+      for (int u = 0; u < kSteps; ++u) {
+        if (h + u * G < n) {
+          copy16(&s.piece[u][0][lane], x + u * x_group);
+          copy16(&s.piece[u][1][lane], x + u * x_group + D / 2);
+          copy16(&s.piece[u][2][lane], dy + u * dy_group);
+          copy16(&s.piece[u][3][lane], dy + u * dy_group + D / 2);
+        }
+      }
+      if (lane < D / 4)
+        copy16(&s.turn[turn_at<P>(lane)], a.rope + (long long)pos * (D / 2) + 2 * lane);
     }
-    float2 cs[2], sn[2];
-    load_turn(rope_row(a, t) + 4 * l, cs, sn);
-    T* dst = head_ptr<T>(a.out[kind], t.b, t.r) + 4 * l;
+    copy_commit();
+  };
+  auto pos_of = [&](int i) {
+    return i < items ? position(a, item_at(a, kind, i, G * kSteps)) : 0;
+  };
+  int next = 0;  // the position of the item to copy next
+  {
+    int pos[kStages];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float2 wa[2], wb[2], pa[2], pb[2], s2 = make_float2(0.f, 0.f), u2 = s2;
+    for (int k = 0; k < kStages; ++k) pos[k] = pos_of(first + k * step);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 xa = v.xa[u].pair(j), xb = v.xb[u].pair(j);
-        const float2 da = v.wa[u].pair(j), db = v.wb[u].pair(j);
-        wa[j] = fma_f32x2(da, cs[j], mul_f32x2(db, sn[j]));
-        wb[j] = fma_f32x2(db, cs[j], mul_f32x2(neg(da), sn[j]));
-        pa[j] = mul_f32x2(wa[j], xa);
-        pb[j] = mul_f32x2(wb[j], xb);
-        s2 = fma_f32x2(xa, xa, s2);
-        s2 = fma_f32x2(xb, xb, s2);
-        u2 = fma_f32x2(ga[j], pa[j], u2);
-        u2 = fma_f32x2(gb[j], pb[j], u2);
+    for (int k = 0; k < kStages - 1; ++k) issue(first + k * step, pos[k], k);
+    next = pos[kStages - 1];
+  }
+  float2 ga[P], gb[P], acc[2 * P] = {};
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int c = N * l + 2 * j;
+    if (a.gain[kind] != nullptr) {
+      const T* w = static_cast<const T*>(a.gain[kind]) + c;
+      ga[j] = make_float2((float)w[0], (float)w[1]);
+      gb[j] = make_float2((float)w[D / 2], (float)w[D / 2 + 1]);
+    } else {
+      const float* w = a.gain32[kind] + c;
+      ga[j] = make_float2(w[0], w[1]);
+      gb[j] = make_float2(w[D / 2], w[D / 2 + 1]);
+    }
+  }
+  int stage = 0;
+  for (int i = first; i < items; i += step) {
+    copy_wait<kStages - 2>();
+    __syncwarp();  // (the turns are other lanes' copies; the stage before is read)
+    const int ahead = i + (kStages - 1) * step;
+    issue(ahead, next, stage == 0 ? kStages - 1 : stage - 1);
+    next = pos_of(ahead + step);
+    const Stage<D>& s = ring[stage];
+    if (++stage == kStages) stage = 0;
+    const Item t = item_at(a, kind, i, G * kSteps);
+    T* out = head_ptr<T>(a.out[kind], t.b, t.r) + (t.head + g) * a.out[kind].head + N * l;
+    float2 cs[P], sn[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const float4 v = s.turn[turn_at<P>(l * P + j)];
+      cs[j] = make_float2(v.x, v.z), sn[j] = make_float2(v.y, v.w);
+    }
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      Wide<T> xa, xb, da, db, ya, yb;
+      xa.r = s.piece[u][0][lane];
+      xb.r = s.piece[u][1][lane];
+      da.r = s.piece[u][2][lane];
+      db.r = s.piece[u][3][lane];
+      float2 wa[P], wb[P], s2 = make_float2(0.f, 0.f), u2 = s2;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float2 va = xa.pair(j), vb = xb.pair(j), ea = da.pair(j), eb = db.pair(j);
+        wa[j] = fma_f32x2(ea, cs[j], mul_f32x2(eb, sn[j]));
+        wb[j] = fma_f32x2(eb, cs[j], mul_f32x2(neg(ea), sn[j]));
+        s2 = fma_f32x2(va, va, s2);
+        s2 = fma_f32x2(vb, vb, s2);
+        u2 = fma_f32x2(mul_f32x2(ga[j], wa[j]), va, u2);
+        u2 = fma_f32x2(mul_f32x2(gb[j], wb[j]), vb, u2);
       }
       float ss = s2.x + s2.y, ux = u2.x + u2.y;
 #pragma unroll
@@ -225,35 +339,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
         ux += __shfl_xor_sync(0xffffffffu, ux, o);
       }
-      const int h = t.head + u * G + g;
-      if (h >= n) continue;
+      if (t.head + u * G + g >= n) continue;
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
       const float2 r2 = both(r), m2 = both(-r * r * r * ux * (1.f / D));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[j] = fma_f32x2(r2, pa[j], acc[j]);
-        acc[2 + j] = fma_f32x2(r2, pb[j], acc[2 + j]);
-        wa[j] = fma_f32x2(mul_f32x2(r2, ga[j]), wa[j], mul_f32x2(v.xa[u].pair(j), m2));
-        wb[j] = fma_f32x2(mul_f32x2(r2, gb[j]), wb[j], mul_f32x2(v.xb[u].pair(j), m2));
+      for (int j = 0; j < P; ++j) {
+        const float2 va = xa.pair(j), vb = xb.pair(j);
+        const float2 pa = mul_f32x2(r2, wa[j]), pb = mul_f32x2(r2, wb[j]);
+        acc[j] = fma_f32x2(pa, va, acc[j]);
+        acc[P + j] = fma_f32x2(pb, vb, acc[P + j]);
+        wa[j] = fma_f32x2(pa, ga[j], mul_f32x2(va, m2));
+        wb[j] = fma_f32x2(pb, gb[j], mul_f32x2(vb, m2));
       }
-      Quad<T>::store(dst + h * a.out[kind].head, wa[0], wa[1]);
-      Quad<T>::store(dst + h * a.out[kind].head + D / 2, wb[0], wb[1]);
+      ya.set(wa);
+      yb.set(wb);
+      T* at = out + u * (G * a.out[kind].head);
+      *reinterpret_cast<uint4*>(at) = ya.r;
+      *reinterpret_cast<uint4*>(at + D / 2) = yb.r;
     }
   }
   // the CTA's sums: lanes that hold the same channels (L apart), then the
   // warps in order
-  __shared__ float red[kWarps][D];
+  copy_wait<0>();
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);  // [kBackWarps][D]
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 2 * N; ++j) {
     float v = (j & 1) ? acc[j >> 1].y : acc[j >> 1].x;
 #pragma unroll
     for (int o = 16; o >= L; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane < L) red[warp][4 * lane + (j & 3) + (j >> 2) * (D / 2)] = v;
+    if (lane < L) red[warp * D + N * lane + (j % N) + (j / N) * (D / 2)] = v;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kBackThreads) {
     float v = 0.f;
-    for (int w = 0; w < kWarps; ++w) v += red[w][i];
+    for (int w = 0; w < kBackWarps; ++w) v += red[w * D + i];
     a.partial[(size_t)blockIdx.x * D + i] = v;
   }
 }
@@ -341,26 +461,28 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The gains' gradients from the CTAs' sums (the first `split` CTAs: the
-// queries'), always in the same order: 32 channels per CTA, 32 slices of the
+// queries'), always in the same order: 16 channels per CTA, 64 slices of the
 // CTAs each.
-__global__ void __launch_bounds__(1024)
+constexpr int kGainCols = 16, kGainSlices = 64;
+
+__global__ void __launch_bounds__(kGainCols * kGainSlices)
     qk_rope_gain_kernel(const float* partial, int split, int n, int d, float* dq_gain,
                         float* dk_gain) {
-  __shared__ float red[32][33];
+  __shared__ float red[kGainSlices][kGainCols + 1];
+  const int c = threadIdx.x % kGainCols, s = threadIdx.x / kGainCols;
+  const int col = blockIdx.x * kGainCols + c, kind = blockIdx.y;
   grid_dep_sync();
-  const int c = threadIdx.x & 31, s = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  const int kind = blockIdx.y;
   float v = 0.f;
   if (col < d)
 #pragma unroll 8
-    for (int i = (kind ? split : 0) + s; i < (kind ? n : split); i += 32)
+    for (int i = (kind ? split : 0) + s; i < (kind ? n : split); i += kGainSlices)
       v += __ldcg(partial + (size_t)i * d + col);
   red[s][c] = v;
   __syncthreads();
   if (s == 0 && col < d) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += red[i][c];
+    for (int i = 0; i < kGainSlices; ++i) sum += red[i][c];
     float* out = kind ? dk_gain : dq_gain;
     if (out != nullptr) out[col] = sum;
   }
@@ -373,13 +495,13 @@ bool vector_view(const HeadView& v, size_t elem) {
 
 // Items of `per` heads, and the CTAs of either kind: as many as there is work
 // for, in proportion to it where `most` are less.
-int share(QkRopeArgs& a, int per, long long most) {
+int share(QkRopeArgs& a, int per, int warps, long long most) {
   long long need[2];
   a.by_rows = Divisor(a.rows);
   for (int k = 0; k < 2; ++k) {
     a.chunks[k] = Divisor((a.heads[k] + per - 1) / per);
     a.items[k] = a.heads[k] > 0 ? a.batch * a.rows * a.chunks[k].d : 0;
-    need[k] = (a.items[k] + kWarps - 1) / kWarps;
+    need[k] = (a.items[k] + warps - 1) / warps;
   }
   const long long all = need[0] + need[1];
   if (all > most)
@@ -390,11 +512,21 @@ int share(QkRopeArgs& a, int per, long long most) {
 }
 
 template <typename T, int D>
-cudaError_t launch_heads(QkRopeArgs& a, bool bwd, int max_ctas, int* ctas, cudaStream_t s) {
-  const int groups = !bwd ? kForward : sizeof(T) == 2 ? kBackward : kBackward / 2;
-  *ctas = share(a, 32 / (D / 8) * groups, bwd ? max_ctas : 1LL << 30);
-  return bwd ? launch_pdl(qk_rope_bwd_kernel<T, D>, dim3(*ctas), dim3(kThreads), 0, s, a)
-             : launch_pdl(qk_rope_kernel<T, D>, dim3(*ctas), dim3(kThreads), 0, s, a);
+cudaError_t launch_heads(QkRopeArgs& a, bool bwd, int num_sms, int* ctas, cudaStream_t s) {
+  if (!bwd) {
+    *ctas = share(a, 32 / (D / 8) * kForward, kWarps, 1LL << 30);
+    return launch_pdl(qk_rope_kernel<T, D>, dim3(*ctas), dim3(kThreads), 0, s, a);
+  }
+  constexpr size_t bytes = sizeof(Stage<D>) * kStages * kBackWarps;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!done_on_device(attr_done)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        qk_rope_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    mark_device(attr_done);
+  }
+  *ctas = share(a, 32 / (D / 2 / Wide<T>::N) * kSteps, kBackWarps, qk_rope_max_ctas(num_sms));
+  return launch_pdl(qk_rope_bwd_kernel<T, D>, dim3(*ctas), dim3(kBackThreads), bytes, s, a);
 }
 
 }  // namespace
@@ -416,18 +548,19 @@ int launch_qk_rope(const QkRopeArgs& args, int bf16, bool bwd, int num_sms, floa
   }
   cudaError_t e;
   if (bf16) {
-    e = launch_heads<__nv_bfloat16, 128>(a, bwd, max_ctas, &ctas, s);
+    e = launch_heads<__nv_bfloat16, 128>(a, bwd, num_sms, &ctas, s);
   } else if (wide && a.d == 64) {
-    e = launch_heads<float, 64>(a, bwd, max_ctas, &ctas, s);
+    e = launch_heads<float, 64>(a, bwd, num_sms, &ctas, s);
   } else if (wide && a.d == 128) {
-    e = launch_heads<float, 128>(a, bwd, max_ctas, &ctas, s);
+    e = launch_heads<float, 128>(a, bwd, num_sms, &ctas, s);
   } else {
-    ctas = share(a, 1, max_ctas);
+    ctas = share(a, 1, kWarps, max_ctas);
     e = bwd ? launch_pdl(qk_rope_any_kernel<true>, dim3(ctas), dim3(kThreads), 0, s, a)
             : launch_pdl(qk_rope_any_kernel<false>, dim3(ctas), dim3(kThreads), 0, s, a);
   }
   if (e != cudaSuccess || !bwd) return (int)e;
-  return (int)launch_pdl(qk_rope_gain_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s,
+  return (int)launch_pdl(qk_rope_gain_kernel, dim3((a.d + kGainCols - 1) / kGainCols, 2),
+                         dim3(kGainCols * kGainSlices), 0, s,
                          a.partial, a.split, ctas, a.d, dq_gain, dk_gain);
 }
 
