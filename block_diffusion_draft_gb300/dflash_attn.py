@@ -453,42 +453,40 @@ class DFlashAttention:
             n = c_size_t(0)
             check(lib().dflash_qk_norm_rope_workspace(self.handle, byref(n)))
             self._rope_ws = n.value
-        # one allocation: the gains' gradients, then the workspace
-        d = self.head_dim
-        pad = (2 * d + 63) // 64 * 64
-        buf = torch.empty(pad + self._rope_ws // 4, device=self.device, dtype=torch.float32)
-        p = buf.data_ptr()
+        dev = self.device
+        d_gain = [None if t is None else torch.empty(self.head_dim, device=dev,
+                                                     dtype=torch.float32) for t in (q, k)]
+        ws = torch.empty(self._rope_ws, device=dev, dtype=torch.uint8)
         _call(self.device, lib().dflash_qk_norm_rope_backward, self.handle, B, R, at[0], at[1],
               self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
-              at[2], at[3], at[4], at[5], None if q is None else p,
-              None if k is None else p + 4 * d, p + 4 * pad, self._rope_ws)
-        return (dq_out, dk_out, None if q is None else buf[:d],
-                None if k is None else buf[d:2 * d])
+              at[2], at[3], at[4], at[5], None if q is None else d_gain[0].data_ptr(),
+              None if k is None else d_gain[1].data_ptr(), ws.data_ptr(), self._rope_ws)
+        return dq_out, dk_out, d_gain[0], d_gain[1]
 
     def _views(self, rows: Tuple[int, int], *tensors: Optional[torch.Tensor]):
         """dflash_heads of tensors of queries and keys in turn: an array of
         (address, batch, row and head stride) that has to outlive the call, and
         the addresses of its parts (None for None)."""
-        flat, dt, d, index = [], self.dtype, self.head_dim, self.device.index
-        shapes = ((*rows, self.n_heads, d), (*rows, self.n_kv_heads, d))
-        for i, t in enumerate(tensors):
+        flat, at, dt, d, dev = [], [], self.dtype, self.head_dim, self.device
+        shape, other = (*rows, self.n_heads, d), (*rows, self.n_kv_heads, d)
+        for t in tensors:
             if t is None:
                 flat += (0, 0, 0, 0)
-                continue
-            on = t.get_device()  # -1: not on a CUDA device
-            if t.shape != shapes[i & 1] or t.dtype is not dt or (
-                    on != index and (index is not None or on < 0)):
-                name = "qk"[i & 1]
-                raise ValueError(f"{name} and what belongs to it must be {list(shapes[i & 1])}, "
-                                 f"{dt} on {self.device}, got {list(t.shape)}, {t.dtype} on "
-                                 f"{t.device}")
-            s = t.stride()
-            if s[3] != 1 and t.numel():
-                raise ValueError("a head's channels must be dense")
-            flat += (t.data_ptr() or 16, s[0], s[1], s[2])  # (no data: no rows)
+                at.append(None)
+            else:
+                s = t.stride()
+                if t.shape != shape or t.dtype is not dt or not _on(t, dev):
+                    raise ValueError(f"queries must be {[*rows, self.n_heads, d]} and keys "
+                                     f"{[*rows, self.n_kv_heads, d]}, {dt} on {dev}, got "
+                                     f"{list(t.shape)}, {t.dtype} on {t.device}")
+                if s[3] != 1 and t.numel():
+                    raise ValueError("a head's channels must be dense")
+                at.append(8 * len(flat))
+                flat += (t.data_ptr() or 16, s[0], s[1], s[2])  # (no data: no rows)
+            shape, other = other, shape
         v = array("q", flat)
         base = v.buffer_info()[0]
-        return v, [None if t is None else base + 32 * i for i, t in enumerate(tensors)]
+        return v, [x if x is None else base + x for x in at]
 
     def _gain(self, name: str, t: Optional[torch.Tensor]) -> Optional[int]:
         if t is None:
@@ -802,7 +800,8 @@ def _linear_ce(x, w, targets, d_nll, grads: int):
         _require("d_nll", d_nll, torch.float32, dev, (N,))
     size = _linear_ce_workspace(N, V, H, grads)
     space = torch.empty(size, device=dev, dtype=torch.uint8)
-    nll, lse = torch.empty((2, N), device=dev, dtype=torch.float32).unbind(0)
+    nll = torch.empty(N, device=dev, dtype=torch.float32)
+    lse = torch.empty(N, device=dev, dtype=torch.float32)
     if not grads:
         _call(dev, lib().dflash_linear_ce, N, V, H, x.data_ptr(), xs[0], w.data_ptr(), ws[0],
               targets.data_ptr(), nll.data_ptr(), lse.data_ptr(), space.data_ptr(), size)
@@ -867,15 +866,16 @@ def _grad_norm(grads, max_norm, out) -> torch.Tensor:
         outs = array("Q", [o.data_ptr() for o in out])
     counts, types = array("q", [g.numel() for g in grads]), array("i", types)
     size = _grad_norm_workspace(n)
-    # one allocation: the norm, then the workspace
-    buf = torch.empty(64 + size // 4, device=dev, dtype=torch.float32)
-    p = buf.data_ptr()
+    ws = torch.empty(size, device=dev, dtype=torch.uint8)
+    norm = torch.empty((), device=dev, dtype=torch.float32)
     lists = [a if a is None else a.buffer_info()[0] for a in (ptrs, outs, counts, types)]
     if max_norm is None:
-        _call(dev, lib().dflash_grad_norm, n, lists[0], lists[2], lists[3], p, p + 256, size)
+        _call(dev, lib().dflash_grad_norm, n, lists[0], lists[2], lists[3], norm.data_ptr(),
+              ws.data_ptr(), size)
     else:
-        _call(dev, lib().dflash_clip_grad_norm, n, *lists, max_norm, p, p + 256, size)
-    return buf[0]
+        _call(dev, lib().dflash_clip_grad_norm, n, *lists, max_norm, norm.data_ptr(),
+              ws.data_ptr(), size)
+    return norm
 
 
 def _dense(t: torch.Tensor) -> bool:
