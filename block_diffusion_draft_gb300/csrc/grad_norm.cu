@@ -4,10 +4,11 @@
 //
 // HBM bounds it: the norm reads every gradient once; clipping, which needs the
 // norm first, reads them again and writes them.  The tensors are cut into
-// chunks of 32 KB (2048 16-byte pieces) in one line, of which every CTA takes
-// an equal run; the second pass goes through its run backwards, so that it
-// begins with what the first one left in L2.  A run's chunks follow one
-// another, so the tensor of a chunk is searched once and then only advanced.
+// chunks of 32 KB (2048 16-byte pieces) in one line, which the CTAs take in turn,
+// so that all of them are near one another in memory (a run of its own for each
+// CTA was 5% slower); the second pass goes backwards and so begins with what the
+// first one left in L2.  One decoder layer's gradients in bf16 (386 MB): the
+// norm 59 us (6.5 TB/s), clipped into other buffers 192 us.
 //
 // A thread adds the squares of up to 64 values in fp32 (relative error below
 // 64 * 2^-24) and everything above that in fp64, in an order that depends on
@@ -63,6 +64,16 @@ __host__ __device__ inline Cut cut(const void* p, long long n, bool wide) {
   c.chunks = n == 0 ? 0 : (int)((c.vecs + kChunk - 1) / kChunk);
   if (n > 0 && c.chunks == 0) c.chunks = 1;
   return c;
+}
+
+// 16 bytes that this CTA reads once
+DF_DEV uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
 }
 
 DF_DEV float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -137,12 +148,10 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ double sm[kThreads / 32];
   grid_dep_sync();
   const int total = t.first[t.tensors];
-  const int c0 = (int)((long long)total * blockIdx.x / gridDim.x);
-  const int c1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
   double acc = 0.;
-  int k = c0 < c1 ? find_tensor(t, c0) : 0;
-  for (int c = c0; c < c1; ++c) {
-    while (c >= t.first[k + 1]) ++k;
+  int k = 0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    if (c >= t.first[k + 1]) k = find_tensor(t, c);
     const void* g = t.g[k];
     const bool wide = (t.n[k] & kWide) != 0;
     const long long n = t.n[k] & ~kWide;
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const long long at = v0 + i * kThreads;
-      v[i] = at < cu.vecs ? __ldg(v4 + at) : make_uint4(0, 0, 0, 0);
+      v[i] = at < cu.vecs ? load_once(v4 + at) : make_uint4(0, 0, 0, 0);
     }
     float s = 0.f;
     if (v0 == threadIdx.x) {  // the first chunk takes the edges, too
@@ -212,7 +221,23 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
     grad_scale_kernel(const __grid_constant__ GradTable<N> t, const double* partial, int n_partial,
                       double max_norm, float* norm, int in_place) {
+  const int total = t.first[t.tensors];
+  int c = total - 1 - (int)blockIdx.x;  // (the grid has at most a CTA per chunk)
+  int k = find_tensor(t, c);
   grid_dep_sync();
+  // the first chunk is on its way while the norm is added up
+  uint4 v[kVecs];
+  auto load = [&] {
+    const bool wide = (t.n[k] & kWide) != 0;
+    const Cut cu = cut(t.g[k], t.n[k] & ~kWide, wide);
+    const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const char*>(t.g[k]) +
+                                                     cu.head * (wide ? 4 : 2));
+    const long long v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (v0 + i * kThreads < cu.vecs) v[i] = load_once(v4 + v0 + i * kThreads);
+  };
+  load();
   const double nm = sqrt(total_square(partial, n_partial));
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nm;
   // (false where the norm is NaN: the gradients stay as they are, as with an
@@ -224,28 +249,16 @@ __global__ void __launch_bounds__(kThreads)
   const bool tiny = f < 1e-30;
   const float fa = (float)(tiny ? f * 18446744073709551616. : f);
   const float fb = tiny ? 5.421010862427522e-20f : 1.f;
-  const int total = t.first[t.tensors];
-  const int c0 = (int)((long long)total * blockIdx.x / gridDim.x);
-  const int c1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
-  int k = c0 < c1 ? find_tensor(t, c1 - 1) : 0;
-  for (int c = c1 - 1; c >= c0; --c) {
-    while (c < t.first[k]) --k;
+  while (true) {
     const void* g = t.g[k];
     void* out = t.out[k];
     const bool wide = (t.n[k] & kWide) != 0;
     const long long n = t.n[k] & ~kWide;
     const Cut cu = cut(g, n, wide);
     const int es = wide ? 4 : 2, per = 16 / es;
-    const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const char*>(g) + cu.head * es);
     char* o = static_cast<char*>(out) + cu.head * es;
     const bool whole = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
     const long long v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
-    uint4 v[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const long long at = v0 + i * kThreads;
-      if (at < cu.vecs) v[i] = v4[at];
-    }
     if (v0 == threadIdx.x && threadIdx.x < 16) {
       const long long at = edge_index(cu, n, per, threadIdx.x);
       if (at >= 0) store_one(out, at, wide, load_one(g, at, wide) * fa * fb);
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t w[4] = {scale_word(v[i].x, wide, fa, fb), scale_word(v[i].y, wide, fa, fb),
                              scale_word(v[i].z, wide, fa, fb), scale_word(v[i].w, wide, fa, fb)};
       if (whole) {
-        reinterpret_cast<uint4*>(o)[at] = make_uint4(w[0], w[1], w[2], w[3]);
+        __stcs(reinterpret_cast<uint4*>(o) + at, make_uint4(w[0], w[1], w[2], w[3]));
       } else if (wide) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(o)[at * 4 + j] = w[j];
@@ -269,6 +282,10 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
+    c -= (int)gridDim.x;
+    if (c < 0) break;
+    if (c < t.first[k]) k = find_tensor(t, c);
+    load();
   }
 }
 
