@@ -142,8 +142,63 @@ DF_DEV double block_sum(double v, double* sm) {
   return s;
 }
 
+// A chunk of a tensor: what a thread of it reads and writes.
+struct Chunk {
+  const void* g;
+  void* out;
+  long long n, v0;  // elements; this thread's first piece
+  Cut cu;
+  bool wide;
+};
+
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+DF_DEV Chunk chunk_at(const GradTable<N>& t, int k, int c) {
+  Chunk x;
+  x.g = t.g[k];
+  x.out = t.out[k];
+  x.wide = (t.n[k] & kWide) != 0;
+  x.n = t.n[k] & ~kWide;
+  x.cu = cut(x.g, x.n, x.wide);
+  x.v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
+  return x;
+}
+
+DF_DEV void load_chunk(const Chunk& x, uint4 (&v)[kVecs]) {
+  const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const char*>(x.g) +
+                                                   x.cu.head * (x.wide ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const long long at = x.v0 + i * kThreads;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (at < x.cu.vecs) v[i] = load_once(v4 + at);
+  }
+}
+
+// The squares of a thread's part of a chunk.
+DF_DEV double chunk_square(const Chunk& x, const uint4 (&v)[kVecs]) {
+  double acc = 0.;
+  if (x.v0 == threadIdx.x && threadIdx.x < 16) {  // the first chunk takes the edges, too
+    const long long at = edge_index(x.cu, x.n, x.wide ? 4 : 8, threadIdx.x);
+    if (at >= 0) {
+      const double e = load_one(x.g, at, x.wide);
+      acc = e * e;
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) s += square4(v[i], x.wide);
+  if (s >= (float)kSmall && s < (float)kBig) return acc + s;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
+  if (any & 0x7fff7fffu)
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) acc += square4_f64(v[i], x.wide);
+  return acc;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     grad_square_kernel(const __grid_constant__ GradTable<N> t, double* partial) {
   __shared__ double sm[kThreads / 32];
   grid_dep_sync();
@@ -152,39 +207,10 @@ __global__ void __launch_bounds__(kThreads)
   int k = 0;
   for (int c = blockIdx.x; c < total; c += gridDim.x) {
     if (c >= t.first[k + 1]) k = find_tensor(t, c);
-    const void* g = t.g[k];
-    const bool wide = (t.n[k] & kWide) != 0;
-    const long long n = t.n[k] & ~kWide;
-    const Cut cu = cut(g, n, wide);
-    const int es = wide ? 4 : 2, per = 16 / es;
-    const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const char*>(g) + cu.head * es);
-    const long long v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
+    const Chunk x = chunk_at(t, k, c);
     uint4 v[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const long long at = v0 + i * kThreads;
-      v[i] = at < cu.vecs ? load_once(v4 + at) : make_uint4(0, 0, 0, 0);
-    }
-    float s = 0.f;
-    if (v0 == threadIdx.x) {  // the first chunk takes the edges, too
-      const long long at = edge_index(cu, n, per, threadIdx.x);
-      if (at >= 0 && threadIdx.x < 16) {
-        const double x = load_one(g, at, wide);
-        acc += x * x;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) s += square4(v[i], wide);
-    if (s >= (float)kSmall && s < (float)kBig) {
-      acc += s;
-    } else {
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
-      if (any & 0x7fff7fffu)
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) acc += square4_f64(v[i], wide);
-    }
+    load_chunk(x, v);
+    acc += chunk_square(x, v);
   }
   const double s = block_sum(acc, sm);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
@@ -217,8 +243,57 @@ DF_DEV void store_one(void* p, long long i, bool wide, float v) {
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16(v);
 }
 
+// What a norm does to the gradients: a factor in two steps, the second one for
+// factors below the normal fp32 numbers.
+struct Factor {
+  bool clip;
+  float a, b;
+};
+
+DF_DEV Factor factor_of(double norm, double max_norm) {
+  // (false where the norm is NaN: the gradients stay as they are, as with an
+  // infinite one)
+  Factor f;
+  f.clip = norm > max_norm && norm <= 1.7976931348623157e308;
+  const double x = f.clip ? max_norm / norm : 1.;
+  const bool tiny = x < 1e-30;
+  f.a = (float)(tiny ? x * 18446744073709551616. : x);
+  f.b = tiny ? 5.421010862427522e-20f : 1.f;
+  return f;
+}
+
+DF_DEV void scale_chunk(const Chunk& x, const uint4 (&v)[kVecs], Factor f) {
+  char* o = static_cast<char*>(x.out) + x.cu.head * (x.wide ? 4 : 2);
+  const bool whole = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+  if (x.v0 == threadIdx.x && threadIdx.x < 16) {
+    const long long at = edge_index(x.cu, x.n, x.wide ? 4 : 8, threadIdx.x);
+    if (at >= 0) store_one(x.out, at, x.wide, load_one(x.g, at, x.wide) * f.a * f.b);
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const long long at = x.v0 + i * kThreads;
+    if (at >= x.cu.vecs) continue;
+    const uint32_t w[4] = {scale_word(v[i].x, x.wide, f.a, f.b),
+                           scale_word(v[i].y, x.wide, f.a, f.b),
+                           scale_word(v[i].z, x.wide, f.a, f.b),
+                           scale_word(v[i].w, x.wide, f.a, f.b)};
+    if (whole) {
+      __stcs(reinterpret_cast<uint4*>(o) + at, make_uint4(w[0], w[1], w[2], w[3]));
+    } else if (x.wide) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(o)[at * 4 + j] = w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        reinterpret_cast<uint16_t*>(o)[at * 8 + 2 * j] = (uint16_t)w[j];
+        reinterpret_cast<uint16_t*>(o)[at * 8 + 2 * j + 1] = (uint16_t)(w[j] >> 16);
+      }
+    }
+  }
+}
+
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     grad_scale_kernel(const __grid_constant__ GradTable<N> t, const double* partial, int n_partial,
                       double max_norm, float* norm, int in_place) {
   const int total = t.first[t.tensors];
@@ -227,65 +302,61 @@ __global__ void __launch_bounds__(kThreads)
   grid_dep_sync();
   // the first chunk is on its way while the norm is added up
   uint4 v[kVecs];
-  auto load = [&] {
-    const bool wide = (t.n[k] & kWide) != 0;
-    const Cut cu = cut(t.g[k], t.n[k] & ~kWide, wide);
-    const uint4* v4 = reinterpret_cast<const uint4*>(static_cast<const char*>(t.g[k]) +
-                                                     cu.head * (wide ? 4 : 2));
-    const long long v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (v0 + i * kThreads < cu.vecs) v[i] = load_once(v4 + v0 + i * kThreads);
-  };
-  load();
+  Chunk x = chunk_at(t, k, c);
+  load_chunk(x, v);
   const double nm = sqrt(total_square(partial, n_partial));
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nm;
-  // (false where the norm is NaN: the gradients stay as they are, as with an
-  // infinite one)
-  const bool clip = nm > max_norm && nm <= 1.7976931348623157e308;
-  if (!clip && in_place) return;
-  // a factor below the normal fp32 numbers goes in two steps
-  const double f = clip ? max_norm / nm : 1.;
-  const bool tiny = f < 1e-30;
-  const float fa = (float)(tiny ? f * 18446744073709551616. : f);
-  const float fb = tiny ? 5.421010862427522e-20f : 1.f;
+  const Factor f = factor_of(nm, max_norm);
+  if (!f.clip && in_place) return;
   while (true) {
-    const void* g = t.g[k];
-    void* out = t.out[k];
-    const bool wide = (t.n[k] & kWide) != 0;
-    const long long n = t.n[k] & ~kWide;
-    const Cut cu = cut(g, n, wide);
-    const int es = wide ? 4 : 2, per = 16 / es;
-    char* o = static_cast<char*>(out) + cu.head * es;
-    const bool whole = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
-    const long long v0 = (long long)(c - t.first[k]) * kChunk + threadIdx.x;
-    if (v0 == threadIdx.x && threadIdx.x < 16) {
-      const long long at = edge_index(cu, n, per, threadIdx.x);
-      if (at >= 0) store_one(out, at, wide, load_one(g, at, wide) * fa * fb);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const long long at = v0 + i * kThreads;
-      if (at >= cu.vecs) continue;
-      const uint32_t w[4] = {scale_word(v[i].x, wide, fa, fb), scale_word(v[i].y, wide, fa, fb),
-                             scale_word(v[i].z, wide, fa, fb), scale_word(v[i].w, wide, fa, fb)};
-      if (whole) {
-        __stcs(reinterpret_cast<uint4*>(o) + at, make_uint4(w[0], w[1], w[2], w[3]));
-      } else if (wide) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(o)[at * 4 + j] = w[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          reinterpret_cast<uint16_t*>(o)[at * 8 + 2 * j] = (uint16_t)w[j];
-          reinterpret_cast<uint16_t*>(o)[at * 8 + 2 * j + 1] = (uint16_t)(w[j] >> 16);
-        }
-      }
-    }
+    scale_chunk(x, v, f);
     c -= (int)gridDim.x;
     if (c < 0) break;
     if (c < t.first[k]) k = find_tensor(t, c);
-    load();
+    x = chunk_at(t, k, c);
+    load_chunk(x, v);
+  }
+}
+
+// Few chunks: one launch of one cluster does all of it, the CTAs' sums going
+// from one's shared memory to the others'.  mode 0: the norm, 1: clip in place,
+// 2: into other tensors.
+constexpr int kClusterCtas = 8, kClusterChunks = 32;
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    grad_cluster_kernel(const __grid_constant__ GradTable<N> t, int mode, double max_norm,
+                        float* norm) {
+  __shared__ double sm[kThreads / 32];
+  __shared__ double sums[kClusterCtas];
+  const int rank = (int)cluster_ctarank(), total = t.first[t.tensors];
+  grid_dep_sync();
+  double acc = 0.;
+  uint4 v[kVecs];
+  Chunk x{};
+  for (int c = rank; c < total; c += kClusterCtas) {
+    x = chunk_at(t, find_tensor(t, c), c);
+    load_chunk(x, v);
+    acc += chunk_square(x, v);
+  }
+  const double s = block_sum(acc, sm);
+  if (threadIdx.x < kClusterCtas)
+    st_cluster_u64(cluster_map(smem_u32(&sums[rank]), threadIdx.x),
+                   (unsigned long long)__double_as_longlong(s));
+  cluster_sync();  // (nothing goes to another CTA's memory after it)
+  double square = 0.;
+  for (int i = 0; i < kClusterCtas; ++i) square += sums[i];
+  const double nm = sqrt(square);
+  if (rank == 0 && threadIdx.x == 0) *norm = (float)nm;
+  if (mode == 0) return;
+  const Factor f = factor_of(nm, max_norm);
+  if (!f.clip && mode == 1) return;
+  for (int c = rank; c < total; c += kClusterCtas) {
+    if (total > kClusterCtas) {  // (otherwise it is the one that was read)
+      x = chunk_at(t, find_tensor(t, c), c);
+      load_chunk(x, v);
+    }
+    scale_chunk(x, v, f);
   }
 }
 
@@ -400,6 +471,15 @@ int run_norm(int n, const void* const* g, void* const* out, const int64_t* count
   GradTable<N> t;
   int n_partial = 0;
   cudaError_t e = cudaSuccess;
+  if (n > 0 && fill_table(t, 0, n, g, out, counts, dtypes) == n && t.tensors > 0 &&
+      t.first[t.tensors] <= kClusterChunks) {
+    e = launch_pdl_cluster(grad_cluster_kernel<N>, dim3(kClusterCtas), dim3(kThreads), 0, s,
+                           (unsigned)kClusterCtas, t, !clip ? 0 : out == nullptr ? 1 : 2,
+                           max_norm, norm);
+    return e == cudaSuccess ? DFLASH_OK
+                            : api_fail(DFLASH_ERR_CUDA, "gradient norm launch: %s",
+                                       cudaGetErrorString(e));
+  }
   const int max_partial = (int)(ws_bytes / sizeof(double));
   for (int i = 0; i < n && e == cudaSuccess;) {
     i = fill_table(t, i, n, g, out, counts, dtypes);

@@ -22,7 +22,7 @@
 // so dx needs the logits once (EXP, ACC: 4 N V H operations) and is divided by
 // the row's sum at the end.  The reference is the target's logit; a row in
 // whose piece a logit lies more than 2^80 above it is done again with its
-// largest one (update and repair kernels, which end at once otherwise).
+// largest one (a second launch of EXP, which ends at once otherwise).
 //
 // The target's column is left out of every sum of exponentials and added
 // where the results are written: 1 - p_t is then a quotient of sums without
@@ -81,7 +81,9 @@ struct CeGemm {
   uint8_t* g;          // EXP, GRAD: [rows_pad][g_pitch] bf16
   uint8_t* low;        // EXP: null, or [rows_pad][g_pitch] the exponentials' next 8 bits
   int g_pitch;
-  const float* ref2;   // EXP: the rows' references; GRAD: their lse, log2 units
+  const float* ref2;   // EXP: the rows' references before the piece; GRAD: their lse, log2 units
+  float* raised;       // EXP: [pieces left][rows_pad] references after the piece and later ones
+  int pieces_left;     // this one included
   const int* target;
   const float* d;      // GRAD, OUT: gradients of the rows' nll
   const float* miss;   // GRAD, OUT: 1 - p_t
@@ -89,9 +91,11 @@ struct CeGemm {
   float* part_m;       // [rows_pad][parts], log2 units: of 128 columns each
   float* part_s;
   int parts;
-  const int* any;      // EXP: null, or whether a repair has anything to do
-  const int* repair;   // and the flags of 32-row groups: only their tiles
+  int* any;            // EXP: whether a reference was raised
+  int repair;          // EXP: only the row tiles with a raised reference, with that
   int add;             // ACC: the buffer holds earlier pieces
+  float* acc;          // repair: [splits][rows_pad][acc_pitch] earlier pieces' products, or null
+  int acc_pitch, acc_slices;
   int* err;
 };
 
@@ -234,14 +238,32 @@ DF_DEV Tile tile_at(const CeGemm& p, int m_tiles, int n_kb, int u) {
   return t;
 }
 
-// Whether a repair has to compute this row tile again: one of its 32-row
-// groups is flagged.
+// Whether a repair has to compute this row tile again: one of its rows has
+// another reference than before.  For a whole warp or for one thread.
 template <int CG>
-DF_DEV bool wanted(const CeGemm& p, const Tile& t) {
-  if (p.repair == nullptr) return true;
+DF_DEV bool raised(const CeGemm& p, const Tile& t, int first, int step) {
   bool any = false;
-  for (int i = 0; i < CG * BM / 32; ++i) any |= __ldcg(p.repair + t.m * (CG * BM / 32) + i) != 0;
+  for (int i = first; i < CG * BM; i += step) {
+    const int row = t.m * CG * BM + i;
+    any |= row < __ldcg(p.n_rows) && __ldcg(p.raised + row) != __ldcg(p.ref2 + row);
+  }
   return any;
+}
+
+// A logit far above the row's reference: it becomes the reference of this
+// piece's repair and of all pieces behind it (the largest such one, whatever the
+// order).
+DF_DEV void raise(const CeGemm& p, int row, float top) {
+  for (int i = 0; i < p.pieces_left; ++i) {
+    int* at = reinterpret_cast<int*>(p.raised + (size_t)i * p.rows_pad + row);
+    int old = *reinterpret_cast<volatile int*>(at);
+    while (__int_as_float(old) < top) {
+      const int seen = atomicCAS(at, old, __float_as_int(top));
+      if (seen == old) break;
+      old = seen;
+    }
+  }
+  *p.any = 1;  // (every writer stores the same)
 }
 
 // What a warp stores by bulk copies goes through slabs of 4 KB of its own, in
@@ -308,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CG == 2) cluster_sync();
   const uint32_t tmem = *tmem_slot;
   grid_dep_sync();
-  const int rows = p.any != nullptr && __ldcg(p.any) == 0 ? 0 : __ldcg(p.n_rows);
+  const bool repair = EPI == EXP && p.repair != 0;
+  const int rows = repair && __ldcg(p.any) == 0 ? 0 : __ldcg(p.n_rows);
   const int m_tiles = EPI == OUT ? p.m_tiles : (rows + CG * BM - 1) / (CG * BM);
   const int n_kb = EPI == OUT ? (rows + BK - 1) / BK : p.n_kb;
   const int units = m_tiles * p.n_tiles * p.splits;
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       for (int u = first; alive && u < units; u += stride) {
         const Tile t = tile_at(p, m_tiles, n_kb, u);
-        if (!wanted<CG>(p, t)) continue;
+        if (repair && !raised<CG>(p, t, 0, 1)) continue;
         const int m0 = (t.m * CG + rank) * BM, n0 = t.n * BN + rank * (BN / CG);
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, p.err)) {
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       for (int u = first; alive && u < units; u += stride) {
         const Tile t = tile_at(p, m_tiles, n_kb, u);
-        if (t.k0 >= t.k1 || !wanted<CG>(p, t)) continue;
+        if (t.k0 >= t.k1 || (repair && !raised<CG>(p, t, 0, 1))) continue;
         const uint32_t buf = tc & 1, use = tc >> 1;
         ++tc;
         if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.err)) break;
@@ -411,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (EPI <= GRAD && row < rows) {
         r.tgt = __ldcg(p.target + row);
-        if (EPI != LSE) r.ref = __ldcg(p.ref2 + row);
+        if (EPI != LSE) r.ref = __ldcg((repair ? p.raised : p.ref2) + row);
         if (EPI == GRAD) {
           r.sc = __ldcg(p.d + row);
           r.miss = __ldcg(p.miss + row);
@@ -419,6 +442,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return r;
     };
+    if (repair && rows > 0 && p.acc != nullptr) {
+      // what the rows hold of earlier pieces follows their references
+      const int warps = gridDim.x * kEpiWarps;
+      for (int r = blockIdx.x * kEpiWarps + warp - 2; r < rows; r += warps) {
+        const float was = __ldcg(p.ref2 + r), now = __ldcg(p.raised + r);
+        if (was == now) continue;
+        const float f = fast_exp2(was - now);
+        for (int s = 0; s < p.acc_slices; ++s) {
+          float* v = p.acc + ((size_t)s * p.rows_pad + r) * p.acc_pitch;
+          for (int i = lane; i < p.acc_pitch; i += 32) v[i] *= f;
+        }
+      }
+    }
     uint32_t tc = 0;
     Tile next{};
     Row next_row;
@@ -433,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = tile_at(p, m_tiles, n_kb, u + stride);
         next_row = row_of(next);
       }
-      if (!wanted<CG>(p, t)) continue;
+      if (repair && !__any_sync(0xffffffffu, raised<CG>(p, t, lane, 32))) continue;
       const bool any = t.k0 < t.k1;  // otherwise the tile is zero
       const int row0 = (t.m * CG + rank) * BM + q * 32, row = row0 + lane;
       const bool live = EPI == ACC || EPI == OUT || row < rows;
@@ -598,8 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (EPI == LSE || EPI == EXP) {
         if (live) {
           const size_t at = (size_t)row * p.parts + (p.v0 + x0) / HN;
-          p.part_m[at] = mx;
+          if (EPI == LSE) p.part_m[at] = mx;
           p.part_s[at] = sum;
+          // (a repair's references are its largest logits)
+          if (EPI == EXP && !repair && mx - ref > kRefSlack) raise(p, row, mx);
         }
       }
     }
@@ -632,7 +670,8 @@ struct CeRows {
   int* place;          // [rows]: compact row or -1
   int* target;         // compact
   float* z_t;          // compact: the target's logit
-  float* ref2;         // compact: reference, log2 units
+  float* ref2;         // compact: [pieces + 1][rows_pad] references before each piece and at
+                       // the end, log2 units
   float* d;            // compact
   unsigned long long* own;  // [vocab] or null: rows with this target, kOwnOne + row each
   __nv_bfloat16* xc;   // [rows_pad][pitch]
@@ -745,67 +784,15 @@ __global__ void __launch_bounds__(kRowThreads) ce_gather_kernel(const __grid_con
     for (int i = 0; i < 8; ++i) z += sm[i];
     a.target[c] = t;
     a.z_t[c] = z;
-    a.ref2[c] = z * kLog2e;
+    for (int i = 0; i <= a.pieces; ++i) a.ref2[(size_t)i * a.rows_pad + c] = z * kLog2e;
     if (a.d_nll != nullptr) a.d[c] = __ldg(a.d_nll + row);
-  }
-}
-
-struct CeUpdate {
-  const int* n;
-  int rows_pad, pitch, first, n_parts, parts, slices;  // `n_parts` from `first` on
-  const float* part_m;
-  float* ref2;
-  float* hist;   // [rows_pad] of this piece
-  int* flag;     // [rows_pad / 32]
-  int* any;      // of this piece
-  float* acc;    // [slices][rows_pad][pitch], earlier pieces; null: none
-};
-
-// After a piece's exponentials, a warp per row: rows whose largest logit
-// leaves the range take it as their reference, what they hold of earlier
-// pieces follows, and their group of 32 is flagged for the repair.
-__global__ void __launch_bounds__(1024) ce_update_kernel(const __grid_constant__ CeUpdate a) {
-  __shared__ float factor[32];
-  grid_dep_sync();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + warp;
-  const bool live = row < __ldcg(a.n);
-  float f = 1.f;
-  if (live) {
-    const float* part = a.part_m + (size_t)row * a.parts + a.first;
-    float m = kNegInf;
-    for (int t = lane; t < a.n_parts; t += 32) m = fmaxf(m, __ldcg(part + t));
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = __ldcg(a.ref2 + row);
-    const bool far = m - ref > kRefSlack;
-    if (far) f = fast_exp2(ref - m);
-    if (lane == 0) {
-      if (far) a.ref2[row] = m;
-      a.hist[row] = far ? m : ref;
-    }
-  }
-  if (lane == 0) factor[warp] = f;
-  const int any = __syncthreads_or(f != 1.f);
-  if (threadIdx.x == 0) {
-    a.flag[blockIdx.x] = any;
-    if (any) *a.any = 1;  // (every writer stores the same)
-  }
-  if (!any || a.acc == nullptr) return;
-  for (int r = 0; r < 32; ++r) {
-    const float k = factor[r];
-    if (k == 1.f) continue;
-    for (int s = 0; s < a.slices; ++s) {
-      float* v = a.acc + ((size_t)s * a.rows_pad + blockIdx.x * 32 + r) * a.pitch;
-      for (int i = threadIdx.x; i < a.pitch; i += 1024) v[i] *= k;
-    }
   }
 }
 
 struct CeSums {
   const float* part_m;  // [rows_pad][parts]
   const float* part_s;
-  const float* hist;    // gradient: [piece][rows_pad] the references of the sums, log2 units
+  const float* refs;    // gradient: [piece][rows_pad] the references of the sums, log2 units
   int parts, piece_parts;
   float* nll;           // [rows]
   float* lse;
@@ -845,7 +832,7 @@ __global__ void __launch_bounds__(kRowThreads)
   float m = kNegInf, sum = 0.f;
   const float* pm = s.part_m + (size_t)c * s.parts;
   const float* ps = s.part_s + (size_t)c * s.parts;
-  if (s.hist == nullptr) {
+  if (s.refs == nullptr) {
     for (int t = threadIdx.x; t < s.parts; t += kRowThreads) join(m, sum, __ldcg(pm + t),
                                                                   __ldcg(ps + t));
   } else {
@@ -853,7 +840,7 @@ __global__ void __launch_bounds__(kRowThreads)
       float one = 0.f;
       for (int t = t0 + threadIdx.x; t < min(t0 + s.piece_parts, s.parts); t += kRowThreads)
         one += __ldcg(ps + t);
-      join(m, sum, __ldcg(s.hist + (size_t)i * a.rows_pad + c), one);
+      join(m, sum, __ldcg(s.refs + (size_t)i * a.rows_pad + c), one);
     }
   }
 #pragma unroll
@@ -882,7 +869,8 @@ __global__ void __launch_bounds__(kRowThreads)
   if (s.dx == nullptr) return;
   // the products are relative to the row's last reference
   const float d = __ldcg(a.d + c);
-  const float f = failed ? nan : d * fast_exp2(__ldcg(a.ref2 + c) - top) / total;
+  const float last = __ldcg(a.ref2 + (size_t)a.pieces * a.rows_pad + c);
+  const float f = failed ? nan : d * fast_exp2(last - top) / total;
   const float g = d * (others / total);
   if (threadIdx.x == 0) {
     s.scale[c] = f;
@@ -967,7 +955,7 @@ struct Plan {
   int piece, pieces;   // columns of a piece (a multiple of 256)
   int splits;          // of ACC's K
   bool keep;           // dw from the exponentials that dx was made from
-  size_t any, place, target, z_t, ref2, d, miss, lse2, scale, own, hist, flag, xc, part_m, part_s, g,
+  size_t any, place, target, z_t, ref2, d, miss, lse2, scale, own, xc, part_m, part_s, g,
       low, acc, total;
 };
 
@@ -1013,17 +1001,15 @@ Plan make_plan(int rows, int vocab, int hidden, int grads) {
   p.place = take((size_t)rows * 4);
   p.target = take(pad * 4);
   p.z_t = take(pad * 4);
-  p.ref2 = take(pad * 4);
+  p.ref2 = take(pad * (p.pieces + 1) * 4);
   p.xc = take(pad * p.pitch * 2);
-  p.part_m = take(pad * p.n_tiles * 2 * 4);
+  if (grads == 0) p.part_m = take(pad * p.n_tiles * 2 * 4);
   p.part_s = take(pad * p.n_tiles * 2 * 4);
   if (grads > 0) {
     p.d = take(pad * 4);
     p.miss = take(pad * 4);
     p.lse2 = take(pad * 4);
     p.scale = take(pad * 4);
-    p.hist = take(pad * p.pieces * 4);
-    p.flag = take(pad / 32 * 4);
     p.g = take(pad * p.piece * 2);
     if (p.keep) p.low = take(pad * p.piece);
     if (grads == 2) p.own = take((size_t)vocab * 8);
@@ -1222,37 +1208,30 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     return done("cross entropy launch");
   }
 
-  sums.hist = f32(p.hist);
+  sums.refs = a.ref2 + pad;
   sums.acc = f32(p.acc);
   sums.slices = p.splits;
   sums.dx = static_cast<__nv_bfloat16*>(c.dx);
   sums.miss = f32(p.miss);
   sums.lse2 = f32(p.lse2);
   sums.scale = f32(p.scale);
-  CeUpdate up{};
-  up.n = a.n;
-  up.rows_pad = pad;
-  up.pitch = p.pitch;
-  up.parts = p.n_tiles * 2;
-  up.slices = p.splits;
-  up.part_m = gm.part_m;
-  up.ref2 = a.ref2;
-  up.flag = i32(p.flag);
   for (int i = 0; i < p.pieces && e == cudaSuccess; ++i) {
     const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
     CeGemm ex = gm;
     ex.v0 = v0;
     ex.n_tiles = tiles;
+    ex.ref2 = a.ref2 + (size_t)i * pad;
+    ex.raised = a.ref2 + (size_t)(i + 1) * pad;
+    ex.pieces_left = p.pieces - i;
+    ex.any = a.any + i;
     if (p.keep) ex.low = reinterpret_cast<uint8_t*>(base + p.low);
     e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
-    up.first = v0 / HN;
-    up.n_parts = tiles * 2;
-    up.hist = f32(p.hist) + (size_t)i * pad;
-    up.any = a.any + i;
-    up.acc = i > 0 ? f32(p.acc) : nullptr;
-    if (e == cudaSuccess) e = launch_pdl(ce_update_kernel, dim3(pad / 32), b1024, 0, s, up);
-    ex.any = up.any;
-    ex.repair = up.flag;
+    ex.repair = 1;
+    if (i > 0) {
+      ex.acc = f32(p.acc);
+      ex.acc_pitch = p.pitch;
+      ex.acc_slices = p.splits;
+    }
     if (e == cudaSuccess)
       e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
     CeGemm ac = gm;
