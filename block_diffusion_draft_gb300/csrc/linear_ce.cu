@@ -266,6 +266,14 @@ DF_DEV void raise(const CeGemm& p, int row, float top) {
   *p.any = 1;  // (every writer stores the same)
 }
 
+// A pair's last row tile of at most 128 rows is half a tile: each CTA takes 64
+// rows, of which the tensor memory's lanes 0-63 hold columns 0-127 of the tile
+// and lanes 64-127 the others, in half the time.
+template <int EPI, int CG>
+DF_DEV bool half_tile(const Tile& t, int rows) {
+  return CG == 2 && EPI != OUT && rows - t.m * CG * BM <= BM;
+}
+
 // What a warp stores by bulk copies goes through slabs of 4 KB of its own, in
 // the layout of the 128-byte swizzle: 16-byte chunk c of row r at place
 // c ^ (r % 8).  A slab is filled once the copy that last read it has.
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = first; alive && u < units; u += stride) {
         const Tile t = tile_at(p, m_tiles, n_kb, u);
         if (repair && !raised<CG>(p, t, 0, 1)) continue;
-        const int m0 = (t.m * CG + rank) * BM, n0 = t.n * BN + rank * (BN / CG);
+        const int m0 = t.m * CG * BM + rank * (half_tile<EPI, CG>(t, rows) ? BM / 2 : BM), n0 = t.n * BN + rank * (BN / CG);
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, p.err)) {
             alive = false;
@@ -375,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_ce(CG * BM, BN, kAmn, kBmn);
       uint32_t s = 0, ph = 0, tc = 0;
       bool alive = true;
       for (int u = first; alive && u < units; u += stride) {
@@ -385,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tc;
         if (!mbar_wait(&acc_empty[buf], (use & 1) ^ 1, abort_flag, p.err)) break;
         tc_fence_after();
+        const uint32_t idesc = half_tile<EPI, CG>(t, rows) ? idesc_ce(BM, BN, kAmn, kBmn)
+                                                           : idesc_ce(CG * BM, BN, kAmn, kBmn);
         const uint32_t d = tmem + buf * BN;
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!mbar_wait(&full[s], ph, abort_flag, p.err)) {
@@ -417,9 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tgt = -1;
       float ref = 0.f, sc = 0.f, miss = 0.f;
     };
+    auto first_row = [&](const Tile& t) {  // of this warp
+      return half_tile<EPI, CG>(t, rows) ? t.m * CG * BM + rank * (BM / 2) + (q & 1) * 32
+                                         : (t.m * CG + rank) * BM + q * 32;
+    };
     auto row_of = [&](const Tile& t) {
       Row r;
-      const int row = (t.m * CG + rank) * BM + q * 32 + lane;
+      const int row = first_row(t) + lane;
       if (EPI == OUT) {  // (here a row is a column of the vocabulary)
         r.sc = 1.f;
         if (p.v0 + row < p.vocab) {
@@ -471,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (repair && !__any_sync(0xffffffffu, raised<CG>(p, t, lane, 32))) continue;
       const bool any = t.k0 < t.k1;  // otherwise the tile is zero
-      const int row0 = (t.m * CG + rank) * BM + q * 32, row = row0 + lane;
+      const bool small = half_tile<EPI, CG>(t, rows);
+      const int row0 = first_row(t), row = row0 + lane;
       const bool live = EPI == ACC || EPI == OUT || row < rows;
-      const int x0 = t.n * BN + half * HN;   // first column of this warp
+      const int x0 = t.n * BN + (small ? q >> 1 : half) * HN;  // first column of this warp
       const int cols = p.vocab - p.v0 - x0;  // logits: columns that exist
       const int tgt = mine.tgt - p.v0 - x0;  // the target's among them
       const float sc = mine.sc, miss = mine.miss;
@@ -485,7 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         tc_fence_after();
       }
-      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + half * HN;
+      if (small && half) {  // the other four warps have all of it
+        __syncwarp();
+        if (any && lane == 0) arrive_cluster(cluster_map(smem_u32(&acc_empty[buf]), 0));
+        continue;
+      }
+      const uint32_t trow =
+          tmem + ((uint32_t)(q * 32) << 16) + buf * BN + (small ? 0 : half * HN);
       float mx = kNegInf, sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < HN / 32; ++c) {
@@ -812,21 +832,23 @@ DF_DEV void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
-// One CTA per row: nll and lse from the tiles' sums, joined in a fixed order,
-// and with a gradient dx = d * (acc / sum - (1 - p_t) * w_t).
+// One CTA per row (or several where rows are few, a share of the channels each):
+// nll and lse from the tiles' sums, joined in a fixed order, and with a gradient dx = d * (acc / sum - (1 - p_t) * w_t).
 __global__ void __launch_bounds__(kRowThreads)
     ce_finish_kernel(const __grid_constant__ CeRows a, const __grid_constant__ CeSums s) {
   __shared__ float sm[8], ss[8];
   grid_dep_sync();
   const int row = blockIdx.x, c = __ldcg(a.place + row), n8 = a.hidden / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = blockIdx.y * kRowThreads + threadIdx.x, step = gridDim.y * kRowThreads;
+  const bool one = threadIdx.x == 0 && blockIdx.y == 0;
   const float nan = __int_as_float(0x7fc00000);
   const bool failed = __ldcg(a.err) != 0;  // a wait ran out: no number is right
   uint4* out = reinterpret_cast<uint4*>(s.dx + (size_t)row * a.hidden);
   if (c < 0) {
-    if (threadIdx.x == 0) s.nll[row] = s.lse[row] = failed ? nan : 0.f;
+    if (one) s.nll[row] = s.lse[row] = failed ? nan : 0.f;
     if (s.dx != nullptr)
-      for (int i = threadIdx.x; i < n8; i += kRowThreads) out[i] = make_uint4(0, 0, 0, 0);
+      for (int i = i0; i < n8; i += step) out[i] = make_uint4(0, 0, 0, 0);
     return;
   }
   float m = kNegInf, sum = 0.f;
@@ -856,7 +878,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const float top = sum == 0.f ? z2 : fmaxf(m, z2);
   const float others = sum == 0.f ? 0.f : sum * fast_exp2(m - top);  // relative to `top`
   const float total = others + fast_exp2(z2 - top);
-  if (threadIdx.x == 0) {
+  if (one) {
     // where the target leads, log1p keeps what is left of a small loss
     const float nll = top == z2 ? log1pf(others) : logf(total) + (top - z2) * kLn2;
     s.nll[row] = failed ? nan : nll;
@@ -872,15 +894,15 @@ __global__ void __launch_bounds__(kRowThreads)
   const float last = __ldcg(a.ref2 + (size_t)a.pieces * a.rows_pad + c);
   const float f = failed ? nan : d * fast_exp2(last - top) / total;
   const float g = d * (others / total);
-  if (threadIdx.x == 0) {
+  if (one) {
     s.scale[c] = f;
     // (whole numbers: the sum does not depend on the rows' order)
     if (a.own != nullptr) atomicAdd(a.own + __ldcg(a.target + c), kOwnOne + (unsigned)c);
   }
   const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
-  for (int i = threadIdx.x; i < n8; i += kRowThreads) {
+  for (int i = i0; i < n8; i += step) {
     float v[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < s.slices; ++k) {
       const float4* p = reinterpret_cast<const float4*>(
                             s.acc + ((size_t)k * a.rows_pad + c) * a.pitch) + 2 * i;
@@ -1243,7 +1265,10 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     if (e == cudaSuccess)
       e = launch_gemm<ACC>(p.cg, g_k, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
   }
-  if (e == cudaSuccess) e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, sums);
+  // (up to 1024 rows a thread has 8 channels: 12 -> 6 us at 16 rows of 4096)
+  const int shares = c.rows <= 1024 ? (H / 8 + kRowThreads - 1) / kRowThreads : 1;
+  if (e == cudaSuccess)
+    e = launch_pdl(ce_finish_kernel, dim3(c.rows, shares), b256, 0, s, a, sums);
   for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
     const int v0 = i * p.piece, tiles = std::min(p.piece, V - v0 + BN - 1) / BN;
     if (p.keep) {

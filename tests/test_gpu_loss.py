@@ -82,7 +82,8 @@ def check(x, w, t, d, grads=("none", "x", "xw")):
 
 SIZES = [(1, 1, 8), (1, 2, 8), (3, 5, 16), (16, 300, 64), (17, 257, 72), (127, 256, 128),
          (128, 1000, 256), (129, 999, 200), (255, 2048, 64), (257, 513, 1000), (300, 5000, 320),
-         (1000, 300, 8), (2, 40001, 104)]
+         (1000, 300, 8), (2, 40001, 104), (384, 700, 128), (385, 700, 128), (383, 1300, 72),
+         (320, 600, 64), (640, 513, 64)]
 
 
 @pytest.mark.parametrize("ignored", [0.0, 0.4])
