@@ -297,6 +297,7 @@ DF_DEV void slab_put(uint8_t* slab, int lane, int chunk, uint4 v) {
 template <int EPI, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
+                   const __grid_constant__ CUtensorMap tm_a64,  // the same in boxes of 64 rows
                    const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CeGemm p) {
   using G = Geo<EPI, CG>;
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_a);
+    prefetch_tmap(&tm_a64);
     prefetch_tmap(&tm_b);
     prefetch_tmap(&tm_out);
   }
@@ -351,14 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = first; alive && u < units; u += stride) {
         const Tile t = tile_at(p, m_tiles, n_kb, u);
         if (repair && !raised<CG>(p, t, 0, 1)) continue;
-        const int m0 = t.m * CG * BM + rank * (half_tile<EPI, CG>(t, rows) ? BM / 2 : BM), n0 = t.n * BN + rank * (BN / CG);
+        const bool small = half_tile<EPI, CG>(t, rows);
+        const int m0 = t.m * CG * BM + rank * (small ? BM / 2 : BM), n0 = t.n * BN + rank * (BN / CG);
         for (int kb = t.k0; kb < t.k1; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, p.err)) {
             alive = false;
             break;
           }
           // (the first CTA's barrier counts the bytes of both)
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * G::STAGE);
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[s], CG * (G::STAGE - (small ? A_BYTES / 2 : 0)));
           const uint32_t bar =
               CG == 2 ? cluster_map(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
           const uint32_t a = smem_u32(smem + s * G::STAGE), b = a + A_BYTES;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < BM / 64; ++i)
               load_box<CG>(a + i * 8192, &tm_a, bar, m0 + 64 * i, kb * BK);
           } else {
-            load_box<CG>(a, &tm_a, bar, kb * BK, m0);
+            load_box<CG>(a, small ? &tm_a64 : &tm_a, bar, kb * BK, m0);
           }
           if (kBmn) {
 #pragma unroll
@@ -1047,8 +1051,9 @@ int make_map(CUtensorMap* m, const void* p, bool f32, long long rows, long long 
 }
 
 template <int EPI, int CG>
-cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
-                        const CeGemm& p, int units, int sms, cudaStream_t s) {
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& a64, const CUtensorMap& b,
+                        const CUtensorMap& out, const CeGemm& p, int units, int sms,
+                        cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   if (!done_on_device(attr_done)) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -1061,15 +1066,15 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
   CeGemm q = p;
   q.by_group = Divisor(kGroup * p.n_tiles);
   return launch_pdl_cluster(ce_gemm_kernel<EPI, CG>, dim3(grid), dim3(kThreads),
-                            Geo<EPI, CG>::SMEM, s, (unsigned)CG, a, b, out, q);
+                            Geo<EPI, CG>::SMEM, s, (unsigned)CG, a, a64, b, out, q);
 }
 
 template <int EPI>
-cudaError_t launch_gemm(int cg, const CUtensorMap& a, const CUtensorMap& b,
-                        const CUtensorMap& out, const CeGemm& p, int units, int sms,
-                        cudaStream_t s) {
-  return cg == 1 ? launch_gemm<EPI, 1>(a, b, out, p, units, sms, s)
-                 : launch_gemm<EPI, 2>(a, b, out, p, units, sms, s);
+cudaError_t launch_gemm(int cg, const CUtensorMap& a, const CUtensorMap& a64,
+                        const CUtensorMap& b, const CUtensorMap& out, const CeGemm& p, int units,
+                        int sms, cudaStream_t s) {
+  return cg == 1 ? launch_gemm<EPI, 1>(a, a64, b, out, p, units, sms, s)
+                 : launch_gemm<EPI, 2>(a, a64, b, out, p, units, sms, s);
 }
 
 struct Call {
@@ -1179,13 +1184,15 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   // maps: x by rows and by channels, w the same, a piece's exponentials, the
   // fp32 products, dw
   const long long w_pitch = V > 1 ? c.w_stride : H;
-  CUtensorMap x_k, w_k, x_mn, w_mn, g_k, g_mn, acc_out, dw_out;
+  CUtensorMap x_k, x_k64, w_k, x_mn, w_mn, g_k, g_k64, g_mn, acc_out, dw_out;
   int bad = make_map(&x_k, a.xc, false, pad, H, p.pitch, 64, BM) |
+            make_map(&x_k64, a.xc, false, pad, H, p.pitch, 64, BM / 2) |
             make_map(&w_k, c.w, false, V, H, w_pitch, 64, BN / p.cg);
   if (grad) {
     const void* g = base + p.g;
     bad |= make_map(&w_mn, c.w, false, V, H, w_pitch, 64, 64) |
            make_map(&g_k, g, false, pad, p.piece, p.piece, 64, BM) |
+           make_map(&g_k64, g, false, pad, p.piece, p.piece, 64, BM / 2) |
            make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, p.pitch, 32, 32);
     if (c.dw != nullptr)
       bad |= make_map(&x_mn, a.xc, false, pad, H, p.pitch, 64, 64) |
@@ -1225,7 +1232,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   if (!grad) {
     gm.n_tiles = p.n_tiles;
     if (e == cudaSuccess)
-      e = launch_gemm<LSE>(p.cg, x_k, w_k, x_k, gm, m_tiles * p.n_tiles, sms, s);
+      e = launch_gemm<LSE>(p.cg, x_k, x_k64, w_k, x_k, gm, m_tiles * p.n_tiles, sms, s);
     if (e == cudaSuccess) e = launch_pdl(ce_finish_kernel, dim3(c.rows), b256, 0, s, a, sums);
     return done("cross entropy launch");
   }
@@ -1247,7 +1254,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ex.pieces_left = p.pieces - i;
     ex.any = a.any + i;
     if (p.keep) ex.low = reinterpret_cast<uint8_t*>(base + p.low);
-    e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
+    e = launch_gemm<EXP>(p.cg, x_k, x_k64, w_k, x_k, ex, m_tiles * tiles, sms, s);
     ex.repair = 1;
     if (i > 0) {
       ex.acc = f32(p.acc);
@@ -1255,7 +1262,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
       ex.acc_slices = p.splits;
     }
     if (e == cudaSuccess)
-      e = launch_gemm<EXP>(p.cg, x_k, w_k, x_k, ex, m_tiles * tiles, sms, s);
+      e = launch_gemm<EXP>(p.cg, x_k, x_k64, w_k, x_k, ex, m_tiles * tiles, sms, s);
     CeGemm ac = gm;
     ac.v0 = v0;
     ac.n_tiles = h_tiles;
@@ -1263,7 +1270,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ac.splits = p.splits;
     ac.add = i > 0;
     if (e == cudaSuccess)
-      e = launch_gemm<ACC>(p.cg, g_k, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
+      e = launch_gemm<ACC>(p.cg, g_k, g_k64, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
   }
   // (up to 1024 rows a thread has 8 channels: 12 -> 6 us at 16 rows of 4096)
   const int shares = c.rows <= 1024 ? (H / 8 + kRowThreads - 1) / kRowThreads : 1;
@@ -1284,7 +1291,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
       gr.ref2 = f32(p.lse2);
       gr.d = a.d;
       gr.miss = f32(p.miss);
-      e = launch_gemm<GRAD>(p.cg, x_k, w_k, x_k, gr, m_tiles * tiles, sms, s);
+      e = launch_gemm<GRAD>(p.cg, x_k, x_k64, w_k, x_k, gr, m_tiles * tiles, sms, s);
     }
     CeGemm ow = gm;
     ow.v0 = v0;
@@ -1294,7 +1301,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ow.miss = f32(p.miss);
     ow.own = a.own;
     if (e == cudaSuccess)
-      e = launch_gemm<OUT>(p.cg, g_mn, x_mn, dw_out, ow, ow.m_tiles * h_tiles, sms, s);
+      e = launch_gemm<OUT>(p.cg, g_mn, g_mn, x_mn, dw_out, ow, ow.m_tiles * h_tiles, sms, s);
   }
   return done("cross entropy launch");
 }
