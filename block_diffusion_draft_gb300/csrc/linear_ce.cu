@@ -836,37 +836,56 @@ DF_DEV void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
-// One CTA per row (or several where rows are few, a share of the channels each):
-// nll and lse from the tiles' sums, joined in a fixed order, and with a gradient dx = d * (acc / sum - (1 - p_t) * w_t).
+// nll and lse of a row from the tiles' sums, joined in a fixed order, and with a
+// gradient dx = d * (acc / sum - (1 - p_t) * w_t): a thread has 8 channels, a row
+// as many CTAs as that takes.  The products and w_t are on their way while the
+// sums are joined.
+constexpr int kAhead = 4;  // slices of the products
+
 __global__ void __launch_bounds__(kRowThreads)
     ce_finish_kernel(const __grid_constant__ CeRows a, const __grid_constant__ CeSums s) {
   __shared__ float sm[8], ss[8];
   grid_dep_sync();
-  const int row = blockIdx.x, c = __ldcg(a.place + row), n8 = a.hidden / 8;
+  const int row = blockIdx.x, c = __ldcg(a.place + row);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i0 = blockIdx.y * kRowThreads + threadIdx.x, step = gridDim.y * kRowThreads;
+  const int i = blockIdx.y * kRowThreads + threadIdx.x;  // of the channels' groups of 8
+  const bool mine = s.dx != nullptr && i < a.hidden / 8;
   const bool one = threadIdx.x == 0 && blockIdx.y == 0;
   const float nan = __int_as_float(0x7fc00000);
   const bool failed = __ldcg(a.err) != 0;  // a wait ran out: no number is right
   uint4* out = reinterpret_cast<uint4*>(s.dx + (size_t)row * a.hidden);
   if (c < 0) {
     if (one) s.nll[row] = s.lse[row] = failed ? nan : 0.f;
-    if (s.dx != nullptr)
-      for (int i = i0; i < n8; i += step) out[i] = make_uint4(0, 0, 0, 0);
+    if (mine) out[i] = make_uint4(0, 0, 0, 0);
     return;
+  }
+  float4 u[kAhead][2];
+  uint4 wt = make_uint4(0, 0, 0, 0);
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k0 + k >= s.slices) break;
+      const float4* p = reinterpret_cast<const float4*>(
+                            s.acc + ((size_t)(k0 + k) * a.rows_pad + c) * a.pitch) + 2 * i;
+      u[k][0] = __ldcg(p), u[k][1] = __ldcg(p + 1);
+    }
+  };
+  if (mine) {
+    wt = __ldg(reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride) + i);
+    load(0);
   }
   float m = kNegInf, sum = 0.f;
   const float* pm = s.part_m + (size_t)c * s.parts;
   const float* ps = s.part_s + (size_t)c * s.parts;
   if (s.refs == nullptr) {
-    for (int t = threadIdx.x; t < s.parts; t += kRowThreads) join(m, sum, __ldcg(pm + t),
-                                                                  __ldcg(ps + t));
+    for (int t = threadIdx.x; t < s.parts; t += kRowThreads)
+      join(m, sum, __ldcg(pm + t), __ldcg(ps + t));
   } else {
-    for (int i = 0, t0 = 0; t0 < s.parts; ++i, t0 += s.piece_parts) {
-      float one = 0.f;
+    for (int k = 0, t0 = 0; t0 < s.parts; ++k, t0 += s.piece_parts) {
+      float piece = 0.f;
       for (int t = t0 + threadIdx.x; t < min(t0 + s.piece_parts, s.parts); t += kRowThreads)
-        one += __ldcg(ps + t);
-      join(m, sum, __ldcg(s.refs + (size_t)i * a.rows_pad + c), one);
+        piece += __ldcg(ps + t);
+      join(m, sum, __ldcg(s.refs + (size_t)k * a.rows_pad + c), piece);
     }
   }
 #pragma unroll
@@ -877,7 +896,7 @@ __global__ void __launch_bounds__(kRowThreads)
   if (lane == 0) sm[warp] = m, ss[warp] = sum;
   __syncthreads();
   m = sm[0], sum = ss[0];
-  for (int i = 1; i < 8; ++i) join(m, sum, sm[i], ss[i]);
+  for (int w = 1; w < 8; ++w) join(m, sum, sm[w], ss[w]);
   const float z = __ldcg(a.z_t + c), z2 = z * kLog2e;
   const float top = sum == 0.f ? z2 : fmaxf(m, z2);
   const float others = sum == 0.f ? 0.f : sum * fast_exp2(m - top);  // relative to `top`
@@ -903,26 +922,24 @@ __global__ void __launch_bounds__(kRowThreads)
     // (whole numbers: the sum does not depend on the rows' order)
     if (a.own != nullptr) atomicAdd(a.own + __ldcg(a.target + c), kOwnOne + (unsigned)c);
   }
-  const uint4* w = reinterpret_cast<const uint4*>(a.w + __ldcg(a.target + c) * a.w_stride);
-  for (int i = i0; i < n8; i += step) {
-    float v[8] = {};
-#pragma unroll 8
-    for (int k = 0; k < s.slices; ++k) {
-      const float4* p = reinterpret_cast<const float4*>(
-                            s.acc + ((size_t)k * a.rows_pad + c) * a.pitch) + 2 * i;
-      const float4 u0 = __ldcg(p), u1 = __ldcg(p + 1);
-      v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
-      v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
-    }
-    const uint4 t = __ldg(w + i);
-    const uint32_t u[4] = {t.x, t.y, t.z, t.w};
-    uint32_t o[4];
+  if (!mine) return;
+  float v[8] = {};
+  for (int k0 = 0; k0 < s.slices; k0 += kAhead) {
+    if (k0 > 0) load(k0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2(v[2 * j] * f - g * __uint_as_float(u[j] << 16),
-                         v[2 * j + 1] * f - g * __uint_as_float(u[j] & 0xffff0000u));
-    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < kAhead; ++k) {
+      if (k0 + k >= s.slices) break;
+      v[0] += u[k][0].x, v[1] += u[k][0].y, v[2] += u[k][0].z, v[3] += u[k][0].w;
+      v[4] += u[k][1].x, v[5] += u[k][1].y, v[6] += u[k][1].z, v[7] += u[k][1].w;
+    }
   }
+  const uint32_t t[4] = {wt.x, wt.y, wt.z, wt.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = pack_bf16x2(v[2 * j] * f - g * __uint_as_float(t[j] << 16),
+                       v[2 * j + 1] * f - g * __uint_as_float(t[j] & 0xffff0000u));
+  out[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The kept exponentials of a piece that is the whole vocabulary, with their
@@ -1272,8 +1289,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     if (e == cudaSuccess)
       e = launch_gemm<ACC>(p.cg, g_k, g_k64, w_mn, acc_out, ac, m_tiles * h_tiles * p.splits, sms, s);
   }
-  // (up to 1024 rows a thread has 8 channels: 12 -> 6 us at 16 rows of 4096)
-  const int shares = c.rows <= 1024 ? (H / 8 + kRowThreads - 1) / kRowThreads : 1;
+  const int shares = (H / 8 + kRowThreads - 1) / kRowThreads;
   if (e == cudaSuccess)
     e = launch_pdl(ce_finish_kernel, dim3(c.rows, shares), b256, 0, s, a, sums);
   for (int i = 0; c.dw != nullptr && i < p.pieces && e == cudaSuccess; ++i) {
