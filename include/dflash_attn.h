@@ -11,8 +11,9 @@
  * cropped back to the accepted prefix after verification.  Around it: the
  * context K/V of several layers from one projection, the rest of the draft
  * decoder layer (norms, residual stream, SwiGLU MLP), a paged cache with a
- * slot mapping and block tables, causal layers, and the attention core of
- * the packed training layout with its backward.
+ * slot mapping and block tables, causal layers, the attention core of
+ * the packed training layout with its backward, and what training needs
+ * around it (head norm and rotation, the head's loss, clipping).
  *
  * Page citations name the page by title and the section or symbol on it:
  *   [P3] "DFlash源码导读（二）：Qwen3DFlashAttention注意力实现全解析"
