@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ double sm[kThreads / 32];
   __shared__ double sums[kClusterCtas];
   const int rank = (int)cluster_ctarank(), total = t.first[t.tensors];
+  cluster_arrive();  // (waited for before anything goes to another CTA's memory)
   grid_dep_sync();
   double acc = 0.;
   uint4 v[kVecs];
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(kThreads)
     acc += chunk_square(x, v);
   }
   const double s = block_sum(acc, sm);
+  cluster_wait();
   if (threadIdx.x < kClusterCtas)
     st_cluster_u64(cluster_map(smem_u32(&sums[rank]), threadIdx.x),
                    (unsigned long long)__double_as_longlong(s));

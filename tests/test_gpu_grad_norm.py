@@ -152,6 +152,28 @@ def test_dense_tensors_in_any_order_of_axes():
     check_clipped([a, b], before, 0.5)
 
 
+def test_neighbouring_slices_of_one_buffer():
+    """Tensors that touch, at any offset: nothing of a neighbour is written."""
+    for dtype in (torch.bfloat16, torch.float32):
+        flat = torch.randn(60000, device="cuda").to(dtype)
+        cuts = [3, 4, 21, 22, 1000, 1007, 30001, 59990]
+        parts = [flat[a:b] for a, b in zip(cuts, cuts[1:])]
+        rest = [flat[:3].clone(), flat[59990:].clone()]
+        before = [p.clone() for p in parts]
+        want = norm64(parts)
+        clip_grad_norm(parts[::2] + parts[1::2], 0.5 * want)
+        check_clipped(parts, before, 0.5)
+        assert torch.equal(flat[:3], rest[0]) and torch.equal(flat[59990:], rest[1])
+
+
+def test_one_gradient_into_two_buffers():
+    g = torch.randn(5001, device="cuda")
+    out = [torch.empty_like(g), torch.empty_like(g)]
+    want = norm64([g, g])
+    clip_grad_norm([g, g], 0.25 * want, out)
+    check_clipped(out, [g, g], 0.25)
+
+
 def test_refusals():
     a, b = torch.randn(64, device="cuda"), torch.randn(64, device="cuda")
     for f in (lambda: grad_norm([]), lambda: grad_norm([a.half()]), lambda: grad_norm([a.cpu()]),
