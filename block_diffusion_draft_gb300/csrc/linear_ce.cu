@@ -111,6 +111,9 @@ struct CeGemm {
   int add;             // ACC: the buffer holds earlier pieces
   float* acc;          // repair: [splits][rows_pad][acc_pitch] earlier pieces' products, or null
   int acc_pitch, acc_slices;
+  float* nll;          // GRAD, OUT: [all_rows] where a wait that ran out leaves NaN (the kernels
+  float* lse;          // before them leave it to the one that writes nll)
+  int all_rows;
   int* err;
 };
 
@@ -685,6 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if ((EPI == GRAD || EPI == OUT) && *abort_flag)
+    for (int r = threadIdx.x; r < p.all_rows; r += kThreads)
+      p.nll[r] = p.lse[r] = __int_as_float(0x7fc00000);
   // no CTA leaves while its pair's copies, products or arrivals may reach it
   if (CG == 2) cluster_sync();
   if (warp == 1) {
@@ -1250,6 +1256,9 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   gm.g = reinterpret_cast<uint8_t*>(base + p.g);
   gm.g_pitch = p.piece;
   gm.parts = p.n_tiles * 2;
+  gm.nll = c.nll;
+  gm.lse = c.lse;
+  gm.all_rows = c.rows;
   gm.err = a.err;
   CeSums sums{};
   sums.part_m = gm.part_m;

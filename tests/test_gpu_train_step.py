@@ -160,3 +160,47 @@ def test_a_captured_step_equals_the_eager_one():
         assert torch.equal(nll_g, nll)
         assert all(torch.equal(grads[k], want[k]) for k in want)
     assert float(norm) == float(grad_norm(list(want.values())))
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing of the training calls needs an eager call before a capture."""
+    code = """
+import torch
+from block_diffusion_draft_gb300 import (DFlashAttention, clip_grad_norm, grad_norm,
+                                         linear_cross_entropy, linear_cross_entropy_grad)
+z = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+attn = DFlashAttention(dict(wq=z(256, 128), wk=z(128, 128), wv=z(128, 128), wo=z(128, 256),
+                            q_norm=z(128), k_norm=z(128)), hidden=128, n_heads=2, n_kv_heads=1,
+                       head_dim=128, max_position=64)
+q, k, pos = z(1, 5, 2, 128), z(1, 5, 1, 128), torch.arange(5, device="cuda").int().view(1, 5)
+x, w = z(300, 64), z(700, 64)
+t, d = torch.arange(300, device="cuda").int(), torch.ones(300, device="cuda")
+few, many = [z(99)], [z(3000000), z(7)]
+def calls():
+    out = list(attn.qk_norm_rope(q, k, pos)) + list(attn.qk_norm_rope_backward(
+        q, k, pos, None, None, q, k))
+    out += linear_cross_entropy(x, w, t)
+    for need in (True, False):
+        out += [o for o in linear_cross_entropy_grad(x, w, t, d, need) if o is not None]
+        out += [o for o in linear_cross_entropy_grad(x[:9], w, t[:9], d[:9], need)
+                if o is not None]
+    return out + [grad_norm(few), grad_norm(many), clip_grad_norm(many, 1e30)]
+s = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=s):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+want = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("captured")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
