@@ -112,3 +112,58 @@ def test_reference_cross_entropy_gradient_equals_differences():
     want = torch.nn.functional.cross_entropy(x @ w.t(), torch.where(t == 7, -100, t),
                                              reduction="none")
     assert torch.allclose(nll, want)
+
+
+def _ce(L, grad, **kw):
+    a = dict(rows=4, vocab=100, hidden=64, x=FAKE, xs=64, w=FAKE, ws=64, targets=FAKE, d_nll=FAKE,
+             nll=FAKE, lse=FAKE, dx=FAKE, dw=None, space=FAKE, bytes=1 << 40)
+    a.update(kw)
+    head = [a[k] for k in ("rows", "vocab", "hidden", "x", "xs", "w", "ws", "targets")]
+    tail = [a["space"], a["bytes"], None]
+    if grad:
+        return L.dflash_linear_ce_grad(*head, *[a[k] for k in ("d_nll", "nll", "lse", "dx", "dw")],
+                                       *tail)
+    return L.dflash_linear_ce(*head, a["nll"], a["lse"], *tail)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("kw,rc", [
+    (dict(rows=-1), -1), (dict(vocab=0), -1), (dict(hidden=0), -1), (dict(hidden=60), -2),
+    (dict(rows=(1 << 20) + 1), -2), (dict(vocab=(1 << 24) + 1), -2),
+    (dict(hidden=(1 << 16) + 8), -2), (dict(x=None), -1), (dict(w=None), -1),
+    (dict(targets=None), -1), (dict(nll=None), -1), (dict(lse=None), -1), (dict(x=FAKE + 8), -1),
+    (dict(w=FAKE + 2), -1), (dict(targets=FAKE + 2), -1), (dict(nll=FAKE + 1), -1),
+    (dict(xs=56), -1), (dict(xs=68), -1), (dict(ws=0), -1), (dict(ws=66), -1),
+    (dict(xs=1 << 33), -2), (dict(space=None), -1), (dict(space=FAKE + 16), -1),
+    (dict(bytes=100), -3)])
+def test_cross_entropy_checks_its_arguments_on_the_host(L, grad, kw, rc):
+    assert _ce(L, grad, **kw) == rc
+
+
+@pytest.mark.parametrize("kw", [dict(d_nll=None), dict(dx=None), dict(dx=FAKE + 8),
+                                dict(dw=FAKE + 4), dict(d_nll=FAKE + 2)])
+def test_cross_entropy_gradient_checks_its_arguments(L, kw):
+    assert _ce(L, True, **kw) == -1
+
+
+def test_cross_entropy_workspace(L):
+    n = ctypes.c_size_t(0)
+    f = lambda *a: L.dflash_linear_ce_workspace(*a, ctypes.byref(n))  # noqa: E731
+    assert L.dflash_linear_ce_workspace(1, 1, 8, 0, None) == -1
+    assert f(1, 1, 8, 3) == -1 and f(1, 1, 9, 0) == -2 and f(0, 1, 8, 2) == 0
+    size = {}
+    for grads in range(3):
+        assert f(4096, 150000, 4096, grads) == 0
+        size[grads] = n.value
+    assert size[0] < size[1] <= size[2]
+    # a piece's exponentials, not the vocabulary's
+    assert f(16384, 1000000, 4096, 2) == 0 and n.value < 8 << 30
+
+
+def test_cross_entropy_checks_its_tensors():
+    x, w = torch.zeros(3, 16).bfloat16(), torch.zeros(5, 16).bfloat16()
+    t, d = torch.zeros(3, dtype=torch.int32), torch.zeros(3)
+    for f in (lambda: D.linear_cross_entropy(x, w, t), lambda: D.linear_cross_entropy(x[0], w, t),
+              lambda: D.linear_cross_entropy_grad(x, w[:, :8], t, d)):
+        with pytest.raises(ValueError):
+            f()
