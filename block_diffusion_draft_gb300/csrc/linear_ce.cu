@@ -73,14 +73,15 @@ constexpr unsigned long long kOwnOne = 1ull << 40;
 enum Epi { LSE = 0, EXP = 1, GRAD = 2, ACC = 3, OUT = 4 };
 
 // CG CTAs work on one tile of CG * 128 rows and 256 columns.  Shared memory
-// holds the ring and the slabs of the epilogues that store through them: two a
-// warp where tiles are short (OUT's are as long as there are rows).
+// holds the ring and the slabs of ACC's epilogue, which adds by bulk copies (the
+// others store from registers: without fences and waits for slabs OUT's short
+// tiles are 6% faster).
 template <int EPI, int CG>
 struct Geo {
   static constexpr uint32_t B_BYTES = BN / CG * BK * 2;
   static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-  static constexpr int SLABS = EPI == ACC ? 1 : EPI == OUT ? 2 : 0;
-  static constexpr size_t FIXED = 1024 + SLABS * kEpiWarps * SLAB + 256;
+  static constexpr uint32_t SLABS = EPI == ACC ? kEpiWarps * SLAB : 0;
+  static constexpr size_t FIXED = 1024 + SLABS + 256;
   static constexpr int STAGES = (int)((232448 - FIXED) / STAGE);
   static constexpr size_t SMEM = FIXED + STAGES * STAGE;
 };
@@ -111,6 +112,7 @@ struct CeGemm {
   int add;             // ACC: the buffer holds earlier pieces
   float* acc;          // repair: [splits][rows_pad][acc_pitch] earlier pieces' products, or null
   int acc_pitch, acc_slices;
+  __nv_bfloat16* dw;   // OUT: [vocab][hidden]
   float* nll;          // GRAD, OUT: [all_rows] where a wait that ran out leaves NaN (the kernels
   float* lse;          // before them leave it to the one that writes nll)
   int all_rows;
@@ -185,8 +187,11 @@ DF_DEV void commit(uint64_t* bar) {
         : "memory");
 }
 
+// Arrival on another CTA's barrier that hands over tensor memory alone, ordered
+// by the tcgen05 fence before it: a release would wait for the epilogue's stores
+// to global memory first.
 DF_DEV void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 
@@ -292,12 +297,11 @@ DF_DEV bool half_tile(const Tile& t, int rows) {
   return CG == 2 && EPI != OUT && rows - t.m * CG * BM <= BM;
 }
 
-// What a warp stores by bulk copies goes through slabs of 4 KB of its own, in
+// What a warp stores by bulk copies goes through a slab of 4 KB of its own, in
 // the layout of the 128-byte swizzle: 16-byte chunk c of row r at place
-// c ^ (r % 8).  A slab is filled once the copy that last read it has.
-template <int SLABS>
+// c ^ (r % 8).  It is filled once the copy that last read it has.
 DF_DEV void slab_begin(int lane) {
-  if (lane == 0) bulk_wait_read<SLABS - 1>();
+  if (lane == 0) bulk_wait_read<0>();
   __syncwarp();
 }
 
@@ -317,14 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                    const __grid_constant__ CUtensorMap tm_a64,  // the same in boxes of 64 rows
                    const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CeGemm p) {
+                   const __grid_constant__ CUtensorMap tm_out,  // ACC
+                   const __grid_constant__ CeGemm p) {
   using G = Geo<EPI, CG>;
   constexpr bool kAmn = EPI == OUT, kBmn = EPI == ACC || EPI == OUT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* slabs = smem + G::STAGES * G::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + G::SLABS * kEpiWarps * SLAB);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slabs + G::SLABS);
   uint64_t* empty = full + G::STAGES;
   uint64_t* acc_full = empty + G::STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2]
@@ -440,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* slab = slabs + (warp - 2) * G::SLABS * SLAB;
-    int other = (int)SLAB;  // from one slab to the other
+    uint8_t* slab = slabs + (warp - 2) * SLAB;
     // a row's part of an epilogue that looks at logits; the next tile's is
     // read before this one's logits are waited for
     struct Row {
@@ -632,45 +636,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (EPI == OUT) {
+          const int x = x0 + c * 32;
+          if (p.v0 + row < p.vocab) {
+            __nv_bfloat16* at = p.dw + (size_t)(p.v0 + row) * p.hidden + x;
+            const bool sectors = (reinterpret_cast<uintptr_t>(at) & 31) == 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= sc;
+            for (int k = 0; k < 2; ++k) {
+              uint32_t h[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                h[i] = pack_bf16x2(v[16 * k + 2 * i] * sc, v[16 * k + 2 * i + 1] * sc);
+              if (sectors && x + 16 * k + 16 <= p.hidden) {
+                store32(at + 16 * k, h);
+              } else {
+                uint4* at4 = reinterpret_cast<uint4*>(at + 16 * k);
+                if (x + 16 * k < p.hidden) at4[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                if (x + 16 * k + 8 < p.hidden) at4[1] = make_uint4(h[4], h[5], h[6], h[7]);
+              }
+            }
+          }
+          continue;
         }
         if (EPI == ACC) {
-          slab_begin<(G::SLABS > 0 ? G::SLABS : 1)>(lane);
+          slab_begin(lane);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             slab_put(slab, lane, j,
                      make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                 __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
-        } else {
-          if ((c & 1) == 0) slab_begin<(G::SLABS > 0 ? G::SLABS : 1)>(lane);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            slab_put(slab, lane, (c & 1) * 4 + j,
-                     make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
-                                pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
-          if ((c & 1) == 0) continue;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (EPI == ACC) {
-            const int x = x0 + c * 32;
-            if (x < p.hidden) {
-              if (p.add) add_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
-              else store_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
-            }
-          } else {
-            const int x = x0 + (c - 1) * 32, y = p.v0 + row0;
-            if (x < p.hidden && y < p.vocab) store_box(&tm_out, slab, x, y);
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int x = x0 + c * 32;
+          if (lane == 0 && x < p.hidden) {
+            if (p.add) add_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
+            else store_box(&tm_out, slab, x, t.split * p.rows_pad + row0);
+            bulk_commit();
           }
-          bulk_commit();
-        }
-        if (G::SLABS == 2) {
-          slab += other;
-          other = -other;
         }
       }
       if (EPI == LSE || EPI == EXP) {
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (EPI == ACC && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -1223,9 +1224,9 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
   if (c.dw != nullptr) a.own = reinterpret_cast<unsigned long long*>(base + p.own);
 
   // maps: x by rows and by channels, w the same, a piece's exponentials, the
-  // fp32 products, dw
+  // fp32 products
   const long long w_pitch = V > 1 ? c.w_stride : H;
-  CUtensorMap x_k, x_k64, w_k, x_mn, w_mn, g_k, g_k64, g_mn, acc_out, dw_out;
+  CUtensorMap x_k, x_k64, w_k, x_mn, w_mn, g_k, g_k64, g_mn, acc_out;
   int bad = make_map(&x_k, a.xc, false, pad, H, p.pitch, 64, BM) |
             make_map(&x_k64, a.xc, false, pad, H, p.pitch, 64, BM / 2) |
             make_map(&w_k, c.w, false, V, H, w_pitch, 64, BN / p.cg);
@@ -1237,8 +1238,7 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
            make_map(&acc_out, base + p.acc, true, (long long)pad * p.splits, H, p.pitch, 32, 32);
     if (c.dw != nullptr)
       bad |= make_map(&x_mn, a.xc, false, pad, H, p.pitch, 64, 64) |
-             make_map(&g_mn, g, false, pad, p.piece, p.piece, 64, 64) |
-             make_map(&dw_out, c.dw, false, V, H, H, 64, 32);
+             make_map(&g_mn, g, false, pad, p.piece, p.piece, 64, 64);
   }
   if (bad != 0) return api_fail(DFLASH_ERR_CUDA, "tensor map encoding failed");
 
@@ -1343,8 +1343,9 @@ int run(const Call& c, bool grad, void* ws, size_t ws_bytes, cudaStream_t s) {
     ow.d = a.d;
     ow.miss = f32(p.miss);
     ow.own = a.own;
+    ow.dw = static_cast<__nv_bfloat16*>(c.dw);
     if (e == cudaSuccess)
-      e = launch_gemm<OUT>(p.cg, g_mn, g_mn, x_mn, dw_out, ow, ow.m_tiles * h_tiles, sms, s);
+      e = launch_gemm<OUT>(p.cg, g_mn, g_mn, x_mn, g_mn, ow, ow.m_tiles * h_tiles, sms, s);
   }
   return done("cross entropy launch");
 }
