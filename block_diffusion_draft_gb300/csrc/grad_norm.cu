@@ -191,7 +191,7 @@ DF_DEV double chunk_square(const Chunk& x, const uint4 (&v)[kVecs]) {
   uint32_t any = 0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
-  if (any & 0x7fff7fffu)
+  if (any & (x.wide ? 0x7fffffffu : 0x7fff7fffu))
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) acc += square4_f64(v[i], x.wide);
   return acc;

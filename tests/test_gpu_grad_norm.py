@@ -94,6 +94,15 @@ def test_magnitudes_at_the_ends_of_the_range(dtype, size):
         assert ((out[0].double() - ref).abs() <= (HALF[dtype] * 1.01 + 40 * U) * ref + tiny).all()
 
 
+@pytest.mark.parametrize("bit", range(23))
+def test_single_bits_below_the_normal_numbers(bit):
+    """Every value the same power of two: 2500 of them, whose root is 50."""
+    t = torch.full((2500,), 1 << bit, dtype=torch.int32, device="cuda").view(torch.float32)
+    assert float(grad_norm([t])) == 50 * 2.0 ** (bit - 149)
+    b = torch.full((2500,), 1 << bit % 7, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    assert float(grad_norm([b])) == 50 * 2.0 ** (bit % 7 - 133)
+
+
 def test_zeros_and_a_single_value():
     z = torch.zeros(100000, device="cuda")
     assert float(grad_norm([z])) == 0.0
