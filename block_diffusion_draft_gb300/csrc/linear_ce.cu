@@ -925,7 +925,8 @@ __global__ void __launch_bounds__(kRowThreads)
   const float total = others + fast_exp2(z2 - top);
   if (one) {
     // where the target leads, log1p keeps what is left of a small loss
-    const float nll = top == z2 ? log1pf(others) : logf(total) + (top - z2) * kLn2;
+    // (an infinite one leaves NaN: the difference is otherwise zero there)
+    const float nll = (top == z2 ? log1pf(others) : logf(total)) + (top - z2) * kLn2;
     s.nll[row] = failed ? nan : nll;
     s.lse[row] = failed ? nan : nll + z;
     if (s.dx != nullptr) {

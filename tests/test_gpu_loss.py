@@ -176,6 +176,30 @@ def test_non_finite_rows_stay_by_themselves():
 
 
 @pytest.mark.parametrize("N", [60, 400])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_a_logit_that_is_not_finite_leaves_no_finite_loss(N, value):
+    """Column 11 is `value` times the first channel: infinite for every row
+    whose first channel has the sign for it; it is the target of some rows."""
+    x, w, t, _ = inputs(N, 700, 64, 14)
+    x, w = x.clone(), w.clone()
+    x[:, 0] = torch.where(torch.arange(N, device="cuda") % 3 == 0, 0.0, 1.0)
+    w[:, 0] = 0.0
+    w[11, 0] = value
+    t[t == 11] = 12
+    t[1::9] = 11
+    d = torch.ones(N, device="cuda")
+    # 0 * value: not a number; -inf is a probability of zero where it is no target
+    bad = torch.ones(N, dtype=torch.bool, device="cuda")
+    if value == -math.inf:
+        bad = (x[:, 0] == 0) | (t == 11)
+    for nll in (linear_cross_entropy(x, w, t)[0],
+                linear_cross_entropy_grad(x, w, t, d, need_dw=False)[0],
+                linear_cross_entropy_grad(x, w, t, d)[0]):
+        assert not torch.isfinite(nll[bad]).any()
+        assert torch.isfinite(nll[~bad]).all()
+
+
+@pytest.mark.parametrize("N", [60, 400])
 def test_the_same_in_every_run_on_streams_and_in_graphs(N):
     x, w, t, d = inputs(N, 3001, 200, 6, 0.1)
     want = linear_cross_entropy_grad(x, w, t, d) + linear_cross_entropy(x, w, t)
