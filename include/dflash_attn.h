@@ -683,7 +683,8 @@ int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const d
  * product.  Sums are taken in an order that depends on the sizes and on which
  * rows have a target alone.
  * A logit that is NaN or +infinity, or the target's where it is -infinity,
- * leaves the row's nll not finite, and nothing of other rows but dw.
+ * leaves the row's nll not finite; an x that is not finite changes dw, but
+ * nothing else of other rows.
  *   workspace  device, 256-byte aligned, the caller's until the work is done;
  *              dflash_linear_ce_workspace gives its size for grads = 0 (nll and
  *              lse), 1 (dx) or 2 (dx and dw): for a piece's exponentials at
