@@ -480,11 +480,17 @@ __global__ void __launch_bounds__(kGainCols * kGainSlices)
   red[s][c] = v;
   __syncthreads();
   if (s == 0 && col < d) {
-    float sum = 0.f;
+    // (eight sums, then those: with one after the other their roundings were
+    // most of the fp32 gradients' error)
+    float sum[8] = {};
 #pragma unroll
-    for (int i = 0; i < kGainSlices; ++i) sum += red[i][c];
+    for (int i = 0; i < kGainSlices; ++i) sum[i & 7] += red[i][c];
+#pragma unroll
+    for (int o = 4; o > 0; o /= 2)
+#pragma unroll
+      for (int i = 0; i < o; ++i) sum[i] += sum[i + o];
     float* out = kind ? dk_gain : dq_gain;
-    if (out != nullptr) out[col] = sum;
+    if (out != nullptr) out[col] = sum[0];
   }
 }
 
