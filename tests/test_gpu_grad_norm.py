@@ -202,3 +202,17 @@ def test_refusals():
             f()
     assert torch.equal(a, keep)
     assert float(grad_norm([a, a])) > 0  # reading twice is allowed
+
+
+def test_a_tensor_of_more_than_2_31_values():
+    """Ones but for two values: their squares' sum and its root are exact."""
+    n = (1 << 31) + 12345
+    t = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+    t[-1], t[12345] = 1024.0, -512.0
+    want = math.sqrt(n - 2 + 2.0 ** 20 + 2.0 ** 18)
+    assert abs(float(grad_norm([t])) - want) <= 34 * U * want
+    # a factor of a half, but for its rounding, gives halves in bf16
+    assert abs(float(clip_grad_norm([t], want / 2)) - want) <= 34 * U * want
+    assert float(t[-1]) == 512.0 and float(t[12345]) == -256.0
+    t[-1] = t[12345] = 0.5
+    assert float(t.min()) == 0.5 and float(t.max()) == 0.5

@@ -139,6 +139,48 @@ def test_several_pieces():
     check(x, w, t, d)
 
 
+def test_a_head_whose_rows_lie_far_apart():
+    x, w, t, d = inputs(20, 260, 64, 15)
+    space = torch.zeros(260 * ((1 << 23) + 8), device="cuda", dtype=torch.bfloat16)
+    far = space.as_strided((260, 64), ((1 << 23) + 8, 1))
+    far.copy_(w)
+    want = linear_cross_entropy_grad(x, w, t, d)
+    assert all(torch.equal(a, b) for a, b in zip(linear_cross_entropy_grad(x, far, t, d), want))
+
+
+def test_a_head_of_more_than_2_31_values():
+    """Zero but for its last 64 columns, which hold the targets: the other
+    columns' logits are 0 and their dw the same everywhere.  Tolerances as
+    above, with z of the last columns alone."""
+    N, V, H, last = 8, 530000, 4096, 64
+    x, tail, t, d = inputs(N, last, H, 16)
+    w = torch.zeros(V, H, device="cuda", dtype=torch.bfloat16)
+    w[-last:] = tail
+    nll, lse, dx, dw = linear_cross_entropy_grad(x, w, t + (V - last), d)
+    z = x.double() @ tail.double().t()
+    want = torch.log(z.exp().sum(1) + (V - last))
+    z_size = (x.double().abs() @ tail.double().abs().t()).amax(1)
+    e = 2 * (H / 16 + 32) * 2 * U * z_size + 4 * U * z.abs().amax(1) + 264 * U
+    within(lse, want, e + 4 * U * want.abs(), "lse")
+    within(nll, want - z.gather(1, t.long()[:, None])[:, 0], e + 4 * U * nll.double().abs(), "nll")
+    p = torch.cat([torch.zeros(N, last, device="cuda", dtype=torch.float64), z], 1)
+    p = (p - want[:, None]).exp()
+    hit = torch.nn.functional.one_hot(t.long() + last, 2 * last)
+    f = d.double()[:, None] * (p - hit)
+    rows = torch.cat([dw[:last], dw[-last:]])
+    rel = 2 * HALF + float(e.max()) + (N / 16 + 32) * 2 * U
+    size = (d.double()[:, None] * (p + hit)).abs().t() @ x.double().abs()
+    ref = f.t() @ x.double()
+    within(rows, ref, HALF * 1.01 * ref.abs() + rel * size, "dw")
+    assert torch.equal(dw[:last], dw[:1].expand(last, H))
+    assert torch.equal(dw[V // 2:V // 2 + last], dw[:last])
+    assert torch.equal(dw[V - 2 * last:V - last], dw[:last])
+    ref = f[:, last:] @ tail.double()
+    size = (d.double()[:, None] * (p + hit)).abs()[:, last:] @ tail.double().abs()
+    within(dx, ref, HALF * 1.01 * ref.abs() + (HALF + e[:, None] + (V / 16 + 32) * 2 * U) * size,
+           "dx")
+
+
 def test_nothing_counts():
     x, w, t, d = inputs(50, 400, 64, 2)
     t.fill_(-1)

@@ -202,3 +202,27 @@ def test_refusals():
                   (2, 9, 4, 128), (9 * 512, 448, 128, 1)))):
         with pytest.raises(DFlashError, match="ARG"):
             f()
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_offsets_above_32_bits(axis):
+    """One axis of every tensor strides over 2^31 elements and more: the same
+    results as of dense tensors."""
+    attn, _ = layer(2, 2, 128, torch.bfloat16)
+    shape = (2, 2, 2, 128)
+    g = torch.Generator().manual_seed(axis)
+    dense = [torch.randn(shape, generator=g).bfloat16().cuda() for _ in range(4)]
+    pos = torch.tensor([[5, 60000], [17, 3]], dtype=torch.int32, device="cuda")
+    want = attn.qk_norm_rope(dense[0], dense[1], pos)
+    back = attn.qk_norm_rope_backward(dense[0], dense[1], pos, None, None, dense[2], dense[3])
+    space = torch.zeros((1 << 31) + 4096 * 6, device="cuda", dtype=torch.bfloat16)
+    strides = [1024, 512, 256, 1]
+    strides[axis] = 1 << 31
+    far = [space[i * 4096:].as_strided(shape, strides) for i in range(6)]
+    for f, x in zip(far, dense):
+        f.copy_(x)
+    got = attn.qk_norm_rope(far[0], far[1], pos, q_out=far[4], k_out=far[5])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = attn.qk_norm_rope_backward(far[0], far[1], pos, None, None, far[2], far[3],
+                                     dq_out=far[4], dk_out=far[5])
+    assert all(torch.equal(a, b) for a, b in zip(got, back))
