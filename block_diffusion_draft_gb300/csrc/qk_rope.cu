@@ -340,16 +340,17 @@ __global__ void __launch_bounds__(kBackThreads, kCtasPerSm)
         ux += __shfl_xor_sync(0xffffffffu, ux, o);
       }
       if (t.head + u * G + g >= n) continue;
+      // (r times a sum of products with x, and r times x, are of ordinary size
+      // whatever x's is; r * r * r leaves fp32's normal numbers above an rms of 4e12)
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float2 r2 = both(r), m2 = both(-r * r * r * ux * (1.f / D));
+      const float2 r2 = both(r), m2 = both(r * (-r * ux * (1.f / D)));
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const float2 va = xa.pair(j), vb = xb.pair(j);
-        const float2 pa = mul_f32x2(r2, wa[j]), pb = mul_f32x2(r2, wb[j]);
-        acc[j] = fma_f32x2(pa, va, acc[j]);
-        acc[P + j] = fma_f32x2(pb, vb, acc[P + j]);
-        wa[j] = fma_f32x2(pa, ga[j], mul_f32x2(va, m2));
-        wb[j] = fma_f32x2(pb, gb[j], mul_f32x2(vb, m2));
+        const float2 na = mul_f32x2(r2, xa.pair(j)), nb = mul_f32x2(r2, xb.pair(j));
+        acc[j] = fma_f32x2(wa[j], na, acc[j]);
+        acc[P + j] = fma_f32x2(wb[j], nb, acc[P + j]);
+        wa[j] = fma_f32x2(mul_f32x2(r2, wa[j]), ga[j], mul_f32x2(na, m2));
+        wb[j] = fma_f32x2(mul_f32x2(r2, wb[j]), gb[j], mul_f32x2(nb, m2));
       }
       ya.set(wa);
       yb.set(wb);

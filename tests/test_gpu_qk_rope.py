@@ -226,3 +226,29 @@ def test_offsets_above_32_bits(axis):
     got = attn.qk_norm_rope_backward(far[0], far[1], pos, None, None, far[2], far[3],
                                      dq_out=far[4], dk_out=far[5])
     assert all(torch.equal(a, b) for a, b in zip(got, back))
+
+
+# Size and kind of the kernels' paths: 16-byte pieces in either type, and any
+# head size (80).
+@pytest.mark.parametrize("size", [1e13, 1e14, 1e15, 1e16, 1e17, 1e18])
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float32),
+                                     (128, torch.float32), (80, torch.float32)])
+def test_large_heads_keep_the_gradients_projection(d, dtype, size):
+    """Heads of root mean square `size`, whose squares' sum is just inside fp32:
+    the gradient is of size |dy| / size, both terms of it."""
+    attn, w = layer(6, 2, d, dtype)
+    q, k, pos, dq, dk = case(2, 9, 6, 2, d, dtype, "dense", 7)
+    q, k = (size * x.double() / x.double().square().mean(-1, keepdim=True).sqrt() for x in (q, k))
+    q, k = q.to(dtype), k.to(dtype)
+    # along x, so that the projection takes most of the gradient away
+    dq = (dq.double() + 3 * q.double() / size).to(dtype)
+    res = attn.qk_norm_rope_backward(q, k, pos.cuda(), None, None, dq, dk)
+    y = attn.qk_norm_rope(q, k, pos.cuda())
+    f = lambda t: t.double().cpu()  # noqa: E731
+    for x, gain, dy, out, dx, dg, name in ((q, w["q_norm"], dq, y[0], res[0], res[2], "q"),
+                                           (k, w["k_norm"], dk, y[1], res[1], res[3], "k")):
+        want, z = R.qk_rope(f(x), f(gain), pos, THETA, EPS)
+        close(out, want, z, dtype, 20, name)
+        want, wdg, z, gz = R.qk_rope_backward(f(x), f(gain), pos, THETA, EPS, f(dy))
+        close(dx, want, z, dtype, 40, "d" + name)
+        close(dg, wdg, gz, torch.float32, 128, "gain of " + name)
