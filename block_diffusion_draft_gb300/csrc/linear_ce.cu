@@ -849,7 +849,7 @@ struct CeSums {
   __nv_bfloat16* dx;
   float* miss;          // compact: 1 - p_t
   float* lse2;          // compact: lse in log2 units
-  float* scale;         // compact: d / sum of the exponentials, with the last reference
+  float* scale;         // compact: 1 / sum of the exponentials, with the last reference
 };
 
 // (m, s) and (m2, s2), sums relative to a reference each, as one
@@ -937,11 +937,12 @@ __global__ void __launch_bounds__(kRowThreads)
     }
   }
   if (s.dx == nullptr) return;
-  // the products are relative to the row's last reference
+  // the products are relative to the row's last reference, the exponentials'
+  // sum up to 2^104: their quotient is an ordinary number, to which d comes last
   const float d = __ldcg(a.d + c);
   const float last = __ldcg(a.ref2 + (size_t)a.pieces * a.rows_pad + c);
-  const float f = failed ? nan : d * fast_exp2(last - top) / total;
-  const float g = d * (others / total);
+  const float f = failed ? nan : fast_exp2(last - top) / total;
+  const float g = others / total;
   if (one) {
     s.scale[c] = f;
     // (whole numbers: the sum does not depend on the rows' order)
@@ -962,14 +963,14 @@ __global__ void __launch_bounds__(kRowThreads)
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    o[j] = pack_bf16x2(v[2 * j] * f - g * __uint_as_float(t[j] << 16),
-                       v[2 * j + 1] * f - g * __uint_as_float(t[j] & 0xffff0000u));
+    o[j] = pack_bf16x2(d * (v[2 * j] * f - g * __uint_as_float(t[j] << 16)),
+                       d * (v[2 * j + 1] * f - g * __uint_as_float(t[j] & 0xffff0000u)));
   out[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The kept exponentials of a piece that is the whole vocabulary, with their
-// sums known: 24-bit numbers times the row's scale, rounded to bf16 once, the
-// target's in its place.  A row and 4 * 2048 columns per CTA.
+// sums known: 24-bit numbers times the row's scale and weight, rounded to bf16
+// once, the target's in its place.  A row and 4 * 2048 columns per CTA.
 constexpr int kScaleCols = 8, kScaleSteps = 4;
 
 __global__ void __launch_bounds__(kRowThreads)
@@ -991,7 +992,7 @@ __global__ void __launch_bounds__(kRowThreads)
       lo[k] = __ldcg(lat + col / kScaleCols);
     }
   }
-  const float s = __ldcg(scale + row), own = -__ldcg(a.d + row) * __ldcg(miss + row);
+  const float s = __ldcg(scale + row), d = __ldcg(a.d + row), own = -d * __ldcg(miss + row);
   const int target = __ldcg(a.target + row);
 #pragma unroll
   for (int k = 0; k < kScaleSteps; ++k) {
@@ -1003,7 +1004,7 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int i = 0; i < 8; ++i) {
       const uint32_t up = (i & 1) ? h[i >> 1] & 0xffff0000u : h[i >> 1] << 16;
       const int down = (int)(int8_t)((i < 4 ? lo[k].x : lo[k].y) >> (8 * (i & 3)));
-      v[i] = __uint_as_float(up + (uint32_t)(down * 256)) * s;
+      v[i] = __uint_as_float(up + (uint32_t)(down * 256)) * s * d;
       if (col + i == target) v[i] = own;
     }
     at[col / kScaleCols] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),

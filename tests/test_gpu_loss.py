@@ -123,6 +123,18 @@ def test_targets_far_below_the_largest_logit(N, size):
     check(x, w, t, d)
 
 
+@pytest.mark.parametrize("N,V", [(30, 1500), (300, 1500), (19000, 30000)])
+def test_tiny_weights_of_rows_far_below_their_largest_logit(N, V):
+    """Weights of 2^-77 of rows whose target is up to 2^-79 as likely as the
+    largest one (one more would have the row done again): gradients of 2^-77,
+    both terms of them.  In one piece and in two."""
+    x, w, t, d = inputs(N, V, 256 if N < 1000 else 64, 9)
+    for i, size in enumerate((20.0, 40.0, 45.0, 50.0)):
+        far_rows(x, w, t, range(3 + i, N, 7 if N < 1000 else 700), 700, size)
+    d = torch.sign(d) * 2.0 ** -77
+    check(x, w, t, d, ("x", "xw"))
+
+
 def test_every_row_far_apart():
     x, w, t, d = inputs(200, 1500, 256, 10)
     check((x.float() * 60.0).bfloat16(), w, t, d)
