@@ -252,3 +252,47 @@ def test_large_heads_keep_the_gradients_projection(d, dtype, size):
         want, wdg, z, gz = R.qk_rope_backward(f(x), f(gain), pos, THETA, EPS, f(dy))
         close(dx, want, z, dtype, 40, "d" + name)
         close(dg, wdg, gz, torch.float32, 128, "gain of " + name)
+
+
+# More work than the backward's persistent warps (152 SMs: 1824, 3648 of the
+# kernel for any head size) take at once, of both kinds: rings that are filled
+# again, gains summed over several items, CTAs shared between the kinds.
+MANY = [(2, 4099, 21, 3, 128, torch.bfloat16),  # items of 16 heads, the second one of 5
+        (1, 10007, 4, 2, 64, torch.float32), (3, 1301, 9, 3, 128, torch.float32),
+        (2, 2003, 6, 3, 80, torch.float32), (2, 2003, 9, 3, 64, torch.float32)]
+
+
+@pytest.mark.parametrize("B,rows,nq,nkv,d,dtype", MANY)
+def test_more_items_than_warps(B, rows, nq, nkv, d, dtype):
+    """A gain's gradient: a thread adds up to 14 items of 4 heads (fp32 heads of
+    80: 10 of one), then 2 to 5 exchanges, 4 or 8 warps, 8 slices of CTAs and
+    the 8 + 3 of their sum: below 88 additions, and 40 for the terms: 128."""
+    attn, w = layer(nq, nkv, d, dtype)
+    q, k, pos, dq, dk = case(B, rows, nq, nkv, d, dtype, "slices", rows)
+    copy = torch.clone
+    if (nq, d) == (9, 64):  # rows that are not on 16-byte boundaries
+        def copy(t):
+            wide = torch.zeros(B, rows, t.shape[2] * d + 1, device="cuda")
+            wide[:, :, 1:] = t.flatten(2)
+            return wide[:, :, 1:].unflatten(-1, t.shape[2:])
+        q, k = copy(q), copy(k)
+    p = pos.cuda()
+    y = attn.qk_norm_rope(q, k, p)
+    res = attn.qk_norm_rope_backward(q, k, p, None, None, dq, dk)
+    alone = (attn.qk_norm_rope_backward(q, None, p, None, None, dq, None),
+             attn.qk_norm_rope_backward(None, k, p, None, None, None, dk))
+    assert torch.equal(res[0], alone[0][0]) and torch.equal(res[1], alone[1][1])
+    f = lambda t: t.double().cpu()  # noqa: E731
+    for x, gain, dy, out, dx, dg, name in ((q, w["q_norm"], dq, y[0], res[0], res[2], "q"),
+                                           (k, w["k_norm"], dk, y[1], res[1], res[3], "k")):
+        want, size = R.qk_rope(f(x), f(gain), pos, THETA, EPS)
+        close(out, want, size, dtype, 20, name)
+        want, wdg, size, gsize = R.qk_rope_backward(f(x), f(gain), pos, THETA, EPS, f(dy))
+        close(dx, want, size, dtype, 40, "d" + name)
+        close(dg, wdg, gsize, torch.float32, 128, "gain of " + name)
+    # in place: no piece may be copied ahead after it was overwritten
+    for over in (0, 1):
+        a, b = (copy(q), dq) if over == 0 else (q, copy(dq))
+        got = attn.qk_norm_rope_backward(a, None, p, None, None, b, None,
+                                         dq_out=a if over == 0 else b)
+        assert torch.equal(got[0], alone[0][0]) and torch.equal(got[2], alone[0][2])
