@@ -151,6 +151,32 @@ def test_several_pieces():
     check(x, w, t, d)
 
 
+@pytest.mark.parametrize("N,V,H", [(12011, 45007, 520), (12011, 100003, 520)])
+def test_several_pieces_of_a_wide_head(N, V, H):
+    """Two and three pieces, 9 k-blocks of which the last is an eighth, three
+    tiles of hidden channels; rows that are done again in one piece, in each of
+    the others, and in several of them; the same in every run."""
+    x, w, t, d = inputs(N, V, H, 13, 0.01)
+    for i, column in enumerate((5, V // 3, V // 2 + 300, V - 1)):
+        far_rows(x, w, t, range(100 + i, N, 3001), column, 90.0 + 30.0 * i)
+    far_rows(x, w, t, range(300, 400, 13), 100, 100.0)
+    far_rows(x, w, t, range(300, 400, 13), V // 2 + 700, 210.0)
+    far_rows(x, w, t, range(300, 400, 26), V - 900, 330.0)
+    check(x, w, t, d, ("x", "xw"))
+    a, b = (linear_cross_entropy_grad(x, w, t, d) for _ in range(2))
+    assert all(torch.equal(m, n) for m, n in zip(a, b))
+
+
+def test_several_pieces_of_tiles_of_one_cta():
+    """Up to 128 rows a piece is 2^21 columns."""
+    N, V = 100, 2200003
+    x, w, t, d = inputs(N, V, 72, 14, 0.1)
+    far_rows(x, w, t, range(3, N, 17), 5, 90.0)
+    far_rows(x, w, t, range(4, N, 17), V - 700, 120.0)
+    far_rows(x, w, t, range(3, N, 34), V - 900, 210.0)
+    check(x, w, t, d, ("x", "xw"))
+
+
 def test_a_head_whose_rows_lie_far_apart():
     x, w, t, d = inputs(20, 260, 64, 15)
     space = torch.zeros(260 * ((1 << 23) + 8), device="cuda", dtype=torch.bfloat16)
