@@ -242,6 +242,11 @@ def _like(x: Optional[torch.Tensor], out: Optional[torch.Tensor],
     return out
 
 
+# Tells autograd that a call has written these tensors of the caller's: a backward
+# pass that has saved one of them raises instead of using the new values.
+_overwritten = torch.autograd.graph.increment_version
+
+
 class DFlashAttention:
     """One draft attention layer held by the library.
 
@@ -427,11 +432,14 @@ class DFlashAttention:
         by default dense tensors.  Returns (q_out, k_out)."""
         B, R = _rows_of(q, k)
         _require("positions", positions, torch.int32, self.device, (B, R))
+        written = [t for t in (q_out, k_out) if t is not None]
         q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
         v, at = self._views((B, R), q, k, q_out, k_out)
         _call(self.device, lib().dflash_qk_norm_rope, self.handle, B, R, at[0], at[1],
               self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
               at[2], at[3])
+        if written:
+            _overwritten(written)
         return q_out, k_out
 
     def qk_norm_rope_backward(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -447,6 +455,7 @@ class DFlashAttention:
         _require("positions", positions, torch.int32, self.device, (B, R))
         if (q is None) != (d_q is None) or (k is None) != (d_k is None):
             raise ValueError("d_q and d_k must be given exactly where q and k are")
+        written = [t for t in (dq_out, dk_out) if t is not None]
         dq_out, dk_out = _like(q, dq_out, "dq_out"), _like(k, dk_out, "dk_out")
         v, at = self._views((B, R), q, k, d_q, d_k, dq_out, dk_out)
         if self._rope_ws is None:
@@ -461,6 +470,8 @@ class DFlashAttention:
               self._gain("q_norm", q_norm), self._gain("k_norm", k_norm), positions.data_ptr(),
               at[2], at[3], at[4], at[5], None if q is None else d_gain[0].data_ptr(),
               None if k is None else d_gain[1].data_ptr(), ws.data_ptr(), self._rope_ws)
+        if written:
+            _overwritten(written)
         return dq_out, dk_out, d_gain[0], d_gain[1]
 
     def _views(self, rows: Tuple[int, int], *tensors: Optional[torch.Tensor]):
@@ -468,6 +479,7 @@ class DFlashAttention:
         (address, batch, row and head stride) that has to outlive the call, and
         the addresses of its parts (None for None)."""
         flat, at, dt, d, dev = [], [], self.dtype, self.head_dim, self.device
+        index = dev.index
         shape, other = (*rows, self.n_heads, d), (*rows, self.n_kv_heads, d)
         for t in tensors:
             if t is None:
@@ -475,7 +487,9 @@ class DFlashAttention:
                 at.append(None)
             else:
                 s = t.stride()
-                if t.shape != shape or t.dtype is not dt or not _on(t, dev):
+                on = t.get_device()  # (as _on, without its calls)
+                if t.shape != shape or t.dtype is not dt or on < 0 or (
+                        on != index and index is not None):
                     raise ValueError(f"queries must be {[*rows, self.n_heads, d]} and keys "
                                      f"{[*rows, self.n_kv_heads, d]}, {dt} on {dev}, got "
                                      f"{list(t.shape)}, {t.dtype} on {t.device}")
@@ -844,11 +858,12 @@ def _grad_norm(grads, max_norm, out) -> torch.Tensor:
     if not grads:
         raise ValueError("no gradients")
     dev, n = grads[0].device, len(grads)
+    index = dev.index
     if dev.type != "cuda":
         raise ValueError("the library runs on CUDA devices only")
     # (whole lists at a time: a training step has hundreds of tensors)
     types = [_GRAD_TYPES.get(g.dtype) for g in grads]
-    if None in types or any([g.get_device() != dev.index for g in grads]):
+    if None in types or any([g.get_device() != index for g in grads]):
         raise ValueError(f"gradients must be float32 or bfloat16 on {dev}")
     dense = [g.is_contiguous() for g in grads]
     if not all(dense) and not all([c or _dense(g) for c, g in zip(dense, grads)]):
@@ -860,7 +875,7 @@ def _grad_norm(grads, max_norm, out) -> torch.Tensor:
         if len(out) != n:
             raise ValueError(f"out must hold {n} tensors, got {len(out)}")
         for g, o, c in zip(grads, out, dense):
-            if o.dtype is not g.dtype or o.get_device() != dev.index or o.shape != g.shape or not (
+            if o.dtype is not g.dtype or o.get_device() != index or o.shape != g.shape or not (
                     c and o.is_contiguous() or o.stride() == g.stride() or g.numel() <= 1):
                 raise ValueError("out must have the gradients' shapes, strides, types and device")
         outs = array("Q", [o.data_ptr() for o in out])
@@ -875,6 +890,7 @@ def _grad_norm(grads, max_norm, out) -> torch.Tensor:
     else:
         _call(dev, lib().dflash_clip_grad_norm, n, *lists, max_norm, norm.data_ptr(),
               ws.data_ptr(), size)
+        _overwritten(grads if out is None else out)
     return norm
 
 
