@@ -1683,6 +1683,8 @@ int run_qk_norm_rope(dflash_attn* a, int batch, int rows, const dflash_heads* co
     return fail(DFLASH_ERR_SHAPE, "too many rows");
   const bool none = batch == 0 || rows == 0;
   if (!none && positions == nullptr) return fail(DFLASH_ERR_ARG, "positions is null");
+  if ((reinterpret_cast<uintptr_t>(positions) & 3) != 0)
+    return fail(DFLASH_ERR_ARG, "positions not aligned to its type");
   static const char* const names[2][3] = {{"q", "d_q", "q_out"}, {"k", "d_k", "k_out"}};
   QkRopeArgs q{};
   q.batch = batch;
@@ -1699,7 +1701,8 @@ int run_qk_norm_rope(dflash_attn* a, int batch, int rows, const dflash_heads* co
     if (x[k] == nullptr) continue;
     q.heads[k] = k == 0 ? a->nq : a->nkv;
     q.gain[k] = gain[k];
-    if (bwd && d_gain[k] == nullptr) return fail(DFLASH_ERR_ARG, "a gain's gradient is null");
+    if (bwd && (d_gain[k] == nullptr || (reinterpret_cast<uintptr_t>(d_gain[k]) & 3) != 0))
+      return fail(DFLASH_ERR_ARG, "a gain's gradient is null or not aligned to its type");
     if (a->dt == DFLASH_BF16 ? !aligned16(gain[k])
                              : (reinterpret_cast<uintptr_t>(gain[k]) & 3) != 0)
       return fail(DFLASH_ERR_ARG, "gains not aligned");

@@ -634,7 +634,7 @@ typedef struct {
  *                 them otherwise), or any layout whose heads do not overlap,
  *                 such as rows of the packed core's keys
  * Strides of inputs may be 0.  bf16: 16-byte boundaries, strides multiples of
- * 8 elements.  batch or rows may be 0.  The layer's device has to be current.
+ * 8 elements; 32-bit tensors: 4-byte boundaries.  batch or rows may be 0.  The layer's device has to be current.
  * Errors: _ARG, _SHAPE, _CUDA. */
 int dflash_qk_norm_rope(dflash_attn* attn, int batch, int rows, const dflash_heads* q,
                         const dflash_heads* k, const void* q_norm_w, const void* k_norm_w,

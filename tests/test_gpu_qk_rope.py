@@ -296,3 +296,36 @@ def test_more_items_than_warps(B, rows, nq, nkv, d, dtype):
         got = attn.qk_norm_rope_backward(a, None, p, None, None, b, None,
                                          dq_out=a if over == 0 else b)
         assert torch.equal(got[0], alone[0][0]) and torch.equal(got[2], alone[0][2])
+
+
+def test_addresses_that_are_not_aligned_are_refused():
+    """On the host, before anything is launched: odd addresses of the 32-bit
+    tensors, and of bf16 heads and gains off their 16-byte boundaries."""
+    from ctypes import c_int64, c_void_p, cast
+    from block_diffusion_draft_gb300 import lib
+    attn, _ = layer(4, 2, 128, torch.bfloat16)
+    q = torch.randn(1, 3, 4, 128, device="cuda").bfloat16()
+    out, pos = torch.zeros_like(q), torch.arange(3, device="cuda", dtype=torch.int32)
+    dg, ws = torch.zeros(132, device="cuda"), torch.zeros(1 << 20, device="cuda")
+    gain = torch.ones(136, device="cuda", dtype=torch.bfloat16)
+
+    def call(pos_off=0, dg_off=0, x_off=0, out_off=0, gain_off=0, back=True):
+        head = lambda t, o: cast((c_int64 * 4)(t.data_ptr() + o, 0, 512, 128),  # noqa: E731
+                                 c_void_p)
+        x, y, p = head(q, x_off), head(out, out_off), pos.data_ptr() + pos_off
+        g = gain.data_ptr() + gain_off
+        stream = torch.cuda.current_stream().cuda_stream
+        if not back:
+            return lib().dflash_qk_norm_rope(attn.handle, 1, 3, x, None, g, None, p, y, None, stream)
+        return lib().dflash_qk_norm_rope_backward(
+            attn.handle, 1, 3, x, None, g, None, p, x, None, y, None, dg.data_ptr() + dg_off, None,
+            ws.data_ptr(), 4 * ws.numel(), stream)
+
+    for back in (False, True):
+        for kw in (dict(pos_off=1), dict(pos_off=2), dict(x_off=8), dict(out_off=2),
+                   dict(gain_off=4)) + ((dict(dg_off=2),) if back else ()):
+            assert call(back=back, **kw) == -1 and b"align" in lib().dflash_last_error(), kw
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (dg == 0).all()
+    assert call(back=False) == 0 and call() == 0
+    assert torch.isfinite(dg[:128]).all() and (dg[128:] == 0).all()
