@@ -8,7 +8,8 @@
 // so that all of them are near one another in memory (a run of its own for each
 // CTA was 5% slower); the second pass goes backwards and so begins with what the
 // first one left in L2.  One decoder layer's gradients in bf16 (386 MB): the
-// norm 59 us (6.5 TB/s), clipped into other buffers 192 us.
+// norm 59 us (6.5 TB/s), clipped into other buffers 187 us (of another alignment:
+// 460 to 525, in stores of 2 bytes).
 //
 // A thread adds the squares of up to 64 values in fp32 (relative error below
 // 64 * 2^-24) and everything above that in fp64, in an order that depends on

@@ -210,9 +210,10 @@ DF_DEV void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Stages, groups of heads of an item, CTAs per SM: 8192 rows of 32 + 8 heads
-// took 51.0 us with (2, 4, 3), 51.9 with (2, 2, 4), 52.3 with (3, 2, 3), 56 with
-// (3, 1, 5), 80 and more where the CTAs' registers or rings leave too few warps.
+// Stages, groups of heads of an item, CTAs per SM: 8192 rows of 32 + 8 heads,
+// bf16, cold and with the gains' kernel, took 51.0 us with (2, 4, 3), 51.9 with (2,
+// 2, 4), 52.3 with (3, 2, 3), 56 with (3, 1, 5), 80 and more where the CTAs' registers
+// or rings leave too few warps; 46 us with (2, 4, 3) among other calls.
 constexpr int kStages = 2, kSteps = 4, kCtasPerSm = 3;
 constexpr int kBackWarps = 4, kBackThreads = kBackWarps * 32;
 
@@ -380,7 +381,8 @@ __global__ void __launch_bounds__(kBackThreads, kCtasPerSm)
 }
 
 // Any even head size up to 256 and any alignment, fp32: a warp takes a head,
-// a lane the pairs lane, lane + 32, ...
+// a lane the pairs lane, lane + 32, ...  With one head in flight per warp it is far
+// from its bytes: 8192 rows of 32 + 8 heads of 80, 121 us, backward 143 (floors 31, 46).
 constexpr int kPairs = 4;
 
 template <bool BWD>

@@ -429,7 +429,8 @@ class DFlashAttention:
         [B, R] (int32).  Channels are dense, other strides free; q or k may be
         None.  Results go to q_out and k_out (the inputs themselves, or any
         tensor of that shape, such as rows of packed_core's keys, transposed),
-        by default dense tensors.  Returns (q_out, k_out)."""
+        by default dense tensors.  Returns (q_out, k_out), which carry no
+        gradients: those are qk_norm_rope_backward's."""
         B, R = _rows_of(q, k)
         _require("positions", positions, torch.int32, self.device, (B, R))
         written = [t for t in (q_out, k_out) if t is not None]
@@ -776,7 +777,9 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     H a multiple of 8), targets [N] int32, one outside [0, V) for a row that does
     not count.  Returns (nll, lse) [N] fp32: logsumexp(x w^T) - (x w^T)[target]
     and logsumexp(x w^T), 0 for rows that do not count.  The logits are never
-    held.  See dflash_linear_ce in include/dflash_attn.h."""
+    held.  Neither result carries gradients, whatever x and w require: in a sum
+    of losses this one's part comes from linear_cross_entropy_grad.  See
+    dflash_linear_ce in include/dflash_attn.h."""
     nll, lse, _, _ = _linear_ce(x, w, targets, None, 0)
     return nll, lse
 
@@ -785,7 +788,9 @@ def linear_cross_entropy_grad(x: torch.Tensor, w: torch.Tensor, targets: torch.T
                               d_nll: torch.Tensor, need_dw: bool = True):
     """linear_cross_entropy and the gradients of sum(d_nll * nll) (d_nll [N]
     fp32, the rows' weights in the loss) in one call.  Returns (nll, lse, dx [N,
-    H] bf16, dw [V, H] bf16 or None: a head that is not trained needs none)."""
+    H] bf16, dw [V, H] bf16 or None: a head that is not trained needs none), which
+    the caller passes on (``x.backward(dx)``, ``w.grad = dw``): autograd knows
+    nothing of them."""
     return _linear_ce(x, w, targets, d_nll, 2 if need_dw else 1)
 
 
@@ -837,9 +842,10 @@ def grad_norm(grads: Sequence[torch.Tensor]) -> torch.Tensor:
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
                    out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
     """Scale the tensors by max_norm / norm where their norm (as grad_norm) is
-    above max_norm, in place or into ``out`` (as grads).  Gradients whose norm
-    is not finite stay as they are.  Returns the norm before clipping, on the
-    device.  See dflash_clip_grad_norm in include/dflash_attn.h."""
+    above max_norm, in place or into ``out`` (as grads).  Gradients with an
+    infinity or NaN among them stay as they are.  Returns the norm before
+    clipping, on the device.  See dflash_clip_grad_norm in
+    include/dflash_attn.h."""
     return _grad_norm(grads, float(max_norm), out)
 
 

@@ -632,9 +632,10 @@ typedef struct {
  *                 clamped and recorded (DFLASH_DEV_POSITION)
  *   q_out, k_out  device, as q and k; may be q and k themselves (not overlap
  *                 them otherwise), or any layout whose heads do not overlap,
- *                 such as rows of the packed core's keys
+ *                 such as rows of the packed core's keys; not one another
  * Strides of inputs may be 0.  bf16: 16-byte boundaries, strides multiples of
- * 8 elements; 32-bit tensors: 4-byte boundaries.  batch or rows may be 0.  The layer's device has to be current.
+ * 8 elements; 32-bit tensors: 4-byte boundaries.  A head's sum of squares has to
+ * lie in fp32's range.  batch or rows may be 0.  The layer's device has to be current.
  * Errors: _ARG, _SHAPE, _CUDA. */
 int dflash_qk_norm_rope(dflash_attn* attn, int batch, int rows, const dflash_heads* q,
                         const dflash_heads* k, const void* q_norm_w, const void* k_norm_w,
@@ -651,7 +652,8 @@ int dflash_qk_norm_rope_workspace(const dflash_attn* attn, size_t* bytes);
  *   d_q_norm,       device fp32 [head_dim]: the gains' gradients, written (not
  *   d_k_norm        added to); NULL iff q (k) is
  *   workspace       device, 16-byte aligned, the caller's until the work is done
- * Every sum is taken in an order that depends on the sizes alone.
+ * Every sum is taken in an order that depends on the sizes and the tensors'
+ * alignment alone.
  * Errors: _ARG, _SHAPE, _CAPACITY (workspace), _CUDA. */
 int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const dflash_heads* q,
                                  const dflash_heads* k, const void* q_norm_w,
@@ -687,10 +689,13 @@ int dflash_qk_norm_rope_backward(dflash_attn* attn, int batch, int rows, const d
  * nothing else of other rows.
  *   workspace  device, 256-byte aligned, the caller's until the work is done;
  *              dflash_linear_ce_workspace gives its size for grads = 0 (nll and
- *              lse), 1 (dx) or 2 (dx and dw): for a piece's exponentials at
- *              most about 1 GiB (or 4096 columns' worth, if that is more; half as
- *              much again with dw and all columns in one piece), and small
- *              multiples of rows * hidden and rows * vocab / 128.
+ *              lse), 1 (dx) or 2 (dx and dw).  With R the rows rounded up to
+ *              256 and H hidden rounded up to 64 it is, in bytes, 2 R H and R *
+ *              vocab / 32 (twice that for grads = 0); with gradients also up to
+ *              64 R H of fp32 sums (few rows: 64, many: 4) and a piece's
+ *              exponentials, at most about 1 GiB (or 4096 columns' worth, if
+ *              that is more; half as much again with dw and all columns in one
+ *              piece); with dw 8 vocab; a few words a row and piece.
  * After a bounded wait that ran out nll and lse are NaN.  Work goes to the
  * current device.
  * Errors: _ARG, _SHAPE, _CAPACITY (workspace), _CUDA. */
@@ -707,8 +712,9 @@ int dflash_linear_ce_grad(int rows, int vocab, int hidden, const void* x, int64_
  * counterpart on the pages).
  *   norm = sqrt(sum over all tensors of g^2)
  *   clipping: where norm > max_norm, out = g * (max_norm / norm); otherwise,
- *   and where the norm is not finite (an infinity or NaN among the gradients,
- *   which the caller finds in `norm`), out = g.
+ *   and where an infinity or NaN is among the gradients (the caller finds it in
+ *   `norm`), out = g.  A norm of finite gradients above fp32's range, which
+ *   `norm` gives as infinite, clips like any other.
  *   n_tensors   at most 2^20; may be 0 (norm 0)
  *   grads, out  host arrays of device pointers, aligned to their types; out
  *               NULL: in place.  What is written must not overlap anything
